@@ -24,6 +24,8 @@ LIB_PATH = os.path.join(_PKG, "libhils.so")
 HILS_F32, HILS_BF16 = 0, 1
 HILS_CALL_SELECT, HILS_CALL_ATTEND_PREFILL, HILS_CALL_ATTEND_DECODE, HILS_CALL_DECODE = 0, 1, 2, 3
 HILS_CALL_ATTEND_BACKWARD = 4
+HILS_CALL_SINK_PREFILL, HILS_CALL_SINK_BACKWARD, HILS_CALL_SINK_WEIGHTS = 5, 6, 7
+HILS_CALL_SINK_DECODE, HILS_CALL_SINK_DECODE_ACC, HILS_CALL_PREFIX_DECODE, HILS_CALL_CACHE_EVICT = 8, 9, 10, 11
 # hils_params.flags: chunks wholly inside a query's window are not selected
 HILS_FLAG_EXCLUDE_WINDOW_CHUNKS = 1
 # hils_params.flags, diagnostic: the tensor-core kernels' waits on work in progress expire at once
@@ -36,7 +38,9 @@ _DTYPES = {torch.float32: HILS_F32, torch.bfloat16: HILS_BF16}
 EXPORTS = ("hils_summarize", "hils_select", "hils_attend_prefill", "hils_attend_decode", "hils_decode",
            "hils_attend_decode_noalloc", "hils_workspace_bytes", "hils_workspace_init",
            "hils_status_string", "hils_last_cuda_error", "hils_summarize_append", "hils_attend_prefill_backward",
-           "hils_select_backward", "hils_summarize_backward", "hils_selftest_fast_math")
+           "hils_select_backward", "hils_summarize_backward", "hils_selftest_fast_math", "hils_sink_prefill",
+           "hils_sink_prefill_backward", "hils_sink_weights", "hils_sink_decode", "hils_prefix_decode",
+           "hils_cache_evict")
 
 
 class HilsError(RuntimeError):
@@ -80,6 +84,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.hils_attend_decode.argtypes = [P, T, T, T, vp, vp, vp, vp, T, vp, vp, sz, vp]
         lib.hils_attend_decode_noalloc.argtypes = [P, T, T, T, vp, vp, vp, vp, T, vp, vp]
         lib.hils_decode.argtypes = [P, T, T, vp, i, T, T, T, vp, vp, vp, vp, T, vp, vp, sz, vp]
+        lib.hils_sink_prefill.argtypes = [P, i, T, i, T, T, i, T, vp, vp, sz, vp]
+        lib.hils_sink_prefill_backward.argtypes = [P, i, T, T, T, i, T, vp, T, T, T, T, vp, sz, vp]
+        lib.hils_sink_weights.argtypes = [P, i, T, i, T, i, vp, vp, vp, i, vp, sz, vp]
+        lib.hils_sink_decode.argtypes = [P, i, T, T, T, i, vp, T, vp, vp, vp, vp, sz, vp]
+        lib.hils_prefix_decode.argtypes = [P, T, T, T, i, T, T, i, vp, T, vp, vp, sz, vp]
+        lib.hils_cache_evict.argtypes = [P, i, i, T, T, i, vp, vp, T, T, vp, vp, vp, vp, sz, vp]
         lib.hils_workspace_bytes.argtypes = [P, i, i, i]
         lib.hils_workspace_bytes.restype = sz
         lib.hils_workspace_init.argtypes = [vp, sz, vp]
@@ -90,7 +100,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         for name in ("hils_summarize", "hils_summarize_append", "hils_attend_prefill_backward",
                      "hils_select_backward", "hils_summarize_backward", "hils_select", "hils_attend_prefill",
                      "hils_attend_decode", "hils_decode", "hils_attend_decode_noalloc", "hils_workspace_init",
-                     "hils_selftest_fast_math"):
+                     "hils_selftest_fast_math", "hils_sink_prefill", "hils_sink_prefill_backward", "hils_sink_weights",
+                     "hils_sink_decode", "hils_prefix_decode", "hils_cache_evict"):
             getattr(lib, name).restype = i
         _lib = lib
     return _lib
@@ -391,6 +402,139 @@ def hils_summarize_backward(p: Params, K, LQ, dKsum, dBsum, dK, dLQ, N: int | No
     _check("hils_summarize_backward", load_library().hils_summarize_backward(
         ctypes.byref(p.c()), _view(K), n, _view(LQ), _ptr(dKsum), _ptr(dBsum), _ptr(dK), _ptr(dLQ),
         _stream(stream)))
+
+
+def _sink_call(call: str, p: Params, views, arrays, workspace, stream, make_args) -> None:
+    """Checks and makes one of the calls below: `views` (name, tensor, shape) are strided in
+    params.dtype, `arrays` (name, tensor, shape, dtype) dense; None is left to the C call.
+    Every tensor has to be on one device, whose current stream is used if `stream` is None."""
+    dev = None
+    for name, t, shape, dt in [(n, t, sh, p.dtype) for n, t, sh in views] + arrays:
+        if t is None:
+            continue
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{call}: {name} has shape {tuple(t.shape)}, expected {shape}")
+        if t.dtype != dt:
+            raise ValueError(f"{call}: {name} has dtype {t.dtype}, expected {dt}")
+        if not t.is_cuda:
+            raise ValueError(f"{call}: {name} must be a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{call}: {name} is on {t.device}, other tensors on {dev}")
+    for name, t, _, _ in arrays:
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{call}: {name} must be dense (contiguous)")
+    if workspace is not None and dev is not None and workspace.device != dev:
+        raise ValueError(f"{call}: workspace is on {workspace.device}, other tensors on {dev}")
+    wp, wn = _ws(workspace)
+    fn = getattr(load_library(), call)
+    args = make_args()
+    if dev is not None and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            _check(call, fn(ctypes.byref(p.c()), *args, wp, wn, _stream(stream)))
+    else:
+        _check(call, fn(ctypes.byref(p.c()), *args, wp, wn, _stream(stream)))
+
+
+def _bhtd(call: str, name: str, t) -> int:
+    """The T of a [B, H, T, d] tensor."""
+    if t is None or len(t.shape) != 4:
+        raise ValueError(f"{call}: {name} must be a [B, H, T, d] tensor")
+    return t.shape[2]
+
+
+def hils_sink_prefill(p: Params, A: int, Q, K, V, O, lse=None, workspace=None, stream=None) -> None:
+    """Attention with a sliding window (p.W) and the first A tokens as sinks for the newest
+    queries of a sequence: Q, O [B,H,Lq,d] at positions N - Lq .. N - 1 of K, V [B,Hk,N,d];
+    lse [B,H,Lq] float32 (optional). p.W >= N is full causal attention.
+    workspace: alloc_workspace(p, HILS_CALL_SINK_PREFILL, Lq, A)."""
+    call = "hils_sink_prefill"
+    lq, n = _bhtd(call, "Q", Q), _bhtd(call, "K", K)
+    q, kv = (p.B, p.H, lq, p.d), (p.B, p.Hk, n, p.d)
+    _sink_call(call, p, [("Q", Q, q), ("K", K, kv), ("V", V, kv), ("O", O, q)], [("lse", lse, q[:3], torch.float32)],
+               workspace, stream,
+               lambda: (A, _view(Q), lq, _view(K), _view(V), n, _view(O), _ptr(lse)))
+
+
+def hils_sink_prefill_backward(p: Params, A: int, Q, K, V, O, lse, dO, dQ, dK, dV, workspace=None, stream=None) -> None:
+    """Gradients of hils_sink_prefill over a whole prompt (Lq = N) from its O and lse and
+    from dO: dQ [B,H,N,d], dK, dV [B,Hk,N,d], all in p.dtype and all written.
+    workspace: alloc_workspace(p, HILS_CALL_SINK_BACKWARD, N, A)."""
+    call = "hils_sink_prefill_backward"
+    n = _bhtd(call, "Q", Q)
+    q, kv = (p.B, p.H, n, p.d), (p.B, p.Hk, n, p.d)
+    _sink_call(call, p, [("Q", Q, q), ("K", K, kv), ("V", V, kv), ("O", O, q), ("dO", dO, q), ("dQ", dQ, q),
+                         ("dK", dK, kv), ("dV", dV, kv)], [("lse", lse, q[:3], torch.float32)], workspace, stream,
+               lambda: (A, _view(Q), _view(K), _view(V), n, _view(O), _ptr(lse), _view(dO), _view(dQ), _view(dK),
+                        _view(dV)))
+
+
+def hils_sink_weights(p: Params, A: int, Q, K, lse, acc, acc_out=None, workspace=None, stream=None) -> None:
+    """Adds the attention weight that each token of K [B,Hk,N,d] drew from the newest queries
+    Q [B,H,Lq,d] (lse [B,H,Lq] of their forward, summed over each group's heads) to acc
+    [B,Hk,T], T >= N, into acc_out (acc itself if None).
+    workspace: alloc_workspace(p, HILS_CALL_SINK_WEIGHTS, N, A)."""
+    call = "hils_sink_weights"
+    lq, n = _bhtd(call, "Q", Q), _bhtd(call, "K", K)
+    out = acc if acc_out is None else acc_out
+    t = acc.shape[-1] if acc is not None else 0
+    w = (p.B, p.Hk, t)
+    _sink_call(call, p, [("Q", Q, (p.B, p.H, lq, p.d)), ("K", K, (p.B, p.Hk, n, p.d))],
+               [("lse", lse, (p.B, p.H, lq), torch.float32), ("acc", acc, w, torch.float32),
+                ("acc_out", out, w, torch.float32)], workspace, stream,
+               lambda: (A, _view(Q), lq, _view(K), n, _ptr(lse), _ptr(acc), _ptr(out), t))
+
+
+def hils_sink_decode(p: Params, A: int, Q, Kc, Vc, cache_len, O, lse=None, acc=None, acc_out=None, workspace=None,
+                     stream=None) -> None:
+    """One new token per sequence over the sinks and the window of its cache Kc, Vc
+    [B,Hk,T,d] (p.W >= T: the whole cache): O [B,H,1,d], lse [B,H] float32 (optional). With
+    acc [B,Hk,T] float32, each visible slot's weight is added to it, into acc_out (acc
+    itself if None). workspace: alloc_workspace(p, HILS_CALL_SINK_DECODE, T, A), with acc
+    HILS_CALL_SINK_DECODE_ACC."""
+    call = "hils_sink_decode"
+    t = _bhtd(call, "Kc", Kc)
+    out = acc if acc_out is None else acc_out
+    q, kv, w = (p.B, p.H, 1, p.d), (p.B, p.Hk, t, p.d), (p.B, p.Hk, t)
+    _sink_call(call, p, [("Q", Q, q), ("Kc", Kc, kv), ("Vc", Vc, kv), ("O", O, q)],
+               [("cache_len", cache_len, (p.B,), torch.int32), ("lse", lse, (p.B, p.H), torch.float32),
+                ("acc", acc, w, torch.float32), ("acc_out", out, w, torch.float32)], workspace, stream,
+               lambda: (A, _view(Q), _view(Kc), _view(Vc), t, _ptr(cache_len), _view(O), _ptr(lse), _ptr(acc),
+                        _ptr(out)))
+
+
+def hils_prefix_decode(p: Params, Q, Kp, Vp, Kc, Vc, cache_len, O, lse=None, workspace=None, stream=None) -> None:
+    """One new token for each sequence of a batch that shares the prefix Kp, Vp [1,Hk,P,d] and
+    goes on in its own cache Kc, Vc [B,Hk,T,d] (cache_len [B] int32 slots of it, 0 allowed):
+    O [B,H,1,d], lse [B,H] float32 (optional). p.W is not used.
+    workspace: alloc_workspace(p, HILS_CALL_PREFIX_DECODE, T, P)."""
+    call = "hils_prefix_decode"
+    t, n = _bhtd(call, "Kc", Kc), _bhtd(call, "Kp", Kp)
+    q, kv, pre = (p.B, p.H, 1, p.d), (p.B, p.Hk, t, p.d), (1, p.Hk, n, p.d)
+    _sink_call(call, p, [("Q", Q, q), ("Kp", Kp, pre), ("Vp", Vp, pre), ("Kc", Kc, kv), ("Vc", Vc, kv), ("O", O, q)],
+               [("cache_len", cache_len, (p.B,), torch.int32), ("lse", lse, (p.B, p.H), torch.float32)], workspace,
+               stream,
+               lambda: (_view(Q), _view(Kp), _view(Vp), n, _view(Kc), _view(Vc), t, _ptr(cache_len), _view(O),
+                        _ptr(lse)))
+
+
+def hils_cache_evict(p: Params, A: int, budget: int, K, V, acc, cache_len, Kout, Vout, acc_out, idx, len_out,
+                     workspace=None, stream=None) -> None:
+    """Cuts the caches K, V [B,Hk,T,d] to budget slots by acc [B,Hk,T]: the first A, the p.W
+    newest and the heaviest between stay, in slot order, in Kout, Vout [B,Hk,budget,d] and
+    acc_out [B,Hk,budget]; idx [B,Hk,budget] int32 gets their old slots (-1 behind the
+    last), len_out [B] int32 the new lengths (may be cache_len).
+    workspace: alloc_workspace(p, HILS_CALL_CACHE_EVICT, T, budget)."""
+    call = "hils_cache_evict"
+    t = _bhtd(call, "K", K)
+    kv, out = (p.B, p.Hk, t, p.d), (p.B, p.Hk, budget, p.d)
+    _sink_call(call, p, [("K", K, kv), ("V", V, kv), ("Kout", Kout, out), ("Vout", Vout, out)],
+               [("acc", acc, kv[:3], torch.float32), ("cache_len", cache_len, (p.B,), torch.int32),
+                ("acc_out", acc_out, out[:3], torch.float32), ("idx", idx, out[:3], torch.int32),
+                ("len_out", len_out, (p.B,), torch.int32)], workspace, stream,
+               lambda: (A, budget, _view(K), _view(V), t, _ptr(acc), _ptr(cache_len), _view(Kout), _view(Vout),
+                        _ptr(acc_out), _ptr(idx), _ptr(len_out)))
 
 
 def alloc_workspace(p: Params, call: int, Lq: int, C: int, device="cuda") -> torch.Tensor | None:

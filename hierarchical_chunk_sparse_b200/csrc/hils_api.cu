@@ -1,10 +1,11 @@
 // C-ABI entry points of libhils: argument validation, workspace sizing and dispatch
 // to one kernel launcher per stage. No call allocates, frees or synchronises.
-#include <math.h>
 #include <stdio.h>
 #include <string.h>
 
+#include "api_checks.cuh"
 #include "backward_common.cuh"
+#include "sink_common.cuh"
 #include "hils_internal.cuh"
 
 namespace hils {
@@ -51,54 +52,6 @@ hils_status kernel_setup(KernelSetup &cache, const void *func, int threads, int 
 
 namespace {
 
-size_t elem_size(hils_dtype dt) { return dt == HILS_BF16 ? 2 : 4; }
-
-// Common parameter checks; fills the effective scale.
-int check_params(const hils_params *p, float *scale) {
-    if (!p) return HILS_ERR_INVALID_ARG;
-    if (p->B < 0 || p->H < 0 || p->K < 0 || p->W < 0) return HILS_ERR_INVALID_ARG;
-    if (p->dtype != HILS_F32 && p->dtype != HILS_BF16) return HILS_ERR_UNSUPPORTED;
-    if (p->d != 64 && p->d != 128) return HILS_ERR_UNSUPPORTED;
-    if (p->S != kChunk) return HILS_ERR_UNSUPPORTED;
-    if (p->K > 32) return HILS_ERR_UNSUPPORTED;
-    if (p->flags & ~(uint32_t)(HILS_FLAG_EXCLUDE_WINDOW_CHUNKS | HILS_FLAG_DIAG_EXPIRE_WAITS))
-        return HILS_ERR_UNSUPPORTED;
-    if (!isfinite(p->scale)) return HILS_ERR_INVALID_ARG;
-    if (p->H_kv < 0 || (p->H_kv > 0 && p->H % p->H_kv != 0)) return HILS_ERR_INVALID_ARG;
-    if (p->H_kv > 0 && p->H / p->H_kv > kMaxGroupHeads) return HILS_ERR_UNSUPPORTED;
-    *scale = p->scale != 0.f ? p->scale : (float)(1.0 / sqrt((double)p->d));
-    return HILS_OK;
-}
-
-// Query heads per key-value head (parameters already checked).
-int groups(const hils_params *p) { return p->H_kv > 0 ? p->H / p->H_kv : 1; }
-
-bool aligned16(const void *ptr) { return ((uintptr_t)ptr & 15u) == 0; }
-
-// A [B, H, T, d] view with T rows used: non-null when it holds elements, 16-byte
-// aligned base and strides.
-int check_view(const void *ptr, int64_t sb, int64_t sh, int64_t st, int64_t rows, const hils_params *p) {
-    if ((int64_t)p->B * p->H * rows == 0) return HILS_OK;
-    if (!ptr) return HILS_ERR_INVALID_ARG;
-    const int64_t es = (int64_t)elem_size(p->dtype);
-    if (!aligned16(ptr)) return HILS_ERR_ALIGNMENT;
-    if ((sb * es) % 16 || (sh * es) % 16 || (st * es) % 16) return HILS_ERR_ALIGNMENT;
-    return HILS_OK;
-}
-
-int check_array(const void *ptr, int64_t count) {
-    if (count > 0 && !ptr) return HILS_ERR_INVALID_ARG;
-    if (ptr && ((uintptr_t)ptr & 3u)) return HILS_ERR_ALIGNMENT;
-    return HILS_OK;
-}
-
-int check_workspace(const void *ws, size_t have, size_t need) {
-    if (need == 0) return HILS_OK;
-    if (!ws || have < need) return HILS_ERR_WORKSPACE;
-    if (!aligned16(ws)) return HILS_ERR_ALIGNMENT;
-    return HILS_OK;
-}
-
 // Units per query of the attend kernels: one per kept chunk plus the window tiles
 // (at least one, so that an empty query still gets o = 0 and lse = -inf).
 int decode_units(const hils_params *p) {
@@ -112,13 +65,6 @@ size_t select_ws_for(const hils_params *p, int Lq, int C) {
     select_plan(p->dtype, p->d, p->B, p->H, Lq, C, p->K, true, device_sm_count(), &a);
     return select_ws_bytes(p->B * p->H * Lq, C, a.path);
 }
-
-#define HILS_TRY(expr)                 \
-    do {                               \
-        const int _rc = (expr);        \
-        if (_rc != HILS_OK) return _rc; \
-    } while (0)
-
 
 int prepare_select(const hils_params *p, hils_ctensor Qcal, int Lq, const int32_t *qpos, int qpos_bias,
                    hils_ctensor Ksum, const float *Bsum, int C, int32_t *idx, float *score, int32_t *nsel,
@@ -239,7 +185,7 @@ size_t hils_workspace_bytes(const hils_params *p, int call, int Lq, int C) {
     case HILS_CALL_ATTEND_BACKWARD: return attend_backward_ws_bytes(p->dtype, p->d, p->B, p->H, p->H / groups(p), Lq, p->K);
     case HILS_CALL_DECODE:
         return decode_select_part(select_ws_for(p, 1, C)) + attend_decode_ws_bytes(p->B * p->H, decode_units(p), p->d);
-    default: return 0;
+    default: return sink_ws_bytes(p, call, Lq, C);
     }
 }
 

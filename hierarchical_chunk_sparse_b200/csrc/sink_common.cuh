@@ -1,0 +1,220 @@
+// Arguments, work division and launchers of the window-and-sink attention (prefill, its
+// backward, one-token decode, accumulated weights), the shared-prefix decode and the
+// cache eviction.
+//
+// A query at position t sees V(t) = { j <= t : j < A or j > t - W }: the first A tokens
+// (the sinks) and the W newest up to its own. With s_tj = scale q_t . k_j,
+//   lse_t = log sum_{j in V(t)} exp(s_tj),  p_tj = exp(s_tj - lse_t),  o_t = sum_j p_tj v_j
+// (an empty V(t): o = 0, lse = -inf). Backward, from O and lse:
+//   D_t = dO_t . o_t,  ds_tj = scale p_tj (dO_t . v_j - D_t),
+//   dQ = ds K,  dK = ds^T Q,  dV = p^T dO,  the last two summed over a group's heads.
+#pragma once
+#include "hils_internal.cuh"
+
+namespace hils {
+
+// ------------------------------------------------------------------ forward
+
+// One call's rows over one key range. Prefill: row (b, h, i) at position N - Lq + i. A
+// shared prefix (`prefix`): the rows of every sequence, (b, h), over all N keys of key
+// batch 0 (W = N, A = 0, Lq = 1).
+struct SinkArgs {
+    View Q, K, V;
+    MutView O;
+    float *lse;              // [B, H, Lq] or null
+    int B, H, G, Lq, N, W, A;  // W, A <= N
+    float scale;
+    int prefix = 0;
+    // split > 1 (or prefix): each row's partial results of key split s go to slot s of
+    // `slots`: part_o [rows][slots][d] (normalised), part_lse [rows][slots] (natural log)
+    int splits = 1, slots = 0;
+    float *part_o = nullptr, *part_lse = nullptr;
+    uint32_t *status = nullptr;
+    long long wait_ns = kWaitLimitNs;
+};
+
+// The key tiles of one row tile: sinks [0, sinks) in ns tiles, then keys [lo, hi) in nw.
+struct SinkSpan {
+    int sinks, ns, lo, hi, nw;
+};
+
+// Rows at positions t0 .. t1, key tiles of `kt` keys. The window's tiles begin at its
+// first visible key exactly, so that a slot that no row sees is never part of a tile.
+__host__ __device__ inline SinkSpan sink_span(int t0, int t1, int W, int A, int kt) {
+    SinkSpan s;
+    s.hi = t1 + 1;
+    s.lo = W > 0 ? (t0 - W + 1 > 0 ? t0 - W + 1 : 0) : s.hi;
+    s.sinks = A < s.lo ? A : s.lo;
+    s.ns = (s.sinks + kt - 1) / kt;
+    s.nw = W > 0 ? (s.hi - s.lo + kt - 1) / kt : 0;
+    return s;
+}
+
+constexpr size_t kSinkStatusBytes = 256;
+inline size_t sink_align(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// Query heads packed into one row tile: the largest power of two <= 8 that divides G.
+inline int sink_pack(int G) {
+    int P = 1;
+    while (P < 8 && G % (2 * P) == 0) P *= 2;
+    return P;
+}
+// Key splits of a prefill call whose 256-row tiles alone would leave most SMs idle. `keys`:
+// the longest key range of a row tile (for the workspace's size, a bound of it).
+inline int sink_prefill_splits(int B, int H, int G, int Lq, int64_t keys, int sms) {
+    const int P = sink_pack(G);
+    const int64_t tiles = (int64_t)B * (H / P) * (((int64_t)Lq * P + 255) / 256);
+    const int64_t fill = tiles > 0 ? sms / tiles : 1;
+    const int64_t most = keys / 512;  // four 128-key tiles or more each
+    const int64_t s = fill < most ? fill : most;
+    return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+}
+// Key splits of a shared prefix of P tokens.
+inline int sink_prefix_splits(int B, int Hk, int G, int P, int sms) {
+    const int nb = 128 / G;
+    const int64_t tiles = (int64_t)Hk * ((B + nb - 1) / nb);
+    const int64_t fill = tiles > 0 ? (2 * (int64_t)sms + tiles - 1) / tiles : 1;
+    const int64_t most = P / 256;
+    const int64_t s = fill < most ? fill : most;
+    return (int)(s < 1 ? 1 : s > 128 ? 128 : s);
+}
+inline size_t sink_part_bytes(int64_t rows, int slots, int d) {
+    return sink_align((size_t)rows * slots * d * 4) + sink_align((size_t)rows * slots * 4);
+}
+
+hils_status launch_sink_forward_general(hils_dtype dt, int d, const SinkArgs &a, cudaStream_t s);
+
+// O and lse of every row from its partials: weights exp(lse_s - max) over the row's slots
+// (slots with lse = -inf are skipped).
+struct SinkCombineArgs {
+    const float *part_o, *part_lse;
+    int64_t rows;
+    int slots, H, Lq;  // row = (b * H + h) * Lq + i
+    MutView O;
+    float *lse;
+};
+hils_status launch_sink_combine(hils_dtype dt, int d, const SinkCombineArgs &a, cudaStream_t s);
+
+// ------------------------------------------------------------------ backward and weights
+
+// Key-major items: a block of kSinkKeys keys of one (b, key-value head) and a segment of
+// its steps. Step s covers query rows [i0 + kSinkRows (s % tiles), ..) of group head
+// s / tiles, where [i0, i1) are the rows that see a key of the block.
+constexpr int kSinkKeys = 128, kSinkRows = 128;
+
+struct SinkBwdArgs {
+    View Q, K, V, O, dO;
+    MutView dQ, dK, dV;
+    const float *lse;       // [B, H, Lq]
+    const float *Dv;        // [B, H, Lq] (backward)
+    const float *acc;       // weights: [B, Hk, T]
+    float *acc_out;
+    int64_t T;
+    int B, H, G, Lq, N, W, A;
+    float scale;
+    // key blocks [0, nsink) are cut into seg_s segments each, the others into seg_w
+    int nblk, nsink, seg_s, seg_w;
+    float *part;            // partial sums of blocks with more than one segment
+    uint32_t *status = nullptr;
+    long long wait_ns = kWaitLimitNs;
+};
+
+// Query rows [i0, i1) that see a key of block [j0, j0 + keys).
+__host__ __device__ inline void sink_rows_of_block(const SinkBwdArgs &a, int j0, int keys, int *i0, int *i1) {
+    const int off = a.N - a.Lq;
+    *i0 = j0 > off ? j0 - off : 0;
+    if (j0 < a.A) {
+        *i1 = a.Lq;
+    } else if (a.W > 0) {
+        const int64_t e = (int64_t)j0 + keys - 1 + a.W - off;
+        *i1 = e < a.Lq ? (int)(e > 0 ? e : 0) : a.Lq;
+    } else {
+        *i1 = *i0;
+    }
+    if (*i1 < *i0) *i1 = *i0;
+}
+
+// The division of the key blocks: enough items for every SM, at least eight steps each.
+inline void sink_key_plan(int B, int Hk, int G, int Lq, int N, int W, int A, SinkBwdArgs *a) {
+    a->nblk = (N + kSinkKeys - 1) / kSinkKeys;
+    a->nsink = (A + kSinkKeys - 1) / kSinkKeys;
+    if (a->nsink > a->nblk) a->nsink = a->nblk;
+    auto segments = [&](int blocks, int64_t rows) {
+        const int64_t steps = (int64_t)G * ((rows + kSinkRows - 1) / kSinkRows);
+        const int64_t fill = 592 / ((int64_t)B * Hk * (blocks > 0 ? blocks : 1));
+        int64_t s = steps / 8 < fill ? steps / 8 : fill;
+        return (int)(s < 1 ? 1 : s);
+    };
+    a->seg_s = segments(a->nsink, Lq);
+    const int64_t wr = (int64_t)W + kSinkKeys;
+    a->seg_w = segments(a->nblk - a->nsink, wr < Lq ? wr : Lq);
+}
+inline int64_t sink_key_items(const SinkBwdArgs &a) {
+    return (int64_t)a.nsink * a.seg_s + (int64_t)(a.nblk - a.nsink) * a.seg_w;
+}
+// Floats of partial sums (`per_key` of each key: 2 d for dK and dV, 1 for weights).
+inline size_t sink_key_part_floats(const SinkBwdArgs &a, int per_key) {
+    if (a.seg_s <= 1 && a.seg_w <= 1) return 0;
+    return (size_t)a.B * (a.H / a.G) * sink_key_items(a) * kSinkKeys * per_key;
+}
+
+struct SinkItem {
+    int blk, seg, nseg;
+};
+__host__ __device__ inline SinkItem sink_item(const SinkBwdArgs &a, int x) {
+    SinkItem it;
+    const int ns = a.nsink * a.seg_s;
+    it.nseg = x < ns ? a.seg_s : a.seg_w;
+    it.blk = x < ns ? x / a.seg_s : a.nsink + (x - ns) / a.seg_w;
+    it.seg = x < ns ? x % a.seg_s : (x - ns) % a.seg_w;
+    return it;
+}
+
+hils_status launch_sink_dot(hils_dtype dt, int d, const SinkBwdArgs &a, float *Dv, cudaStream_t s);
+hils_status launch_sink_backward_general(hils_dtype dt, int d, const SinkBwdArgs &a, cudaStream_t s);
+hils_status launch_sink_weights_general(hils_dtype dt, int d, const SinkBwdArgs &a, cudaStream_t s);
+// Sums the segments' partials in segment order into dK and dV, or acc_out.
+hils_status launch_sink_reduce(hils_dtype dt, int d, const SinkBwdArgs &a, bool weights, cudaStream_t s);
+
+// ------------------------------------------------------------------ decode
+
+struct SinkDecodeArgs {
+    View Q, K, V;
+    const int32_t *cache_len;  // [B]
+    int B, H, G, T, W, A;      // W, A <= T
+    float scale;
+    int splits, slot0, slots;  // this call's partials are slots slot0 .. slot0 + splits - 1
+    float *part_o, *part_lse;  // rows (b, h)
+    float *logits;             // with acc: [B, H, logit_stride] scaled logits in log2 units, by visible order
+    int64_t logit_stride;
+};
+// The slots that a sequence of n tokens sees: [0, sinks), then [lo, n).
+__host__ __device__ inline void sink_visible(int n, int W, int A, int *sinks, int *lo) {
+    *lo = n > W ? n - W : 0;
+    *sinks = A < *lo ? A : *lo;
+}
+int sink_decode_splits(int B, int Hk, int64_t keys, int sms);
+hils_status launch_sink_decode(hils_dtype dt, int d, const SinkDecodeArgs &a, cudaStream_t s);
+// acc_out[b, hk, j] = acc[b, hk, j] + sum over the group's heads of p_j, for the visible
+// slots j, from the call's logits and the rows' lse [B, H].
+hils_status launch_sink_decode_acc(const SinkDecodeArgs &a, const float *lse, const float *acc, float *acc_out,
+                                   cudaStream_t s);
+
+// ------------------------------------------------------------------ eviction
+
+struct EvictArgs {
+    View K, V;
+    MutView Kout, Vout;
+    const float *acc;          // [B, Hk, T]
+    const int32_t *cache_len;  // [B]
+    float *acc_out;            // [B, Hk, budget]
+    int32_t *idx;              // [B, Hk, budget]
+    int32_t *len_out;          // [B]
+    int B, Hk, T, budget, W, A;
+};
+hils_status launch_cache_evict(hils_dtype dt, int d, const EvictArgs &a, cudaStream_t s);
+
+// Workspace sizes of the calls above (0: invalid parameters or another call).
+size_t sink_ws_bytes(const hils_params *p, int call, int rows, int other);
+
+}  // namespace hils

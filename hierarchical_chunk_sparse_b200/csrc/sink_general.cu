@@ -1,0 +1,505 @@
+// Window-and-sink attention on the CUDA cores: prefill, shared prefix, backward and
+// accumulated weights (formulas in sink_common.cuh). 64 x 64 tiles of scores, 256 threads
+// with 4 x 4 of them each; every product and sum in float32.
+#include "sink_common.cuh"
+
+namespace hils {
+namespace {
+
+constexpr int kT = 64;        // rows and keys per tile
+constexpr int kThr = 256;
+constexpr int kPS = kT + 4;   // row stride of the probability tiles in shared memory
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
+
+// 16 lanes' maximum / sum (the threads that share a row)
+__device__ __forceinline__ float max16(float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+__device__ __forceinline__ float sum16(float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+
+// Row r of a [64][D + 4] float tile from element pointer src (null: zeros).
+template <typename T, int D, typename F>
+__device__ __forceinline__ void load_tile(float *dst, F row_ptr) {
+    constexpr int kV = Vec<T>::kN, kU = D / kV;  // 16-byte units per row
+    for (int e = threadIdx.x; e < kT * kU; e += kThr) {
+        const int r = e / kU, u = e % kU;
+        const T *p = row_ptr(r);
+        float f[kV];
+        if (p) {
+            widen(__ldg(reinterpret_cast<const uint4 *>(p) + u), f, T());
+        } else {
+#pragma unroll
+            for (int i = 0; i < kV; ++i) f[i] = 0.f;
+        }
+        float *d = dst + r * (D + 4) + u * kV;
+#pragma unroll
+        for (int i = 0; i < kV; i += 4) *reinterpret_cast<float4 *>(d + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+    }
+}
+
+// acc[r][c] = X row (4 ty + r) . Y row (tx + 16 c) over D
+template <int D>
+__device__ __forceinline__ void dot_tile(float (&acc)[4][4], const float *X, const float *Y, int ty, int tx) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[r][c] = 0.f;
+#pragma unroll 4
+    for (int x = 0; x < D; x += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const float4 *>(X + (4 * ty + r) * (D + 4) + x);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) b[c] = *reinterpret_cast<const float4 *>(Y + (tx + 16 * c) * (D + 4) + x);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                acc[r][c] = fmaf(a[r].x, b[c].x, acc[r][c]);
+                acc[r][c] = fmaf(a[r].y, b[c].y, acc[r][c]);
+                acc[r][c] = fmaf(a[r].z, b[c].z, acc[r][c]);
+                acc[r][c] = fmaf(a[r].w, b[c].w, acc[r][c]);
+            }
+    }
+}
+
+// o[r][4 u + i] += sum_k P[4 ty + r][k] Y[k][64 u + 4 tx + i]
+template <int D>
+__device__ __forceinline__ void add_product(float (&o)[4][D / 16], const float *P, const float *Y, int ty, int tx) {
+#pragma unroll 4
+    for (int k = 0; k < kT; ++k) {
+        float p[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) p[r] = P[(4 * ty + r) * kPS + k];
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u) {
+            const float4 y = *reinterpret_cast<const float4 *>(Y + k * (D + 4) + 64 * u + 4 * tx);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                o[r][4 * u + 0] = fmaf(p[r], y.x, o[r][4 * u + 0]);
+                o[r][4 * u + 1] = fmaf(p[r], y.y, o[r][4 * u + 1]);
+                o[r][4 * u + 2] = fmaf(p[r], y.z, o[r][4 * u + 2]);
+                o[r][4 * u + 3] = fmaf(p[r], y.w, o[r][4 * u + 3]);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void store4(float *p, float a, float b, float c, float d) {
+    *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void store4(bf16 *p, float a, float b, float c, float d) {
+    uint2 v;
+    const __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
+    v.x = *reinterpret_cast<const uint32_t *>(&x);
+    v.y = *reinterpret_cast<const uint32_t *>(&y);
+    *reinterpret_cast<uint2 *>(p) = v;
+}
+
+template <int D>
+constexpr int fwd_smem() {
+    return (3 * kT * (D + 4) + kT * kPS) * 4;
+}
+
+// One CTA per (row tile, split): online softmax over the tile's keys.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThr) sink_fwd_kernel(SinkArgs a, int tiles) {
+    extern __shared__ float sm[];
+    float *Qs = sm, *Ks = Qs + kT * (D + 4), *Vs = Ks + kT * (D + 4), *Ps = Vs + kT * (D + 4);
+    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+    const int Hk = a.H / a.G;
+    int x = blockIdx.x;
+    const int split = x % a.splits;
+    x /= a.splits;
+    const int tile = a.prefix ? x % tiles : tiles - 1 - x % tiles;  // latest rows (most keys) first
+    x /= tiles;
+    const int nb = a.prefix ? kT / a.G : 1;
+    const int h = a.prefix ? 0 : x % a.H, b = a.prefix ? 0 : x / a.H;
+    const int hk = a.prefix ? x : h / a.G;
+    // row r of this tile: its query, its place among all rows, its position (-1: no row)
+    auto row = [&](int r, const T **q, int64_t *place) -> int {
+        int bb = b, hh = h, i = tile * kT + r;
+        if (a.prefix) {
+            bb = tile * nb + r / a.G;
+            hh = hk * a.G + r % a.G;
+            i = 0;
+            if (r >= nb * a.G || bb >= a.B) return -1;
+        } else if (i >= a.Lq) {
+            return -1;
+        }
+        *q = static_cast<const T *>(a.Q.ptr) + bb * a.Q.sb + hh * a.Q.sh + i * a.Q.st;
+        *place = ((int64_t)bb * a.H + hh) * a.Lq + i;
+        return a.prefix ? max(a.N - 1, 0) : a.N - a.Lq + i;
+    };
+    const T *Kb = static_cast<const T *>(a.K.ptr) + b * a.K.sb + hk * a.K.sh;
+    const T *Vb = static_cast<const T *>(a.V.ptr) + b * a.V.sb + hk * a.V.sh;
+    const int t0 = a.prefix ? a.N - 1 : a.N - a.Lq + tile * kT;
+    const int t1 = a.prefix ? a.N - 1 : min(a.N - 1, t0 + kT - 1);
+    SinkSpan sp = sink_span(t0, t1, a.W, a.A, kT);
+    if (a.prefix) sp = {0, 0, 0, a.N, (a.N + kT - 1) / kT};
+    const int nt = sp.ns + sp.nw;
+    const int i0 = (int)((int64_t)nt * split / a.splits), i1 = (int)((int64_t)nt * (split + 1) / a.splits);
+
+    load_tile<T, D>(Qs, [&](int r) -> const T * {
+        const T *q = nullptr;
+        int64_t place;
+        return row(r, &q, &place) >= 0 ? q : nullptr;
+    });
+    int tr[4];
+    int64_t place[4];
+    float m[4], l[4], o[4][D / 16];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const T *q;
+        place[r] = 0;
+        tr[r] = row(4 * ty + r, &q, &place[r]);
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) o[r][c] = 0.f;
+    }
+    const float scale2 = a.scale * 1.4426950408889634f;
+    for (int i = i0; i < i1; ++i) {
+        const bool sink = i < sp.ns;
+        const int k0 = sink ? i * kT : sp.lo + (i - sp.ns) * kT;
+        const int end = sink ? sp.sinks : sp.hi;
+        __syncthreads();
+        load_tile<T, D>(Ks, [&](int r) -> const T * { return k0 + r < end ? Kb + (int64_t)(k0 + r) * a.K.st : nullptr; });
+        load_tile<T, D>(Vs, [&](int r) -> const T * { return k0 + r < end ? Vb + (int64_t)(k0 + r) * a.V.st : nullptr; });
+        __syncthreads();
+        float s[4][4];
+        dot_tile<D>(s, Qs, Ks, ty, tx);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float mt = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int j = k0 + tx + 16 * c;
+                const bool in = j < end && j <= tr[r] && (sink || j < a.A || j > tr[r] - a.W);
+                s[r][c] = in ? s[r][c] * scale2 : -INFINITY;
+                mt = fmaxf(mt, s[r][c]);
+            }
+            mt = fmaxf(max16(mt), m[r]);
+            const float f = mt == -INFINITY ? 1.f : exp2f(m[r] - mt);
+            const float ref = mt == -INFINITY ? 0.f : mt;
+            float z = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float p = exp2f(s[r][c] - ref);
+                z += p;
+                Ps[(4 * ty + r) * kPS + tx + 16 * c] = p;
+            }
+            l[r] = l[r] * f + sum16(z);
+            m[r] = mt;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) o[r][c] *= f;
+        }
+        __syncwarp();  // a row's probabilities are written and read by one half-warp
+        add_product<D>(o, Ps, Vs, ty, tx);
+    }
+    const bool part = a.part_o != nullptr;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        if (tr[r] < 0) continue;
+        const float inv = l[r] > 0.f ? 1.f / l[r] : 0.f;
+        const float lse = l[r] > 0.f ? (m[r] + log2f(l[r])) * 0.6931471805599453f : -INFINITY;
+        if (part) {
+            float *dst = a.part_o + (place[r] * a.slots + split) * D;
+#pragma unroll
+            for (int u = 0; u < D / 64; ++u)
+                store4(dst + 64 * u + 4 * tx, o[r][4 * u] * inv, o[r][4 * u + 1] * inv, o[r][4 * u + 2] * inv, o[r][4 * u + 3] * inv);
+            if (tx == 0) a.part_lse[place[r] * a.slots + split] = lse;
+        } else {
+            const int64_t i = place[r] % a.Lq, bh = place[r] / a.Lq;
+            T *dst = static_cast<T *>(a.O.ptr) + (bh / a.H) * a.O.sb + (bh % a.H) * a.O.sh + i * a.O.st;
+#pragma unroll
+            for (int u = 0; u < D / 64; ++u)
+                store4(dst + 64 * u + 4 * tx, o[r][4 * u] * inv, o[r][4 * u + 1] * inv, o[r][4 * u + 2] * inv, o[r][4 * u + 3] * inv);
+            if (tx == 0 && a.lse) a.lse[place[r]] = lse;
+        }
+    }
+}
+
+// D_i = dO_i . o_i, one warp per query row.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) sink_dot_kernel(SinkBwdArgs a, float *Dv) {
+    const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    if (row >= (int64_t)a.B * a.H * a.Lq) return;
+    const int64_t i = row % a.Lq, bh = row / a.Lq, b = bh / a.H, h = bh % a.H;
+    const T *o = static_cast<const T *>(a.O.ptr) + b * a.O.sb + h * a.O.sh + i * a.O.st;
+    const T *g = static_cast<const T *>(a.dO.ptr) + b * a.dO.sb + h * a.dO.sh + i * a.dO.st;
+    float s = 0.f;
+#pragma unroll
+    for (int x = 2 * lane; x < D; x += 64) {
+        const float2 u = load2(o + x), v = load2(g + x);
+        s = fmaf(u.x, v.x, fmaf(u.y, v.y, s));
+    }
+    s = warp_sum(s);
+    if (lane == 0) Dv[row] = s;
+}
+
+// Whether any query row sees key j: the slots of acc_out that a weights call writes.
+__device__ __forceinline__ bool seen_key(const SinkBwdArgs &a, int j) {
+    int i0, i1;
+    sink_rows_of_block(a, j, 1, &i0, &i1);
+    return i0 < i1;
+}
+
+enum { kModeDq = 0, kModeDkv = 1, kModeWeights = 2 };
+
+template <int D>
+constexpr int bwd_smem(int mode) {
+    return mode == kModeWeights ? 2 * kT * (D + 4) * 4 : (4 * kT * (D + 4) + 2 * kT * kPS + 2 * kT) * 4;
+}
+
+// Query-major (dQ): rows are 64 queries of one head, tiles are keys. Key-major (dK and dV,
+// or the weights): rows are 64 keys of one key-value head, tiles are queries of the
+// group's heads. X1, X2 are the rows' Q, dO or K, V; Y1, Y2 the tiles' K, V or Q, dO.
+template <int MODE, typename T, int D>
+__global__ void __launch_bounds__(kThr) sink_bwd_kernel(SinkBwdArgs a, int tiles) {
+    extern __shared__ float sm[];
+    constexpr bool kTwo = MODE != kModeWeights;
+    float *X1 = sm, *Y1 = X1 + kT * (D + 4);
+    float *X2 = Y1 + kT * (D + 4), *Y2 = X2 + kT * (D + 4), *Ps = Y2 + kT * (D + 4), *Ss = Ps + kT * kPS;
+    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+    const int Hk = a.H / a.G, off = a.N - a.Lq;
+    const float kLog2e = 1.4426950408889634f, scale2 = a.scale * kLog2e;
+    auto at = [&](const View &v, int b, int h, int i) {
+        return static_cast<const T *>(v.ptr) + b * v.sb + h * v.sh + (int64_t)i * v.st;
+    };
+    int b, h, hk, r0, nrows, s0, s1, qtiles = 1, i0 = 0, ilim = 0;
+    SinkSpan sp{};
+    SinkItem it{};
+    int xb = 0;
+    if (MODE == kModeDq) {
+        const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
+        b = bh / a.H;
+        h = bh % a.H;
+        hk = h / a.G;
+        r0 = tile * kT;
+        nrows = min(kT, a.Lq - r0);
+        sp = sink_span(off + r0, off + r0 + nrows - 1, a.W, a.A, kT);
+        s0 = 0;
+        s1 = sp.ns + sp.nw;
+    } else {
+        // an item's 128-key block in two halves of 64 keys
+        const int half = blockIdx.x % 2, x = (blockIdx.x / 2) % tiles;
+        xb = (blockIdx.x / 2) / tiles;
+        b = xb / Hk;
+        hk = xb % Hk;
+        h = 0;
+        it = sink_item(a, x);
+        r0 = it.blk * kSinkKeys + half * kT;
+        nrows = max(0, min(kT, a.N - r0));
+        if (nrows == 0) return;
+        sink_rows_of_block(a, r0, kT, &i0, &ilim);
+        qtiles = (ilim - i0 + kT - 1) / kT;
+        const int64_t steps = (int64_t)a.G * qtiles;
+        s0 = (int)(steps * it.seg / it.nseg);
+        s1 = (int)(steps * (it.seg + 1) / it.nseg);
+    }
+    load_tile<T, D>(X1, [&](int r) -> const T * {
+        return r < nrows ? (MODE == kModeDq ? at(a.Q, b, h, r0 + r) : at(a.K, b, hk, r0 + r)) : nullptr;
+    });
+    if (kTwo)
+        load_tile<T, D>(X2, [&](int r) -> const T * {
+            return r < nrows ? (MODE == kModeDq ? at(a.dO, b, h, r0 + r) : at(a.V, b, hk, r0 + r)) : nullptr;
+        });
+    float o1[4][D / 16], o2[4][D / 16], w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) o1[r][c] = o2[r][c] = 0.f;
+    for (int st = s0; st < s1; ++st) {
+        int k0 = 0, end = 0, hh = h, q0 = 0;
+        bool sink = false;
+        if (MODE == kModeDq) {
+            sink = st < sp.ns;
+            k0 = sink ? st * kT : sp.lo + (st - sp.ns) * kT;
+            end = sink ? sp.sinks : sp.hi;
+        } else {
+            hh = hk * a.G + st / qtiles;
+            q0 = i0 + (st % qtiles) * kT;
+        }
+        auto y = [&](const View &kv, const View &qv, int r) -> const T * {
+            if (MODE == kModeDq) return k0 + r < end ? at(kv, b, hk, k0 + r) : nullptr;
+            return q0 + r < ilim ? at(qv, b, hh, q0 + r) : nullptr;
+        };
+        __syncthreads();
+        load_tile<T, D>(Y1, [&](int r) { return y(a.K, a.Q, r); });
+        if (kTwo) load_tile<T, D>(Y2, [&](int r) { return y(a.V, a.dO, r); });
+        __syncthreads();
+        float s[4][4], dp[4][4];
+        dot_tile<D>(s, X1, Y1, ty, tx);
+        if (kTwo) dot_tile<D>(dp, X2, Y2, ty, tx);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int rr = 4 * ty + r, cc = tx + 16 * c;
+                const int i = MODE == kModeDq ? r0 + rr : q0 + cc;  // query row
+                const int j = MODE == kModeDq ? k0 + cc : r0 + rr;  // key
+                const int t = off + i;
+                const bool in = (MODE == kModeDq ? rr < nrows && j < end : i < ilim && rr < nrows) && j <= t &&
+                                (sink || j < a.A || j > t - a.W);
+                const int64_t q = ((int64_t)b * a.H + hh) * a.Lq + i;
+                const float L = in ? __ldg(a.lse + q) : -INFINITY;
+                const float p = in && L != -INFINITY ? exp2f(s[r][c] * scale2 - L * kLog2e) : 0.f;
+                if (kTwo) {
+                    const float ds = in ? a.scale * p * (dp[r][c] - __ldg(a.Dv + q)) : 0.f;
+                    if (MODE == kModeDkv) Ps[rr * kPS + cc] = p;
+                    Ss[rr * kPS + cc] = ds;
+                } else {
+                    w[r] += p;
+                }
+            }
+        if (kTwo) {
+            __syncwarp();
+            add_product<D>(o1, Ss, Y1, ty, tx);
+            if (MODE == kModeDkv) add_product<D>(o2, Ps, Y2, ty, tx);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int rr = 4 * ty + r;
+        const float ws = MODE == kModeWeights ? sum16(w[r]) : 0.f;
+        if (rr >= nrows) continue;
+        const int64_t item = (int64_t)xb * tiles + (blockIdx.x / 2) % tiles;  // key-major: partial sums' place
+        const int kr = r0 + rr - it.blk * kSinkKeys;
+        if (MODE == kModeWeights) {
+            if (tx == 0) {
+                const int64_t g = ((int64_t)b * Hk + hk) * a.T + r0 + rr;
+                if (it.nseg > 1) a.part[item * kSinkKeys + kr] = ws;
+                else if (seen_key(a, r0 + rr)) a.acc_out[g] = a.acc[g] + ws;
+            }
+            continue;
+        }
+        if (MODE == kModeDkv && it.nseg > 1) {
+            float *d1 = a.part + (item * 2 * kSinkKeys + kr) * D, *d2 = d1 + kSinkKeys * D;
+#pragma unroll
+            for (int u = 0; u < D / 64; ++u) {
+                store4(d1 + 64 * u + 4 * tx, o1[r][4 * u], o1[r][4 * u + 1], o1[r][4 * u + 2], o1[r][4 * u + 3]);
+                store4(d2 + 64 * u + 4 * tx, o2[r][4 * u], o2[r][4 * u + 1], o2[r][4 * u + 2], o2[r][4 * u + 3]);
+            }
+            continue;
+        }
+        const MutView &v1 = MODE == kModeDq ? a.dQ : a.dK;
+        T *d1 = static_cast<T *>(v1.ptr) + b * v1.sb + (MODE == kModeDq ? h : hk) * v1.sh + (int64_t)(r0 + rr) * v1.st;
+        T *d2 = MODE == kModeDkv ? static_cast<T *>(a.dV.ptr) + b * a.dV.sb + hk * a.dV.sh + (int64_t)(r0 + rr) * a.dV.st : nullptr;
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u) {
+            store4(d1 + 64 * u + 4 * tx, o1[r][4 * u], o1[r][4 * u + 1], o1[r][4 * u + 2], o1[r][4 * u + 3]);
+            if (MODE == kModeDkv)
+                store4(d2 + 64 * u + 4 * tx, o2[r][4 * u], o2[r][4 * u + 1], o2[r][4 * u + 2], o2[r][4 * u + 3]);
+        }
+    }
+}
+
+// One warp per key row of a block with several segments: the partials in segment order.
+template <bool WEIGHTS, typename T, int D>
+__global__ void __launch_bounds__(256) sink_reduce_kernel(SinkBwdArgs a, int items) {
+    const int64_t g = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32, Hk = a.H / a.G;
+    if (g >= (int64_t)a.B * Hk * a.N) return;
+    const int j = (int)(g % a.N);
+    const int64_t xb = g / a.N;
+    const int blk = j / kSinkKeys, kr = j % kSinkKeys;
+    const int nseg = blk < a.nsink ? a.seg_s : a.seg_w;
+    if (nseg <= 1) return;
+    const int64_t first = xb * items + (blk < a.nsink ? blk * a.seg_s : a.nsink * a.seg_s + (blk - a.nsink) * a.seg_w);
+    if (WEIGHTS) {
+        if (lane != 0 || !seen_key(a, j)) return;
+        float s = 0.f;
+        for (int q = 0; q < nseg; ++q) s += a.part[(first + q) * kSinkKeys + kr];
+        const int64_t at = xb * a.T + j;
+        a.acc_out[at] = a.acc[at] + s;
+        return;
+    }
+    const int b = (int)(xb / Hk), hk = (int)(xb % Hk);
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const MutView &v = which ? a.dV : a.dK;
+        T *dst = static_cast<T *>(v.ptr) + b * v.sb + hk * v.sh + (int64_t)j * v.st;
+        for (int x = 2 * lane; x < D; x += 64) {
+            float2 s = make_float2(0.f, 0.f);
+            for (int q = 0; q < nseg; ++q) {
+                const float2 p = load2(a.part + ((first + q) * 2 * kSinkKeys + which * kSinkKeys + kr) * D + x);
+                s.x += p.x;
+                s.y += p.y;
+            }
+            store2(dst + x, s.x, s.y);
+        }
+    }
+}
+
+template <typename K>
+hils_status run(KernelSetup &setup, K kernel, int64_t grid, int threads, int smem, cudaStream_t s, auto... args) {
+    if (grid <= 0) return HILS_OK;
+    if (grid > 0x7fffffffll) return HILS_ERR_UNSUPPORTED;
+    const hils_status st = kernel_setup(setup, (const void *)kernel, threads, smem, nullptr);
+    if (st != HILS_OK) return st;
+    kernel<<<(unsigned)grid, threads, smem, s>>>(args...);
+    return record_cuda_error(cudaGetLastError());
+}
+
+template <typename T, int D>
+hils_status forward(const SinkArgs &a, cudaStream_t s) {
+    static KernelSetup setup;
+    const int tiles = a.prefix ? (a.B + kT / a.G - 1) / (kT / a.G) : (a.Lq + kT - 1) / kT;
+    const int64_t grid = (int64_t)tiles * a.splits * (a.prefix ? a.H / a.G : (int64_t)a.B * a.H);
+    return run(setup, sink_fwd_kernel<T, D>, grid, kThr, fwd_smem<D>(), s, a, tiles);
+}
+template <typename T, int D>
+hils_status dot(const SinkBwdArgs &a, float *Dv, cudaStream_t s) {
+    static KernelSetup setup;
+    return run(setup, sink_dot_kernel<T, D>, ((int64_t)a.B * a.H * a.Lq + 7) / 8, 256, 0, s, a, Dv);
+}
+template <typename T, int D>
+hils_status backward(const SinkBwdArgs &a, cudaStream_t s) {
+    static KernelSetup sq, sk;
+    const int tiles = (a.Lq + kT - 1) / kT;
+    const hils_status st =
+        run(sq, sink_bwd_kernel<kModeDq, T, D>, (int64_t)tiles * a.B * a.H, kThr, bwd_smem<D>(kModeDq), s, a, tiles);
+    if (st != HILS_OK) return st;
+    const int items = (int)sink_key_items(a);
+    return run(sk, sink_bwd_kernel<kModeDkv, T, D>, 2ll * items * a.B * (a.H / a.G), kThr, bwd_smem<D>(kModeDkv), s, a, items);
+}
+template <typename T, int D>
+hils_status weights(const SinkBwdArgs &a, cudaStream_t s) {
+    static KernelSetup setup;
+    const int items = (int)sink_key_items(a);
+    return run(setup, sink_bwd_kernel<kModeWeights, T, D>, 2ll * items * a.B * (a.H / a.G), kThr, bwd_smem<D>(kModeWeights), s,
+               a, items);
+}
+template <typename T, int D>
+hils_status reduce(const SinkBwdArgs &a, bool w, cudaStream_t s) {
+    static KernelSetup s0, s1;
+    if (a.seg_s <= 1 && a.seg_w <= 1) return HILS_OK;
+    const int64_t grid = ((int64_t)a.B * (a.H / a.G) * a.N + 7) / 8;
+    const int items = (int)sink_key_items(a);
+    return w ? run(s0, sink_reduce_kernel<true, T, D>, grid, 256, 0, s, a, items)
+             : run(s1, sink_reduce_kernel<false, T, D>, grid, 256, 0, s, a, items);
+}
+
+}  // namespace
+
+#define BY_TYPE(fn, ...)                                                                              \
+    (dt == HILS_BF16 ? (d == 64 ? fn<bf16, 64>(__VA_ARGS__) : fn<bf16, 128>(__VA_ARGS__))             \
+                     : (d == 64 ? fn<float, 64>(__VA_ARGS__) : fn<float, 128>(__VA_ARGS__)))
+
+hils_status launch_sink_forward_general(hils_dtype dt, int d, const SinkArgs &a, cudaStream_t s) { return BY_TYPE(forward, a, s); }
+hils_status launch_sink_dot(hils_dtype dt, int d, const SinkBwdArgs &a, float *Dv, cudaStream_t s) { return BY_TYPE(dot, a, Dv, s); }
+hils_status launch_sink_backward_general(hils_dtype dt, int d, const SinkBwdArgs &a, cudaStream_t s) { return BY_TYPE(backward, a, s); }
+hils_status launch_sink_weights_general(hils_dtype dt, int d, const SinkBwdArgs &a, cudaStream_t s) { return BY_TYPE(weights, a, s); }
+hils_status launch_sink_reduce(hils_dtype dt, int d, const SinkBwdArgs &a, bool w, cudaStream_t s) { return BY_TYPE(reduce, a, w, s); }
+
+}  // namespace hils

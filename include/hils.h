@@ -18,6 +18,12 @@
  *   hils_summarize_append  decode-time summary of the chunk each newest token completed
  *   hils_attend_prefill_backward, hils_select_backward, hils_summarize_backward
  *                        gradients for a fixed selection            (Eq. 10, Eq. 7, Eq. 8)
+ * Beside them, for a model's layers without chunk selection and their caches:
+ *   hils_sink_prefill, hils_sink_prefill_backward, hils_sink_decode
+ *                        attention with a sliding window and sinks
+ *   hils_sink_weights, hils_cache_evict
+ *                        accumulated attention weights; eviction from a cache by them
+ *   hils_prefix_decode   one decode step of a batch that shares a prefix
  *
  * Conventions shared by every call
  * --------------------------------
@@ -149,7 +155,16 @@ typedef enum {
     HILS_CALL_ATTEND_PREFILL = 1,
     HILS_CALL_ATTEND_DECODE = 2,
     HILS_CALL_DECODE = 3,
-    HILS_CALL_ATTEND_BACKWARD = 4
+    HILS_CALL_ATTEND_BACKWARD = 4,
+    /* the window-and-sink, shared-prefix and eviction calls: what Lq and C of
+     * hils_workspace_bytes are for them stands at each call */
+    HILS_CALL_SINK_PREFILL = 5,
+    HILS_CALL_SINK_BACKWARD = 6,
+    HILS_CALL_SINK_WEIGHTS = 7,
+    HILS_CALL_SINK_DECODE = 8,
+    HILS_CALL_SINK_DECODE_ACC = 9,
+    HILS_CALL_PREFIX_DECODE = 10,
+    HILS_CALL_CACHE_EVICT = 11
 } hils_call;
 
 /* Landmark chunk summaries (summary page, Methodology 1, Eq. 8).
@@ -330,6 +345,94 @@ int hils_select_backward(const hils_params *p, hils_ctensor Qcal, int Lq, hils_c
 int hils_summarize_backward(const hils_params *p, hils_ctensor K, int N, hils_ctensor LQ,
                             const float *dKsum, const float *dBsum, float *dK, float *dLQ, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------------------
+ * Attention with a sliding window and sinks, for the layers of a model that do not select
+ * chunks, and the calls that keep their caches. The pages have no counterpart.
+ *
+ * A query at position t sees the first A tokens (the sinks) and the W = params->W newest
+ * up to its own, each once:
+ *   V(t) = { j <= t : j < A or j > t - W },   s_tj = scale q_t . k_j,
+ *   lse_t = log sum_{j in V(t)} exp(s_tj),    p_tj = exp(s_tj - lse_t),
+ *   o_t = sum_{j in V(t)} p_tj v_j.
+ * W >= N is full causal attention; A = 0 is the plain window; a query that sees nothing
+ * (A = 0 and W = 0) gets o = 0 and lse = -inf. params->K is not used. With grouped heads,
+ * query head h reads key-value head h / G.
+ * Slots that no query of a call sees are never part of a result, whatever they hold (NaN
+ * included); a slot that some query sees has to be finite.
+ * Sums, softmax statistics and products are float32; for bf16 the probabilities and the
+ * score gradients are rounded to bf16 as operands of their matrix products.
+ * The first 32-bit word of each workspace is a status word, as in hils_attend_prefill.
+ * No result depends on an order of atomic additions: equal calls give equal bits.
+ * ------------------------------------------------------------------------------------ */
+
+/* The Lq newest queries of N tokens (query i at t = N - Lq + i; Lq = N is a whole prompt,
+ * Lq < N a later piece of one whose earlier keys are cached).
+ *   Q, O [B, H, Lq, d];  K, V [B, Hk, N, d];  lse [B, H, Lq] float32 out, or NULL
+ *   workspace: hils_workspace_bytes(p, HILS_CALL_SINK_PREFILL, Lq, A), zeroed before first use */
+int hils_sink_prefill(const hils_params *p, int A, hils_ctensor Q, int Lq, hils_ctensor K, hils_ctensor V, int N,
+                      hils_tensor O, float *lse, void *workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* Its backward for Lq = N, from O and lse of the forward:
+ *   D_t = dO_t . o_t,  ds_tj = scale p_tj (dO_t . v_j - D_t),
+ *   dQ = ds K,  dK = ds^T Q,  dV = p^T dO (summed over a group's heads).
+ *   O, dO [B, H, N, d];  lse [B, H, N];  dQ [B, H, N, d], dK, dV [B, Hk, N, d] out, in
+ *   dtype, every element written (zeros for a token that no query sees)
+ *   workspace: hils_workspace_bytes(p, HILS_CALL_SINK_BACKWARD, N, A), zeroed before first use */
+int hils_sink_prefill_backward(const hils_params *p, int A, hils_ctensor Q, hils_ctensor K, hils_ctensor V, int N,
+                               hils_ctensor O, const float *lse, hils_ctensor dO, hils_tensor dQ, hils_tensor dK,
+                               hils_tensor dV, void *workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* The attention weight that each cached token drew from the Lq newest queries:
+ *   acc_out[b, hk, j] = acc[b, hk, j] + sum over the group's heads and the queries of p_tj
+ * for every token j that some of the queries sees; the other slots of acc_out are left as
+ * they were. acc_out may be acc.
+ *   Q [B, H, Lq, d];  K [B, Hk, N, d];  lse [B, H, Lq] of the forward
+ *   acc, acc_out [B, Hk, T] float32, T >= N
+ *   workspace: hils_workspace_bytes(p, HILS_CALL_SINK_WEIGHTS, N, A), zeroed before first use */
+int hils_sink_weights(const hils_params *p, int A, hils_ctensor Q, int Lq, hils_ctensor K, int N, const float *lse,
+                      const float *acc, float *acc_out, int T, void *workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* One new token per sequence: the query sits at t = cache_len[b] - 1 (W >= T attends to the
+ * whole cache). cache_len[b] = 0 gives o = 0, lse = -inf; a value outside [0, T] counts as
+ * the nearer end.
+ *   Q, O [B, H, 1, d];  Kc, Vc [B, Hk, T, d] (invisible slots are not read);  cache_len [B]
+ *   int32, device;  lse [B, H] float32 out, or NULL
+ *   acc, acc_out [B, Hk, T] float32, or both NULL: acc_out[b, hk, j] = acc[b, hk, j] + the
+ *   sum of p_j over the group's heads for the visible slots j, others left as they were;
+ *   acc_out may be acc
+ *   workspace: hils_workspace_bytes(p, HILS_CALL_SINK_DECODE, T, A), with acc
+ *   HILS_CALL_SINK_DECODE_ACC; zeroed before first use */
+int hils_sink_decode(const hils_params *p, int A, hils_ctensor Q, hils_ctensor Kc, hils_ctensor Vc, int T,
+                     const int32_t *cache_len, hils_tensor O, float *lse, const float *acc, float *acc_out,
+                     void *workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* One new token for each of B sequences that share a prefix of P tokens and go on in caches
+ * of their own: softmax over the prefix and the sequence's cache_len[b] slots together.
+ * The prefix is read once for the whole batch. params->W is not used.
+ *   Q, O [B, H, 1, d];  Kp, Vp [1, Hk, P, d] (their sb is not used);  Kc, Vc [B, Hk, T, d];
+ *   cache_len [B] int32, device, each in [0, T] (outside: the nearer end);
+ *   lse [B, H] float32 out, or NULL
+ *   workspace: hils_workspace_bytes(p, HILS_CALL_PREFIX_DECODE, T, P), zeroed before first use */
+int hils_prefix_decode(const hils_params *p, hils_ctensor Q, hils_ctensor Kp, hils_ctensor Vp, int P, hils_ctensor Kc,
+                       hils_ctensor Vc, int T, const int32_t *cache_len, hils_tensor O, float *lse, void *workspace,
+                       size_t ws_bytes, cudaStream_t stream);
+
+/* Cuts caches to `budget` slots by accumulated weight. A sequence of n = cache_len[b] <=
+ * budget tokens keeps them all. A longer one keeps, per key-value head, the slots [0, A),
+ * the W = params->W newest and, of those between, the budget - A - W with the largest acc
+ * (equal ones: the lower slot; NaN counts as the smallest). A + W <= budget.
+ *   K, V [B, Hk, T, d];  acc [B, Hk, T] float32;  cache_len [B] int32, device (outside
+ *   [0, T]: the nearer end)
+ *   Kout, Vout [B, Hk, budget, d] out: the kept rows in slot order; rows behind the last
+ *   kept one are left as they were, as in acc_out [B, Hk, budget]
+ *   idx [B, Hk, budget] int32 out: each kept row's old slot, -1 behind the last
+ *   len_out [B] int32 out: min(n, budget); may be cache_len
+ * Outputs must not share an address range with K, V or acc (HILS_ERR_INVALID_ARG).
+ *   workspace: hils_workspace_bytes(p, HILS_CALL_CACHE_EVICT, T, budget), zeroed before first use */
+int hils_cache_evict(const hils_params *p, int A, int budget, hils_ctensor K, hils_ctensor V, int T, const float *acc,
+                     const int32_t *cache_len, hils_tensor Kout, hils_tensor Vout, float *acc_out, int32_t *idx,
+                     int32_t *len_out, void *workspace, size_t ws_bytes, cudaStream_t stream);
+
 /* Diagnostic (no counterpart on the pages): evaluates the two FMA-pipe helpers that the
  * tensor-core prefill attend uses instead of MUFU instructions, element by element:
  *   exp2_out[i]  = 2^x[i]  (a fitted degree-5 polynomial; relative error <= 2.4e-7 for
@@ -342,7 +445,8 @@ int hils_selftest_fast_math(const float *x, const float *z, int n, float *exp2_o
                             cudaStream_t stream);
 
 /* Bytes of workspace a call needs for these sizes (Lq = queries per (b, h); C =
- * summarised chunks). Returns 0 for invalid parameters. */
+ * summarised chunks; for the sink, prefix and evict calls as said there). Returns 0 for
+ * invalid parameters. */
 size_t hils_workspace_bytes(const hils_params *p, int call, int Lq, int C);
 
 /* Zeroes a workspace on `stream` (cudaMemsetAsync); needed once after allocation. */
