@@ -39,6 +39,11 @@ int check_sink(const hils_params *p, int A, int64_t rows, float *scale) {
 // Longest key range of a prefill row tile.
 int64_t prefill_keys(const hils_params *p, int A, int Lq) { return (int64_t)p->W + A + (Lq < 256 ? Lq : 256); }
 
+hils_status forward(const hils_params *p, const SinkArgs &a, cudaStream_t s) {
+    hils_status st;
+    return launch_sink_forward_tc(p->dtype, p->d, a, s, &st) ? st : launch_sink_forward_general(p->dtype, p->d, a, s);
+}
+
 struct Carve {  // consecutive 256-byte aligned parts of a workspace
     uint8_t *base;
     size_t used = 0;
@@ -141,7 +146,7 @@ int hils_sink_prefill(const hils_params *p, int A, hils_ctensor Q, int Lq, hils_
         a.part_o = ws.take<float>((size_t)rows * a.slots * p->d);
         a.part_lse = ws.take<float>((size_t)rows * a.slots);
     }
-    HILS_TRY(launch_sink_forward_general(p->dtype, p->d, a, stream));
+    HILS_TRY(forward(p, a, stream));
     if (a.splits == 1) return HILS_OK;
     return launch_sink_combine(p->dtype, p->d, {a.part_o, a.part_lse, rows, a.slots, a.H, Lq, a.O, lse}, stream);
 }
@@ -325,7 +330,7 @@ int hils_prefix_decode(const hils_params *p, hils_ctensor Q, hils_ctensor Kp, hi
     s.slots = a.slots;
     s.part_o = a.part_o;
     s.part_lse = a.part_lse;
-    HILS_TRY(launch_sink_forward_general(p->dtype, p->d, a, stream));
+    HILS_TRY(forward(p, a, stream));
     HILS_TRY(launch_sink_decode(p->dtype, p->d, s, stream));
     return launch_sink_combine(p->dtype, p->d, {a.part_o, a.part_lse, rows, a.slots, a.H, 1, mut(O), lse}, stream);
 }

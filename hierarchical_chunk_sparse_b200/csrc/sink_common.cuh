@@ -69,11 +69,11 @@ inline int sink_prefill_splits(int B, int H, int G, int Lq, int64_t keys, int sm
     const int64_t s = fill < most ? fill : most;
     return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
-// Key splits of a shared prefix of P tokens.
+// Key splits of a shared prefix of P tokens: two for each CTA of one wave over the row tiles.
 inline int sink_prefix_splits(int B, int Hk, int G, int P, int sms) {
     const int nb = 128 / G;
     const int64_t tiles = (int64_t)Hk * ((B + nb - 1) / nb);
-    const int64_t fill = tiles > 0 ? (2 * (int64_t)sms + tiles - 1) / tiles : 1;
+    const int64_t fill = tiles > 0 && tiles < sms ? 2 * (sms / tiles) : 2;
     const int64_t most = P / 256;
     const int64_t s = fill < most ? fill : most;
     return (int)(s < 1 ? 1 : s > 128 ? 128 : s);
@@ -83,6 +83,8 @@ inline size_t sink_part_bytes(int64_t rows, int slots, int d) {
 }
 
 hils_status launch_sink_forward_general(hils_dtype dt, int d, const SinkArgs &a, cudaStream_t s);
+// On the tensor cores; false, and nothing launched, for a type or strides that it cannot take.
+bool launch_sink_forward_tc(hils_dtype dt, int d, const SinkArgs &a, cudaStream_t s, hils_status *st);
 
 // O and lse of every row from its partials: weights exp(lse_s - max) over the row's slots
 // (slots with lse = -inf are skipped).

@@ -1,0 +1,111 @@
+// What the tcgen05 kernels of the window-and-sink calls share: bounded waits, tensor maps
+// of the row tiles, and the masks of a tile's columns.
+#pragma once
+#include "sink_common.cuh"
+#include "tc_common.cuh"
+
+namespace hils {
+namespace tc {
+
+// The CTA's waits. Each is bounded by the global timer; the first one that expires sets
+// the abort flag and bit 0 of the call's status word, after which every wait fails, the
+// roles stop issuing, and the CTA drains what it started and returns.
+struct Pipe {
+    uint32_t bars;                  // shared address of the first mbarrier
+    volatile uint32_t *abort_flag;  // shared
+    uint32_t *status;
+    long long wait_ns;
+
+    __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8u * i; }
+    __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
+        const uint32_t b = bar(i);
+        if (wait_ns > 0) {
+            if (mbar_try_wait(b, parity)) return true;
+            const uint64_t t0 = global_ns();
+            for (int it = 0;; ++it) {
+                if (mbar_try_wait(b, parity)) return true;
+                if ((it & 15) == 15) {
+                    if (*abort_flag) return false;
+                    if ((long long)(global_ns() - t0) > wait_ns) break;
+                }
+            }
+        }
+        *abort_flag = 1u;
+        atomicOr(status, 1u);
+        return false;
+    }
+    // every lane waits; true if all succeeded
+    __device__ __forceinline__ bool wait_warp(int i, uint32_t parity) const {
+        return __all_sync(kFull, wait(i, parity));
+    }
+    __device__ __forceinline__ void arrive(int i) const {
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar(i)) : "memory");
+    }
+    // bounded wait for this CTA's own copies or MMAs while it stops: `uses` phases of barrier i
+    __device__ __forceinline__ void drain(int i, int uses) const {
+        if (uses == 0) return;
+        const uint64_t t0 = global_ns();
+        while (!mbar_try_wait(bar(i), (uint32_t)(uses - 1) & 1u))
+            if ((long long)(global_ns() - t0) > kDrainLimitNs) break;
+    }
+};
+
+__device__ __forceinline__ void tmem_alloc(uint32_t smem_slot, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_slot), "r"(cols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+}
+__device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(cols));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Bit q is set where lo <= c0 + q < hi.
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi, int c0) {
+    const int l = max(lo - c0, 0), h = min(hi - c0, 32);
+    if (h <= l) return 0u;
+    return (0xffffffffu >> (32 - (h - l))) << l;
+}
+
+// The work item of round r for CTA c of n: rounds alternate direction, so that every CTA
+// gets a similar share of the expensive items, which come first.
+__device__ __forceinline__ int item_of_round(int r, int c, int n) { return r * n + ((r & 1) ? (n - 1 - c) : c); }
+
+// A map of a bf16 tensor with extents dims[0] = d elements (contiguous) and three outer
+// dimensions with strides in elements, in boxes of 64 x b1 x b2 x 1 with the 128-byte
+// swizzle; what lies outside the extents reads as zero. False if it cannot be described.
+inline bool make_row_map(CUtensorMap *m, const void *ptr, int d, const int64_t (&dims)[3], const int64_t (&strides)[3],
+                         int b1, int b2) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dm[4] = {(cuuint64_t)d}, st[3];
+    for (int i = 0; i < 3; ++i) {
+        if (dims[i] <= 0 || dims[i] > 0x7fffffffll) return false;
+        dm[i + 1] = (cuuint64_t)dims[i];
+        const int64_t s = dims[i] == 1 ? (int64_t)d : strides[i];  // the stride of one row is of no matter
+        if (s <= 0 || s >= (1ll << 38)) return false;
+        st[i] = (cuuint64_t)s * 2;
+    }
+    const cuuint32_t box[4] = {64u, (cuuint32_t)b1, (cuuint32_t)b2, 1u}, estr[4] = {1u, 1u, 1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dm, st, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Rows of a [B, H, T, d] view: boxes of `rows` rows of `heads` heads.
+inline bool make_view_map(CUtensorMap *m, const View &v, int64_t B, int64_t H, int64_t T, int d, int rows, int heads) {
+    return make_row_map(m, v.ptr, d, {T, H, B}, {v.st, v.sh, v.sb}, rows, heads);
+}
+
+}  // namespace tc
+}  // namespace hils
