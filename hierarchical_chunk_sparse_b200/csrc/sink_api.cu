@@ -191,7 +191,9 @@ int hils_sink_prefill_backward(const hils_params *p, int A, hils_ctensor Q, hils
     a.Dv = Dv;
     a.part = ws.take<float>(part / 4);
     HILS_TRY(launch_sink_dot(p->dtype, p->d, a, Dv, stream));
-    HILS_TRY(launch_sink_backward_general(p->dtype, p->d, a, stream));
+    hils_status st;
+    if (!launch_sink_backward_tc(p->dtype, p->d, a, stream, &st)) st = launch_sink_backward_general(p->dtype, p->d, a, stream);
+    HILS_TRY(st);
     return launch_sink_reduce(p->dtype, p->d, a, false, stream);
 }
 

@@ -174,6 +174,9 @@ __host__ __device__ inline SinkItem sink_item(const SinkBwdArgs &a, int x) {
 
 hils_status launch_sink_dot(hils_dtype dt, int d, const SinkBwdArgs &a, float *Dv, cudaStream_t s);
 hils_status launch_sink_backward_general(hils_dtype dt, int d, const SinkBwdArgs &a, cudaStream_t s);
+// dQ, and dK and dV or their partials, on the tensor cores; false, and nothing launched, for
+// a type or strides that it cannot take.
+bool launch_sink_backward_tc(hils_dtype dt, int d, const SinkBwdArgs &a, cudaStream_t s, hils_status *st);
 hils_status launch_sink_weights_general(hils_dtype dt, int d, const SinkBwdArgs &a, cudaStream_t s);
 // Sums the segments' partials in segment order into dK and dV, or acc_out.
 hils_status launch_sink_reduce(hils_dtype dt, int d, const SinkBwdArgs &a, bool weights, cudaStream_t s);

@@ -51,9 +51,16 @@ enum {
 
 struct FwdTc {
     SinkArgs a;
-    int P, qt, nqb;     // prefill: packed heads, queries of a tile, items per (b, packed heads, split)
+    int P, qt, nqb;     // prefill: packed heads, queries of a tile, row items per (b, packed heads)
     int nb, tiles;      // prefix: sequences of a tile, tiles
     int items, sink_box;
+};
+
+struct PrefixItem {
+    int hk, h, i0;      // key-value head, its first query head, first sequence
+    int split;
+    bool hasB;          // there is a second key range
+    int r0[2], r1[2];   // the key tiles of A's and B's range
 };
 
 template <int D, bool PREFIX>
@@ -67,46 +74,16 @@ struct Smem {
     static constexpr int kBytes = kMisc + 16 + 1024;  // + alignment slack
 };
 
-struct Item {
-    int b, h, hk, i0;   // prefill: batch, first packed head, first query of A; prefix: i0 = first sequence
-    int tA, tB;         // first positions
-    SinkSpan sp;
-    int e0, e1, eA, wB; // entries of this split; A sees entries < eA, B the sinks' and window tiles >= wB
-    int split;
-    bool hasB;          // B has rows
-    int r0[2], r1[2];   // prefix: the key tiles of A's and B's range
-
-    // keys of entry e that tile x multiplies (0: it skips the entry)
-    __device__ __forceinline__ int keys(int x, int e, const SinkArgs &a, int *k0) const {
-        if (e < sp.ns) {
-            *k0 = e * kKeys;
-            return x == 0 || hasB ? min(kKeys, sp.sinks - *k0) : 0;
-        }
-        *k0 = sp.lo + (e - sp.ns) * kKeys;
-        if (x == 0) return e < eA ? min(kKeys, min(sp.hi, tB) - *k0) : 0;
-        return hasB && e - sp.ns >= wB ? min(kKeys, sp.hi - *k0) : 0;
-    }
-    // the last entry that tile x sees (-1: none)
-    __device__ __forceinline__ int last(int x) const {
-        if (x == 0) return min(e1, eA) > e0 ? min(e1, eA) - 1 : -1;
-        if (!hasB) return -1;
-        int l = e1 - 1;
-        if (l >= sp.ns && l - sp.ns < wB) l = min(l, sp.ns - 1);
-        return l >= e0 ? l : -1;
-    }
-};
-
 template <bool PREFIX>
-__device__ __forceinline__ Item decode_item(const FwdTc &f, int j) {
+__device__ __forceinline__ auto decode_item(const FwdTc &f, int j) {
     const SinkArgs &a = f.a;
-    Item it;
-    if (PREFIX) {
+    if constexpr (PREFIX) {
+        PrefixItem it;
         const int pairs = (a.splits + 1) / 2;
         it.split = j % pairs;
         const int u = j / pairs;
         it.i0 = (u % f.tiles) * f.nb;
         it.hk = u / f.tiles;
-        it.b = 0;
         it.h = it.hk * a.G;
         it.hasB = 2 * it.split + 1 < a.splits;
         const int nt = (a.N + kKeys - 1) / kKeys;
@@ -117,27 +94,9 @@ __device__ __forceinline__ Item decode_item(const FwdTc &f, int j) {
             it.r1[x] = x == 0 || it.hasB ? (int)((int64_t)nt * (r + 1) / a.splits) : 0;
         }
         return it;
+    } else {
+        return RowItem<kKeys>(j, a.B, a.H, a.G, f.P, f.qt, f.nqb, a.Lq, a.N, a.W, a.A, a.splits);
     }
-    it.split = j % a.splits;
-    j /= a.splits;
-    const int hp = a.H / f.P, units = a.B * hp;
-    const int qb = f.nqb - 1 - j / units, u = j % units;  // latest queries (most keys) first
-    it.b = u / hp;
-    it.h = (u % hp) * f.P;
-    it.hk = it.h / a.G;
-    it.i0 = qb * 2 * f.qt;
-    it.tA = a.N - a.Lq + it.i0;
-    it.tB = it.tA + f.qt;
-    it.hasB = it.tB < a.N;
-    const int t1 = min(a.N - 1, it.tB + f.qt - 1);
-    it.sp = sink_span(it.tA, t1, a.W, a.A, kKeys);
-    const int nt = it.sp.ns + it.sp.nw;
-    it.e0 = (int)((int64_t)nt * it.split / a.splits);
-    it.e1 = (int)((int64_t)nt * (it.split + 1) / a.splits);
-    it.eA = it.sp.ns + (it.sp.nw > 0 ? (min(it.sp.hi, it.tB) - it.sp.lo + kKeys - 1) / kKeys : 0);
-    const int gone = it.tB - a.W - it.sp.lo - (kKeys - 1);  // >= 0: B sees no key of the first window tile
-    it.wB = it.sp.lo >= a.A && gone >= 0 ? gone / kKeys + 1 : 0;
-    return it;
 }
 
 template <int D, bool PREFIX>
@@ -201,8 +160,8 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
             for (int r = 0; ok; ++r) {
                 const int j = item_of_round(r, cta, G);
                 if (j >= f.items) break;
-                const Item it = decode_item<PREFIX>(f, j);
-                if (PREFIX) {
+                const auto it = decode_item<PREFIX>(f, j);
+                if constexpr (PREFIX) {
                     if (nq[0] > 0 && !(ok = pipe.wait(kBarQfree, (nq[0] - 1) & 1))) break;
                     mbar_expect_tx(pipe.bar(kBarQfull), (uint32_t)(f.nb * a.G) * D * 2);
                     ++nq[0];
@@ -212,8 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                         if (i < n0) load_kv((nv[0] & 1), 0, (it.r0[0] + i) * kKeys, false, it.hk, 0);
                         if (ok && i < n1) load_kv(2 + (nv[1] & 1), 1, (it.r0[1] + i) * kKeys, false, it.hk, 0);
                     }
-                    continue;
-                }
+                } else {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (it.last(x) < 0) continue;
@@ -223,8 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                     tile(sbase + L::kQ + x * L::kTileBytes, &tmQ, kBarQfull + x, it.i0 + x * f.qt, it.h, it.b);
                 }
                 for (int e = it.e0; e < it.e1 && ok; ++e, ++g) {
-                    const bool sink = e < it.sp.ns;
-                    load_kv(g & 1, g & 1, sink ? e * kKeys : it.sp.lo + (e - it.sp.ns) * kKeys, sink, it.hk, it.b);
+                    load_kv(g & 1, g & 1, it.first_key(e), e < it.sp.ns, it.hk, it.b);
+                }
                 }
             }
             // what was started lands before the CTA's memory is released
@@ -273,8 +231,8 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
             for (int r = 0; ok; ++r) {
                 const int j = item_of_round(r, cta, G);
                 if (j >= f.items) break;
-                const Item it = decode_item<PREFIX>(f, j);
-                if (PREFIX) {
+                const auto it = decode_item<PREFIX>(f, j);
+                if constexpr (PREFIX) {
                     if (!(ok = pipe.wait(kBarQfull, r & 1))) break;
                     const int nt = it.r1[x] - it.r0[x];
                     if (nt == 0) {
@@ -286,8 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                         run_tile(2 * x + (c & 1), (c >> 1) & 1, x, c & 1, min(kKeys, a.N - (it.r0[x] + i) * kKeys), i == 0,
                                  i + 1 == nt);
                     ++n;
-                    continue;
-                }
+                } else {
                 const int last = it.last(x);
                 if (last >= 0) {
                     if (!(ok = pipe.wait(kBarQfull + x, nqx & 1))) break;
@@ -296,8 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                 }
                 bool first = true;
                 for (int e = it.e0; e < it.e1 && ok; ++e, ++g) {
-                    int k0;
-                    const int nk = it.keys(x, e, a, &k0), s = g & 1;
+                    const int nk = it.keys(x, e), s = g & 1;
                     const uint32_t par = (g >> 1) & 1;
                     if (nk > 0) {
                         run_tile(s, par, s, par, nk, first, e == last);
@@ -310,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                     }
                 }
                 if (last >= 0) ++n;
+                }
             }
             mma_commit(pipe.bar(kBarDrain + x));  // what was issued completes before TMEM is released
             pipe.drain(kBarDrain + x, 1);
@@ -326,16 +283,21 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
         for (int r = 0; ok; ++r) {
             const int j = item_of_round(r, cta, G);
             if (j >= f.items) break;
-            const Item it = decode_item<PREFIX>(f, j);
+            const auto it = decode_item<PREFIX>(f, j);
             int b, h, i, t;
             bool have;
-            if (PREFIX) {
+            int first_e, end_e;
+            if constexpr (PREFIX) {
+                first_e = it.r0[x];
+                end_e = it.r1[x];
                 b = it.i0 + row / a.G;
                 h = it.h + row % a.G;
                 i = 0;
                 t = a.N;
                 have = row < f.nb * a.G && b < a.B && (x == 0 || it.hasB);
             } else {
+                first_e = it.e0;
+                end_e = it.e1;
                 b = it.b;
                 h = it.h + row / f.qt;
                 i = it.i0 + x * f.qt + row % f.qt;
@@ -344,28 +306,18 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
             }
             float m = -INFINITY, l = 0.f;
             bool any_tile = false;
-            const int first_e = PREFIX ? it.r0[x] : it.e0, end_e = PREFIX ? it.r1[x] : it.e1;
             for (int e = first_e; e < end_e; ++e) {
-                int k0;
-                int n;
-                if (PREFIX) {
-                    k0 = e * kKeys;
-                    n = min(kKeys, a.N - k0);
+                int n, lo, hi, as;  // visible columns: [lo, hi) and [0, as)
+                if constexpr (PREFIX) {
+                    n = hi = min(kKeys, a.N - e * kKeys);
+                    lo = as = 0;
                 } else {
-                    n = it.keys(x, e, a, &k0);
+                    n = it.keys(x, e);
                     if (n <= 0) continue;
-                }
-                any_tile = true;
-                // visible columns: [lo, hi) and [0, as)
-                int lo = 0, hi = n, as = 0;
-                if (!PREFIX) {
-                    hi = min(n, t + 1 - k0);
-                    if (e >= it.sp.ns) {
-                        lo = t - a.W + 1 - k0;
-                        as = min(a.A - k0, hi);
-                    }
+                    it.columns(e, n, t, a.W, &lo, &hi, &as);
                     if (!have) hi = as = 0;
                 }
+                any_tile = true;
                 const bool full = __all_sync(kFull, lo <= 0 && hi == kKeys);
                 if (!(ok = pipe.wait_warp(kBarS + x, c & 1))) break;
                 tc_fence_after();

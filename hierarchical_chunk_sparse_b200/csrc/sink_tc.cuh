@@ -82,6 +82,67 @@ __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int c0) {
 // gets a similar share of the expensive items, which come first.
 __device__ __forceinline__ int item_of_round(int r, int c, int n) { return r * n + ((r & 1) ? (n - 1 - c) : c); }
 
+// Two neighbouring row tiles A and B (P packed heads x qt queries each) of one (b, head
+// pack), and the KT-key tiles that they see: the sinks' first, then the window's.
+template <int KT>
+struct RowItem {
+    int b, h, hk, i0;   // batch, first packed head, its key-value head, first query of A
+    int tA, tB, A;      // first positions, sinks
+    SinkSpan sp;
+    int e0, e1, eA, wB; // entries of this split; A sees entries < eA, B the sinks' and window tiles >= wB
+    int split;
+    bool hasB;          // B has rows
+
+    __device__ __forceinline__ RowItem(int j, int B, int H, int G, int P, int qt, int nqb, int Lq, int N, int W, int A_,
+                                       int splits) {
+        split = j % splits;
+        j /= splits;
+        const int hp = H / P, units = B * hp;
+        const int qb = nqb - 1 - j / units, u = j % units;  // latest queries (most keys) first
+        b = u / hp;
+        h = (u % hp) * P;
+        hk = h / G;
+        i0 = qb * 2 * qt;
+        A = A_;
+        tA = N - Lq + i0;
+        tB = tA + qt;
+        hasB = tB < N;
+        sp = sink_span(tA, min(N - 1, tB + qt - 1), W, A, KT);
+        const int nt = sp.ns + sp.nw;
+        e0 = (int)((int64_t)nt * split / splits);
+        e1 = (int)((int64_t)nt * (split + 1) / splits);
+        eA = sp.ns + (sp.nw > 0 ? (min(sp.hi, tB) - sp.lo + KT - 1) / KT : 0);
+        const int gone = tB - W - sp.lo - (KT - 1);  // >= 0: B sees no key of the first window tile
+        wB = sp.lo >= A && gone >= 0 ? gone / KT + 1 : 0;
+    }
+    __device__ __forceinline__ int first_key(int e) const { return e < sp.ns ? e * KT : sp.lo + (e - sp.ns) * KT; }
+    // keys of entry e that tile x multiplies (0: it skips the entry)
+    __device__ __forceinline__ int keys(int x, int e) const {
+        const int k0 = first_key(e);
+        if (e < sp.ns) return x == 0 || hasB ? min(KT, sp.sinks - k0) : 0;
+        if (x == 0) return e < eA ? min(KT, min(sp.hi, tB) - k0) : 0;
+        return hasB && e - sp.ns >= wB ? min(KT, sp.hi - k0) : 0;
+    }
+    // the last entry that tile x sees (-1: none)
+    __device__ __forceinline__ int last(int x) const {
+        if (x == 0) return min(e1, eA) > e0 ? min(e1, eA) - 1 : -1;
+        if (!hasB) return -1;
+        int l = e1 - 1;
+        if (l >= sp.ns && l - sp.ns < wB) l = min(l, sp.ns - 1);
+        return l >= e0 ? l : -1;
+    }
+    // visible columns of entry e for a row at position t, among n: [*lo, *hi) and [0, *as)
+    __device__ __forceinline__ void columns(int e, int n, int t, int W, int *lo, int *hi, int *as) const {
+        const int k0 = first_key(e);
+        *lo = *as = 0;
+        *hi = min(n, t + 1 - k0);
+        if (e >= sp.ns) {
+            *lo = t - W + 1 - k0;
+            *as = min(A - k0, *hi);
+        }
+    }
+};
+
 // A map of a bf16 tensor with extents dims[0] = d elements (contiguous) and three outer
 // dimensions with strides in elements, in boxes of 64 x b1 x b2 x 1 with the 128-byte
 // swizzle; what lies outside the extents reads as zero. False if it cannot be described.
