@@ -59,7 +59,8 @@ size_t key_ws(const hils_params *p, int Lq, int N, int A, int per_key, SinkBwdAr
     a->B = p->B;
     a->H = p->H;
     a->G = groups(p);
-    sink_key_plan(p->B, p->H / a->G, a->G, Lq, N, clip(p->W, N), clip(A, N), a);
+    sink_key_plan(p->B, p->H / a->G, a->G, Lq, N, clip(p->W, N), clip(A, N),
+                  per_key == 1 && p->dtype == HILS_BF16 ? 2 * kSinkKeys : kSinkKeys, a);
     return sink_align(sink_key_part_floats(*a, per_key) * 4);
 }
 
@@ -227,7 +228,9 @@ int hils_sink_weights(const hils_params *p, int A, hils_ctensor Q, int Lq, hils_
     Carve ws{static_cast<uint8_t *>(workspace)};
     a.status = ws.take<uint32_t>(kSinkStatusBytes / 4);
     a.part = ws.take<float>(part / 4);
-    HILS_TRY(launch_sink_weights_general(p->dtype, p->d, a, stream));
+    hils_status st;
+    if (!launch_sink_weights_tc(p->dtype, p->d, a, stream, &st)) st = launch_sink_weights_general(p->dtype, p->d, a, stream);
+    HILS_TRY(st);
     return launch_sink_reduce(p->dtype, p->d, a, true, stream);
 }
 

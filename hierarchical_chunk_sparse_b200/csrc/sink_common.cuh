@@ -99,8 +99,8 @@ hils_status launch_sink_combine(hils_dtype dt, int d, const SinkCombineArgs &a, 
 
 // ------------------------------------------------------------------ backward and weights
 
-// Key-major items: a block of kSinkKeys keys of one (b, key-value head) and a segment of
-// its steps. Step s covers query rows [i0 + kSinkRows (s % tiles), ..) of group head
+// Key-major items: a block of `keys` keys (kSinkKeys; 256 for bf16 weights) of one (b,
+// key-value head) and a segment of its steps. Step s covers query rows [i0 + kSinkRows (s % tiles), ..) of group head
 // s / tiles, where [i0, i1) are the rows that see a key of the block.
 constexpr int kSinkKeys = 128, kSinkRows = 128;
 
@@ -115,7 +115,7 @@ struct SinkBwdArgs {
     int B, H, G, Lq, N, W, A;
     float scale;
     // key blocks [0, nsink) are cut into seg_s segments each, the others into seg_w
-    int nblk, nsink, seg_s, seg_w;
+    int nblk, nsink, seg_s, seg_w, keys;
     float *part;            // partial sums of blocks with more than one segment
     uint32_t *status = nullptr;
     long long wait_ns = kWaitLimitNs;
@@ -137,9 +137,10 @@ __host__ __device__ inline void sink_rows_of_block(const SinkBwdArgs &a, int j0,
 }
 
 // The division of the key blocks: enough items for every SM, at least eight steps each.
-inline void sink_key_plan(int B, int Hk, int G, int Lq, int N, int W, int A, SinkBwdArgs *a) {
-    a->nblk = (N + kSinkKeys - 1) / kSinkKeys;
-    a->nsink = (A + kSinkKeys - 1) / kSinkKeys;
+inline void sink_key_plan(int B, int Hk, int G, int Lq, int N, int W, int A, int keys, SinkBwdArgs *a) {
+    a->keys = keys;
+    a->nblk = (N + keys - 1) / keys;
+    a->nsink = (A + keys - 1) / keys;
     if (a->nsink > a->nblk) a->nsink = a->nblk;
     auto segments = [&](int blocks, int64_t rows) {
         const int64_t steps = (int64_t)G * ((rows + kSinkRows - 1) / kSinkRows);
@@ -148,7 +149,7 @@ inline void sink_key_plan(int B, int Hk, int G, int Lq, int N, int W, int A, Sin
         return (int)(s < 1 ? 1 : s);
     };
     a->seg_s = segments(a->nsink, Lq);
-    const int64_t wr = (int64_t)W + kSinkKeys;
+    const int64_t wr = (int64_t)W + keys;
     a->seg_w = segments(a->nblk - a->nsink, wr < Lq ? wr : Lq);
 }
 inline int64_t sink_key_items(const SinkBwdArgs &a) {
@@ -157,7 +158,7 @@ inline int64_t sink_key_items(const SinkBwdArgs &a) {
 // Floats of partial sums (`per_key` of each key: 2 d for dK and dV, 1 for weights).
 inline size_t sink_key_part_floats(const SinkBwdArgs &a, int per_key) {
     if (a.seg_s <= 1 && a.seg_w <= 1) return 0;
-    return (size_t)a.B * (a.H / a.G) * sink_key_items(a) * kSinkKeys * per_key;
+    return (size_t)a.B * (a.H / a.G) * sink_key_items(a) * a.keys * per_key;
 }
 
 struct SinkItem {
@@ -177,6 +178,7 @@ hils_status launch_sink_backward_general(hils_dtype dt, int d, const SinkBwdArgs
 // dQ, and dK and dV or their partials, on the tensor cores; false, and nothing launched, for
 // a type or strides that it cannot take.
 bool launch_sink_backward_tc(hils_dtype dt, int d, const SinkBwdArgs &a, cudaStream_t s, hils_status *st);
+bool launch_sink_weights_tc(hils_dtype dt, int d, const SinkBwdArgs &a, cudaStream_t s, hils_status *st);
 hils_status launch_sink_weights_general(hils_dtype dt, int d, const SinkBwdArgs &a, cudaStream_t s);
 // Sums the segments' partials in segment order into dK and dV, or acc_out.
 hils_status launch_sink_reduce(hils_dtype dt, int d, const SinkBwdArgs &a, bool weights, cudaStream_t s);

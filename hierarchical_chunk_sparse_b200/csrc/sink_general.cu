@@ -291,14 +291,14 @@ __global__ void __launch_bounds__(kThr) sink_bwd_kernel(SinkBwdArgs a, int tiles
         s0 = 0;
         s1 = sp.ns + sp.nw;
     } else {
-        // an item's 128-key block in two halves of 64 keys
-        const int half = blockIdx.x % 2, x = (blockIdx.x / 2) % tiles;
-        xb = (blockIdx.x / 2) / tiles;
+        // an item's key block in parts of 64 keys
+        const int parts = a.keys / kT, part = blockIdx.x % parts, x = (blockIdx.x / parts) % tiles;
+        xb = (blockIdx.x / parts) / tiles;
         b = xb / Hk;
         hk = xb % Hk;
         h = 0;
         it = sink_item(a, x);
-        r0 = it.blk * kSinkKeys + half * kT;
+        r0 = it.blk * a.keys + part * kT;
         nrows = max(0, min(kT, a.N - r0));
         if (nrows == 0) return;
         sink_rows_of_block(a, r0, kT, &i0, &ilim);
@@ -373,12 +373,12 @@ __global__ void __launch_bounds__(kThr) sink_bwd_kernel(SinkBwdArgs a, int tiles
         const int rr = 4 * ty + r;
         const float ws = MODE == kModeWeights ? sum16(w[r]) : 0.f;
         if (rr >= nrows) continue;
-        const int64_t item = (int64_t)xb * tiles + (blockIdx.x / 2) % tiles;  // key-major: partial sums' place
-        const int kr = r0 + rr - it.blk * kSinkKeys;
+        const int64_t item = (int64_t)xb * tiles + (blockIdx.x / (a.keys / kT)) % tiles;  // key-major: partial sums' place
+        const int kr = r0 + rr - it.blk * a.keys;
         if (MODE == kModeWeights) {
             if (tx == 0) {
                 const int64_t g = ((int64_t)b * Hk + hk) * a.T + r0 + rr;
-                if (it.nseg > 1) a.part[item * kSinkKeys + kr] = ws;
+                if (it.nseg > 1) a.part[item * a.keys + kr] = ws;
                 else if (seen_key(a, r0 + rr)) a.acc_out[g] = a.acc[g] + ws;
             }
             continue;
@@ -412,14 +412,14 @@ __global__ void __launch_bounds__(256) sink_reduce_kernel(SinkBwdArgs a, int ite
     if (g >= (int64_t)a.B * Hk * a.N) return;
     const int j = (int)(g % a.N);
     const int64_t xb = g / a.N;
-    const int blk = j / kSinkKeys, kr = j % kSinkKeys;
+    const int blk = j / a.keys, kr = j % a.keys;
     const int nseg = blk < a.nsink ? a.seg_s : a.seg_w;
     if (nseg <= 1) return;
     const int64_t first = xb * items + (blk < a.nsink ? blk * a.seg_s : a.nsink * a.seg_s + (blk - a.nsink) * a.seg_w);
     if (WEIGHTS) {
         if (lane != 0 || !seen_key(a, j)) return;
         float s = 0.f;
-        for (int q = 0; q < nseg; ++q) s += a.part[(first + q) * kSinkKeys + kr];
+        for (int q = 0; q < nseg; ++q) s += a.part[(first + q) * a.keys + kr];
         const int64_t at = xb * a.T + j;
         a.acc_out[at] = a.acc[at] + s;
         return;
@@ -471,13 +471,13 @@ hils_status backward(const SinkBwdArgs &a, cudaStream_t s) {
         run(sq, sink_bwd_kernel<kModeDq, T, D>, (int64_t)tiles * a.B * a.H, kThr, bwd_smem<D>(kModeDq), s, a, tiles);
     if (st != HILS_OK) return st;
     const int items = (int)sink_key_items(a);
-    return run(sk, sink_bwd_kernel<kModeDkv, T, D>, 2ll * items * a.B * (a.H / a.G), kThr, bwd_smem<D>(kModeDkv), s, a, items);
+    return run(sk, sink_bwd_kernel<kModeDkv, T, D>, (int64_t)(a.keys / kT) * items * a.B * (a.H / a.G), kThr, bwd_smem<D>(kModeDkv), s, a, items);
 }
 template <typename T, int D>
 hils_status weights(const SinkBwdArgs &a, cudaStream_t s) {
     static KernelSetup setup;
     const int items = (int)sink_key_items(a);
-    return run(setup, sink_bwd_kernel<kModeWeights, T, D>, 2ll * items * a.B * (a.H / a.G), kThr, bwd_smem<D>(kModeWeights), s,
+    return run(setup, sink_bwd_kernel<kModeWeights, T, D>, (int64_t)(a.keys / kT) * items * a.B * (a.H / a.G), kThr, bwd_smem<D>(kModeWeights), s,
                a, items);
 }
 template <typename T, int D>

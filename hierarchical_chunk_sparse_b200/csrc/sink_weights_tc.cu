@@ -1,0 +1,333 @@
+// Accumulated attention weights on the 5th-generation tensor cores (bf16; formulas in
+// sink_common.cuh), key-major: a thread owns a key and adds up exp2(s - lse) over the
+// queries, so that no sum crosses threads.
+//
+// Items are 256 keys of one (b, key-value head), two 128-key tiles A and B, and a segment of
+// their steps; a step is 128 query rows: of one head, or, where only few queries see a block,
+// of several heads of the group (the rows stay full). S^T = K Q^T (M = 128 keys, N = 128
+// rows, K = d) into TMEM, double-buffered per tile; the keys of the next item and the rows of
+// the next steps are loaded meanwhile. The rows' lse (log2 units) are staged in shared memory.
+// The exponentials bound it (16 a cycle and SM on the MUFU against 8192 products): every
+// fourth one is evaluated on the FMA pipe instead.
+// Warps 0-3, 4-7: rows of tile A, B; 8, 9: tcgen05.mma of A, B; 10: TMA and lse.
+// TMEM: S_A [0,128), [128,256); S_B [256,384), [384,512).
+#include "fast_math.cuh"
+#include "sink_tc.cuh"
+
+namespace hils {
+namespace {
+
+using namespace tc;
+
+constexpr int kM = 128, kKeys = 2 * kM, kRows = 128, kStages = 3, kThreads = 384, kMmaWarp = 8, kLoadWarp = 10;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+
+enum {
+    kBarXfull = 0,   // + buffer: the item's keys
+    kBarXfree = 2,   // + buffer (both tiles)
+    kBarYfull = 4,   // + stage: query rows (bytes) and lse (32 arrivals)
+    kBarYfree = 7,   // + stage: both tiles' products, and the 8 warps' reads of lse
+    kBarS = 10,      // + 2 * tile + buffer: S^T written
+    kBarSfree = 14,  // + 2 * tile + buffer: S^T read (4 warps)
+    kBarDrain = 18,  // + tile
+    kNumBars = 20
+};
+template <int D>
+struct Smem {
+    static constexpr int kX = kM * D * 2, kY = kRows * D * 2;
+    static constexpr int kK = 0, kQ = 4 * kX, kL = kQ + kStages * kY;
+    static constexpr int kBars = kL + kStages * kRows * 4, kMisc = kBars + 8 * kNumBars;
+    static constexpr int kBytes = kMisc + 16 + 1024;  // + alignment slack
+};
+struct Args {
+    SinkBwdArgs a;
+    int P, qn;   // heads and queries of each in a step
+    int items;   // of one (b, key-value head)
+};
+struct Item {
+    int xb, b, hk, j0, i0, tiles, s0, s1, nseg, index;
+    int r0[2], r1[2];  // the queries that see a key of A, B
+
+    __device__ __forceinline__ bool valid(int x, int q0, int qn) const { return q0 < r1[x] && q0 + qn > r0[x]; }
+};
+__device__ __forceinline__ Item decode(const Args &f, int j) {
+    const SinkBwdArgs &a = f.a;
+    const int Hk = a.H / a.G, heads = a.B * Hk;
+    Item it;
+    it.xb = j % heads;  // the blocks with most steps (the first ones of a causal range) come first
+    const int y = j / heads;
+    it.b = it.xb / Hk;
+    it.hk = it.xb % Hk;
+    const SinkItem k = sink_item(a, y);
+    it.j0 = k.blk * kKeys;
+    it.nseg = k.nseg;
+    it.index = it.xb * f.items + y;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int j1 = it.j0 + x * kM;
+        it.r0[x] = it.r1[x] = 0;
+        if (j1 < a.N) sink_rows_of_block(a, j1, min(kM, a.N - j1), &it.r0[x], &it.r1[x]);
+    }
+    const bool hasA = it.r0[0] < it.r1[0], hasB = it.r0[1] < it.r1[1];
+    it.i0 = hasA ? it.r0[0] : it.r0[1];
+    const int i1 = hasB ? max(it.r1[1], hasA ? it.r1[0] : 0) : it.r1[0];
+    it.tiles = hasA || hasB ? (i1 - it.i0 + f.qn - 1) / f.qn : 0;
+    const int64_t steps = (int64_t)(a.G / f.P) * it.tiles;
+    it.s0 = (int)(steps * k.seg / k.nseg);
+    it.s1 = (int)(steps * (k.seg + 1) / k.nseg);
+    return it;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
+                                                                      const __grid_constant__ CUtensorMap tmK, Args f,
+                                                                      int total) {
+    extern __shared__ uint8_t smem_raw[];
+    using L = Smem<D>;
+    constexpr int kBlocks = D / 64, kBlk = kM * 128;
+    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    const SinkBwdArgs &a = f.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t sbase = smem_u32(smem);
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + L::kMisc);
+    float *lse = reinterpret_cast<float *>(smem + L::kL);
+    const Pipe pipe{sbase + L::kBars, misc + 1, a.status, a.wait_ns};
+    const int G = gridDim.x, cta = blockIdx.x;
+
+    if (tid == 0) {
+        for (int i = 0; i < kNumBars; ++i) {
+            uint32_t cnt = 1;
+            if (i == kBarXfree || i == kBarXfree + 1) cnt = 2;
+            if (i >= kBarYfull && i < kBarYfull + kStages) cnt = 33;
+            if (i >= kBarYfree && i < kBarYfree + kStages) cnt = 10;
+            if (i >= kBarSfree && i < kBarSfree + 4) cnt = 4;
+            mbar_init(pipe.bar(i), cnt);
+        }
+        misc[1] = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (warp == kMmaWarp) tmem_alloc(sbase + L::kMisc, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+
+    if (warp == kLoadWarp) {
+        int n = 0, g = 0;  // items with steps, steps
+        bool ok = true;
+        for (int r = 0; ok; ++r) {
+            const int j = item_of_round(r, cta, G);
+            if (j >= total) break;
+            const Item it = decode(f, j);
+            if (it.s0 >= it.s1) continue;
+            const int xb = n & 1;
+            if (n >= 2 && !(ok = pipe.wait_warp(kBarXfree + xb, ((n >> 1) - 1) & 1))) break;
+            if (lane == 0) {
+                mbar_expect_tx(pipe.bar(kBarXfull + xb), 2 * L::kX);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)  // B's keys may lie behind the last one: zeros
+#pragma unroll
+                    for (int c = 0; c < kBlocks; ++c)
+                        tma_load_4d(sbase + L::kK + (2 * xb + x) * L::kX + c * kBlk, &tmK, pipe.bar(kBarXfull + xb), c * 64,
+                                    it.j0 + x * kM, it.hk, it.b);
+            }
+            ++n;
+            float sc[4];  // lse of rows lane + 32 m of the next step
+            auto scalars = [&](int s) {
+                const int h0 = it.hk * a.G + s / it.tiles * f.P, q0 = it.i0 + (s % it.tiles) * f.qn;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int row = lane + 32 * m, i = q0 + row % f.qn;
+                    float v = -INFINITY;
+                    if (i < a.Lq) v = __ldg(a.lse + ((int64_t)it.b * a.H + h0 + row / f.qn) * a.Lq + i);
+                    sc[m] = v == -INFINITY ? INFINITY : v * kLog2e;  // nothing seen: exp2(s - inf) = 0
+                }
+            };
+            scalars(it.s0);
+            for (int s = it.s0; s < it.s1; ++s, ++g) {
+                const int st = g % kStages;
+                if (g >= kStages && !(ok = pipe.wait_warp(kBarYfree + st, (g / kStages - 1) & 1))) break;
+                if (lane == 0) {
+                    mbar_expect_tx(pipe.bar(kBarYfull + st), L::kY);
+#pragma unroll
+                    for (int c = 0; c < kBlocks; ++c)
+                        tma_load_4d(sbase + L::kQ + st * L::kY + c * kBlk, &tmQ, pipe.bar(kBarYfull + st), c * 64,
+                                    it.i0 + (s % it.tiles) * f.qn, it.hk * a.G + s / it.tiles * f.P, it.b);
+                }
+#pragma unroll
+                for (int m = 0; m < 4; ++m) lse[st * kRows + lane + 32 * m] = sc[m];
+                pipe.arrive(kBarYfull + st);
+                if (s + 1 < it.s1) scalars(s + 1);
+            }
+        }
+        if (lane == 0) {
+            for (int x = 0; x < 2; ++x) pipe.drain(kBarXfull + x, n > x ? (n - x + 1) / 2 : 0);
+            for (int s = 0; s < kStages; ++s) pipe.drain(kBarYfull + s, g > s ? (g - s + kStages - 1) / kStages : 0);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+        const int x = warp - kMmaWarp;
+        if (lane == 0) {
+            int n = 0, g = 0, c = 0;  // items with steps, steps, steps of x
+            bool ok = true;
+            for (int r = 0; ok; ++r) {
+                const int j = item_of_round(r, cta, G);
+                if (j >= total) break;
+                const Item it = decode(f, j);
+                if (it.s0 >= it.s1) continue;
+                const int xb = n & 1;
+                const uint32_t kb = sbase + L::kK + (2 * xb + x) * L::kX;
+                if (!(ok = pipe.wait(kBarXfull + xb, (n >> 1) & 1))) break;
+                for (int s = it.s0; s < it.s1; ++s, ++g) {
+                    const int st = g % kStages;
+                    if (!(ok = pipe.wait(kBarYfull + st, (g / kStages) & 1))) break;
+                    if (!it.valid(x, it.i0 + (s % it.tiles) * f.qn, f.qn)) {
+                        pipe.arrive(kBarYfree + st);
+                        continue;
+                    }
+                    const int sb = 2 * x + (c & 1);
+                    if (c >= 2 && !(ok = pipe.wait(kBarSfree + sb, ((c >> 1) - 1) & 1))) break;
+                    tc_fence_after();
+                    const uint32_t qb = sbase + L::kQ + st * L::kY;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t o = (k >> 2) * kBlk + (k & 3) * 32;
+                        mma_ss(tmem + sb * 128, smem_desc(kb + o, 16, 1024), smem_desc(qb + o, 16, 1024),
+                               idesc_bf16(kM, kRows, false), k > 0);
+                    }
+                    mma_commit(pipe.bar(kBarS + sb));
+                    mma_commit(pipe.bar(kBarYfree + st));
+                    ++c;
+                }
+                if (!ok) break;
+                mma_commit(pipe.bar(kBarXfree + xb));
+                ++n;
+            }
+            mma_commit(pipe.bar(kBarDrain + x));
+            pipe.drain(kBarDrain + x, 1);
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        const int x = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        const float scale2 = a.scale * kLog2e;
+        const int off = a.N - a.Lq, Hk = a.H / a.G;
+        bool ok = true;
+        int g = 0, c = 0;
+        for (int r = 0; ok; ++r) {
+            const int j = item_of_round(r, cta, G);
+            if (j >= total) break;
+            const Item it = decode(f, j);
+            const int key = it.j0 + x * kM + row;
+            float w = 0.f;
+            for (int s = it.s0; s < it.s1; ++s, ++g) {
+                const int st = g % kStages, q0 = it.i0 + (s % it.tiles) * f.qn;
+                if (!(ok = pipe.wait_warp(kBarYfull + st, (g / kStages) & 1))) break;
+                if (!it.valid(x, q0, f.qn)) {
+                    if (lane == 0) pipe.arrive(kBarYfree + st);
+                    continue;
+                }
+                // queries of each head that see this key
+                const int lo = key - off - q0, end = min(f.qn, a.Lq - q0);
+                const int hi = key < a.A ? end : min(end, (int)min((int64_t)key + a.W - off - q0, (int64_t)kRows));
+                const bool full = __all_sync(kFull, lo <= 0 && hi == f.qn);
+                const int sb = 2 * x + (c & 1);
+                if (!(ok = pipe.wait_warp(kBarS + sb, (c >> 1) & 1))) break;
+                tc_fence_after();
+                const uint32_t s_col = tmem + lanes + sb * 128;
+                const float *lr = lse + st * kRows;
+                float z0 = 0.f, z1 = 0.f, z2 = 0.f, z3 = 0.f;
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t mk = kFull;
+                    if (!full) {
+                        mk = range_bits(lo, hi, (ch * 32) & (f.qn - 1));
+                        if (f.qn == 16) mk |= mk << 16;
+                        if (!__any_sync(kFull, mk != 0)) continue;
+                    }
+                    uint32_t v[32];
+                    tmem_ld32(s_col + ch * 32, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 32; q += 4) {
+                        const float4 L4 = *reinterpret_cast<const float4 *>(lr + ch * 32 + q);
+                        float e[4] = {fmaf(__uint_as_float(v[q]), scale2, -L4.x), fmaf(__uint_as_float(v[q + 1]), scale2, -L4.y),
+                                      fmaf(__uint_as_float(v[q + 2]), scale2, -L4.z),
+                                      fmaf(__uint_as_float(v[q + 3]), scale2, -L4.w)};
+                        if (!full) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) e[k] = (mk >> (q + k)) & 1u ? e[k] : -INFINITY;
+                        }
+                        z0 += ex2(e[0]);
+                        z1 += ex2(e[1]);
+                        z2 += ex2(e[2]);
+                        z3 += exp2_fma(e[3]);
+                    }
+                }
+                w += (z0 + z1) + (z2 + z3);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    pipe.arrive(kBarSfree + sb);
+                    pipe.arrive(kBarYfree + st);
+                }
+                ++c;
+            }
+            if (!ok) break;
+            if (key >= a.N) continue;
+            if (it.nseg > 1) {
+                a.part[(int64_t)it.index * kKeys + x * kM + row] = w;
+            } else {
+                int k0, k1;
+                sink_rows_of_block(a, key, 1, &k0, &k1);
+                const int64_t at = ((int64_t)it.b * Hk + it.hk) * a.T + key;
+                if (k0 < k1) a.acc_out[at] = a.acc[at] + w;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_free(tmem, kTmemCols);
+    }
+}
+
+template <int D>
+hils_status run(const Args &f, const CUtensorMap (&m)[2], int total, cudaStream_t s) {
+    static KernelSetup setup;
+    int per_sm = 0;
+    const auto k = sink_weights_tc_kernel<D>;
+    const hils_status st = kernel_setup(setup, (const void *)k, kThreads, Smem<D>::kBytes, &per_sm);
+    if (st != HILS_OK) return st;
+    if (per_sm < 1) return HILS_ERR_CUDA;
+    const int sms = device_sm_count();
+    k<<<total < sms ? total : sms, kThreads, Smem<D>::kBytes, s>>>(m[0], m[1], f, total);
+    return record_cuda_error(cudaGetLastError());
+}
+
+}  // namespace
+
+bool launch_sink_weights_tc(hils_dtype dt, int d, const SinkBwdArgs &a, cudaStream_t s, hils_status *st) {
+    if (dt != HILS_BF16 || a.N == 0 || a.keys != kKeys) return false;
+    const int Hk = a.H / a.G;
+    Args f{};
+    f.a = a;
+    // few queries: several heads of the group share a step
+    const int64_t see = (int64_t)a.W + kKeys;  // queries that see a block of the window
+    const int rows = a.A == 0 && see < a.Lq ? (int)see : a.Lq;
+    f.P = 1;
+    while (f.P < 8 && a.G % (2 * f.P) == 0 && rows * 2 * f.P <= kRows) f.P *= 2;
+    f.qn = kRows / f.P;
+    f.items = (int)sink_key_items(a);
+    const int64_t total = (int64_t)f.items * a.B * Hk;
+    if (total > 0x7fffffffll - 1024) return false;
+    CUtensorMap m[2];
+    if (!make_view_map(&m[0], a.Q, a.B, a.H, a.Lq, d, f.qn, f.P) || !make_view_map(&m[1], a.K, a.B, Hk, a.N, d, kM, 1))
+        return false;
+    *st = d == 64 ? run<64>(f, m, (int)total, s) : run<128>(f, m, (int)total, s);
+    return true;
+}
+
+}  // namespace hils
