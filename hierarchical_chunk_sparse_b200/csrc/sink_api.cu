@@ -65,8 +65,8 @@ size_t key_ws(const hils_params *p, int Lq, int N, int A, int per_key, SinkBwdAr
 }
 
 struct DecodePlan {
-    int splits, prefix_splits;
-    int64_t keys;
+    int ctas, prefix_splits;
+    int64_t keys, segs;  // longest visible range of a cache; segments of the CTAs' shares
     size_t bytes;
 };
 DecodePlan decode_plan(const hils_params *p, int64_t T, int64_t A, int64_t P, bool prefix, bool acc) {
@@ -74,11 +74,27 @@ DecodePlan decode_plan(const hils_params *p, int64_t T, int64_t A, int64_t P, bo
     const int Hk = p->H / groups(p), sms = device_sm_count();
     const int64_t rows = (int64_t)p->B * p->H;
     d.keys = prefix ? T : (T < A + p->W ? T : A + p->W);
-    d.splits = sink_decode_splits(p->B, Hk, d.keys, sms);
     d.prefix_splits = prefix ? sink_prefix_splits(p->B, Hk, groups(p), (int)P, sms) : 0;
-    d.bytes = kSinkStatusBytes + sink_part_bytes(rows, d.splits + d.prefix_splits, p->d) + sink_align(rows * 4) +
+    d.ctas = sink_decode_ctas(p->dtype, p->B, Hk, d.keys, sms);
+    d.segs = d.ctas + (int64_t)p->B * Hk;
+    d.bytes = kSinkStatusBytes + sink_align((size_t)p->B * Hk * 4) + sink_part_bytes(rows, d.prefix_splits, p->d) +
+              sink_part_bytes(d.segs * groups(p), 1, p->d) + sink_align(rows * 4) +
               (acc ? sink_align((size_t)rows * d.keys * 4) : 0);
     return d;
+}
+
+// The decode kernel's parts of the workspace; the status word stays in front.
+void decode_space(const hils_params *p, const DecodePlan &plan, Carve &ws, float *lse, SinkDecodeArgs *a) {
+    const size_t rows = (size_t)p->B * p->H, segs = (size_t)plan.segs * a->G;
+    ws.take<uint32_t>(kSinkStatusBytes / 4);
+    a->counters = ws.take<int>(rows / a->G);
+    a->slots = plan.prefix_splits;
+    a->part_o = ws.take<float>(rows * a->slots * p->d);
+    a->part_lse = ws.take<float>(rows * a->slots);
+    a->seg_o = ws.take<float>(segs * p->d);
+    a->seg_lse = ws.take<float>(segs);
+    float *row_lse = ws.take<float>(rows);
+    a->lse = lse ? lse : row_lse;
 }
 
 }  // namespace
@@ -256,6 +272,7 @@ int hils_sink_decode(const hils_params *p, int A, hils_ctensor Q, hils_ctensor K
     a.Q = view(Q);
     a.K = view(Kc);
     a.V = view(Vc);
+    a.O = mut(O);
     a.cache_len = cache_len;
     a.B = p->B;
     a.H = p->H;
@@ -264,20 +281,14 @@ int hils_sink_decode(const hils_params *p, int A, hils_ctensor Q, hils_ctensor K
     a.W = clip(p->W, T);
     a.A = clip(A, T);
     a.scale = scale;
-    a.splits = a.slots = plan.splits;
     Carve ws{static_cast<uint8_t *>(workspace)};
-    ws.take<uint32_t>(kSinkStatusBytes / 4);
-    a.part_o = ws.take<float>((size_t)rows * a.slots * p->d);
-    a.part_lse = ws.take<float>((size_t)rows * a.slots);
-    float *row_lse = ws.take<float>(rows);
+    decode_space(p, plan, ws, lse, &a);
     if (acc) {
         a.logits = ws.take<float>((size_t)rows * plan.keys);
         a.logit_stride = plan.keys;
     }
-    if (!lse) lse = row_lse;
-    HILS_TRY(launch_sink_decode(p->dtype, p->d, a, stream));
-    HILS_TRY(launch_sink_combine(p->dtype, p->d, {a.part_o, a.part_lse, rows, a.slots, a.H, 1, mut(O), lse}, stream));
-    return acc ? launch_sink_decode_acc(a, lse, acc, acc_out, stream) : HILS_OK;
+    HILS_TRY(launch_sink_decode(p->dtype, p->d, a, plan.ctas, stream));
+    return acc ? launch_sink_decode_acc(a, a.lse, acc, acc_out, stream) : HILS_OK;
 }
 
 int hils_prefix_decode(const hils_params *p, hils_ctensor Q, hils_ctensor Kp, hils_ctensor Vp, int P, hils_ctensor Kc,
@@ -298,46 +309,41 @@ int hils_prefix_decode(const hils_params *p, hils_ctensor Q, hils_ctensor Kp, hi
     if (rows == 0) return HILS_OK;
     const DecodePlan plan = decode_plan(p, T, 0, P, true, false);
     HILS_TRY(check_workspace(workspace, ws_bytes, plan.bytes));
+    SinkDecodeArgs s{};
+    s.Q = view(Q);
+    s.K = view(Kc);
+    s.V = view(Vc);
+    s.O = mut(O);
+    s.cache_len = cache_len;
+    s.B = p->B;
+    s.H = p->H;
+    s.G = groups(p);
+    s.T = T;
+    s.W = T;
+    s.A = 0;
+    s.scale = scale;
     Carve ws{static_cast<uint8_t *>(workspace)};
+    decode_space(p, plan, ws, lse, &s);
     SinkArgs a{};
-    a.status = ws.take<uint32_t>(kSinkStatusBytes / 4);
-    a.Q = view(Q);
+    a.status = static_cast<uint32_t *>(workspace);
+    a.Q = s.Q;
     a.K = view(Kp);
     a.V = view(Vp);
     a.B = p->B;
     a.H = p->H;
-    a.G = groups(p);
+    a.G = s.G;
     a.Lq = 1;
     a.N = P;
     a.W = P;
     a.A = 0;
     a.scale = scale;
     a.prefix = 1;
-    a.splits = plan.prefix_splits;
-    a.slots = plan.splits + plan.prefix_splits;
-    a.part_o = ws.take<float>((size_t)rows * a.slots * p->d);
-    a.part_lse = ws.take<float>((size_t)rows * a.slots);
+    a.splits = a.slots = s.slots;
+    a.part_o = const_cast<float *>(s.part_o);
+    a.part_lse = const_cast<float *>(s.part_lse);
     a.wait_ns = work_wait_ns(p->flags);
-    SinkDecodeArgs s{};
-    s.Q = view(Q);
-    s.K = view(Kc);
-    s.V = view(Vc);
-    s.cache_len = cache_len;
-    s.B = p->B;
-    s.H = p->H;
-    s.G = a.G;
-    s.T = T;
-    s.W = T;
-    s.A = 0;
-    s.scale = scale;
-    s.splits = plan.splits;
-    s.slot0 = a.splits;
-    s.slots = a.slots;
-    s.part_o = a.part_o;
-    s.part_lse = a.part_lse;
     HILS_TRY(forward(p, a, stream));
-    HILS_TRY(launch_sink_decode(p->dtype, p->d, s, stream));
-    return launch_sink_combine(p->dtype, p->d, {a.part_o, a.part_lse, rows, a.slots, a.H, 1, mut(O), lse}, stream);
+    return launch_sink_decode(p->dtype, p->d, s, plan.ctas, stream);
 }
 
 int hils_cache_evict(const hils_params *p, int A, int budget, hils_ctensor K, hils_ctensor V, int T, const float *acc,

@@ -187,11 +187,20 @@ hils_status launch_sink_reduce(hils_dtype dt, int d, const SinkBwdArgs &a, bool 
 
 struct SinkDecodeArgs {
     View Q, K, V;
+    MutView O;
+    float *lse;                // [B, H]
     const int32_t *cache_len;  // [B]
     int B, H, G, T, W, A;      // W, A <= T
     float scale;
-    int splits, slot0, slots;  // this call's partials are slots slot0 .. slot0 + splits - 1
-    float *part_o, *part_lse;  // rows (b, h)
+    View Kp, Vp;               // P shared tokens before each sequence's own, read per sequence
+    int P = 0;
+    // partial results of rows (b, h) from another kernel: part_o [rows][slots][d], part_lse [rows][slots]
+    const float *part_o, *part_lse;
+    int slots = 0;
+    // this kernel's own: of CTA c's share of row r = (b, hk), head g, at (c + r) * G + g (a
+    // staircase: no two pairs (c, r) that meet have the same sum)
+    float *seg_o, *seg_lse;
+    int *counters;             // [B * Hk] arrivals, zero before and after the call
     float *logits;             // with acc: [B, H, logit_stride] scaled logits in log2 units, by visible order
     int64_t logit_stride;
 };
@@ -200,8 +209,8 @@ __host__ __device__ inline void sink_visible(int n, int W, int A, int *sinks, in
     *lo = n > W ? n - W : 0;
     *sinks = A < *lo ? A : *lo;
 }
-int sink_decode_splits(int B, int Hk, int64_t keys, int sms);
-hils_status launch_sink_decode(hils_dtype dt, int d, const SinkDecodeArgs &a, cudaStream_t s);
+int sink_decode_ctas(hils_dtype dt, int B, int Hk, int64_t keys, int sms);
+hils_status launch_sink_decode(hils_dtype dt, int d, const SinkDecodeArgs &a, int ctas, cudaStream_t s);
 // acc_out[b, hk, j] = acc[b, hk, j] + sum over the group's heads of p_j, for the visible
 // slots j, from the call's logits and the rows' lse [B, H].
 hils_status launch_sink_decode_acc(const SinkDecodeArgs &a, const float *lse, const float *acc, float *acc_out,

@@ -1,96 +1,515 @@
-// One query per sequence over the visible slots of its cache (formulas in sink_common.cuh):
-// the slots are cut into splits, one CTA each, whose partial results meet in the combine.
+// One query per sequence over the visible slots of its cache (formulas in sink_common.cuh).
 #include "sink_common.cuh"
 
 namespace hils {
 namespace {
 
-constexpr int kThr = 128, kWarps = kThr / 32;
+constexpr int kThr = 128, kWarps = kThr / 32, kStages = 3;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+template <typename T>
+constexpr int tile_keys() { return sizeof(T) == 2 ? 32 : 16; }
 template <typename T, int D>
-__global__ void __launch_bounds__(kThr) sink_decode_kernel(SinkDecodeArgs a) {
-    constexpr int kE = D / 32;  // elements of a row per lane
-    const int Hk = a.H / a.G;
-    const int split = blockIdx.x % a.splits, bk = blockIdx.x / a.splits;
-    const int b = bk / Hk, hk = bk % Hk;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int n = min(max(__ldg(a.cache_len + b), 0), a.T);
-    int sinks, lo;
-    sink_visible(n, a.W, a.A, &sinks, &lo);
-    const int nvis = sinks + n - lo;
-    const int v0 = (int)((int64_t)nvis * split / a.splits), v1 = (int)((int64_t)nvis * (split + 1) / a.splits);
-    __shared__ float sm[kWarps][kMaxGroupHeads], sl[kWarps][kMaxGroupHeads], so[kWarps][kMaxGroupHeads][D];
-    float q[kMaxGroupHeads][kE], o[kMaxGroupHeads][kE], m[kMaxGroupHeads], l[kMaxGroupHeads];
-    const float scale2 = a.scale * 1.4426950408889634f;
-#pragma unroll
-    for (int g = 0; g < kMaxGroupHeads; ++g) {
-        m[g] = -INFINITY;
-        l[g] = 0.f;
-        const T *qp = static_cast<const T *>(a.Q.ptr) + b * a.Q.sb + (hk * a.G + min(g, a.G - 1)) * a.Q.sh;
-#pragma unroll
-        for (int e = 0; e < kE; e += 2) {
-            const float2 v = load2(qp + lane * kE + e);
-            q[g][e] = v.x;
-            q[g][e + 1] = v.y;
-            o[g][e] = o[g][e + 1] = 0.f;
+constexpr int tile_bytes() { return tile_keys<T>() * D * (int)sizeof(T); }  // of K, and of V
+template <typename T, int D>
+constexpr int decode_smem() {
+    return kWarps * kStages * 2 * tile_bytes<T, D>() + kWarps * kMaxGroupHeads * (D + 2) * 4 + kMaxGroupHeads * (D + 16) * 4;
+}
+
+// What a sequence sees, in order: the shared prefix, the sinks, the window.
+struct Visible {
+    int n, prefix, sinks, lo;  // n in all
+    int tiles;
+};
+template <int KT>
+__device__ __forceinline__ Visible visible(const SinkDecodeArgs &a, int b) {
+    Visible v;
+    const int len = min(max(__ldg(a.cache_len + b), 0), a.T);
+    sink_visible(len, a.W, a.A, &v.sinks, &v.lo);
+    v.prefix = a.P;
+    v.n = a.P + v.sinks + len - v.lo;
+    v.tiles = max(1, (v.n + KT - 1) / KT);  // an empty row still gets its outputs
+    return v;
+}
+
+// A place in the flattened tiles of all (b, key-value head) rows.
+template <int KT>
+struct Place {
+    int b, hk, k;  // tile k of row (b, hk)
+    Visible v;
+    __device__ __forceinline__ void advance(const SinkDecodeArgs &a, int Hk, int by) {
+        k += by;
+        while (k >= v.tiles && b < a.B) {
+            k -= v.tiles;
+            if (++hk == Hk) {
+                hk = 0;
+                if (++b < a.B) v = visible<KT>(a, b);
+            }
         }
     }
-    for (int v = v0 + warp; v < v1; v += kWarps) {
-        const int64_t j = v < sinks ? v : lo + (v - sinks);
-        const T *kp = static_cast<const T *>(a.K.ptr) + b * a.K.sb + hk * a.K.sh + j * a.K.st + lane * kE;
-        const T *vp = static_cast<const T *>(a.V.ptr) + b * a.V.sb + hk * a.V.sh + j * a.V.st + lane * kE;
-        float k[kE], u[kE];
+};
+
+// Tiles of all rows, and the place of tile `at` (every lane of the warp).
+template <int KT>
+__device__ int64_t all_tiles(const SinkDecodeArgs &a, int Hk) {
+    int64_t t = 0;
+    for (int b = threadIdx.x % 32; b < a.B; b += 32) t += visible<KT>(a, b).tiles;
 #pragma unroll
-        for (int e = 0; e < kE; e += 2) {
-            const float2 x = load2(kp + e), y = load2(vp + e);
-            k[e] = x.x;
-            k[e + 1] = x.y;
-            u[e] = y.x;
-            u[e + 1] = y.y;
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(kFull, t, o);
+    return t * Hk;
+}
+template <int KT>
+__device__ Place<KT> find_tile(const SinkDecodeArgs &a, int Hk, int64_t at) {
+    const int lane = threadIdx.x % 32;
+    int64_t before = 0;
+    for (int b0 = 0;; b0 += 32) {
+        int64_t t = b0 + lane < a.B ? (int64_t)visible<KT>(a, b0 + lane).tiles * Hk : 0, sum = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(kFull, sum, o);
+            if (lane >= o) sum += x;
         }
+        const unsigned hit = __ballot_sync(kFull, before + sum > at);
+        if (hit == 0u && b0 + 32 < a.B) {
+            before += __shfl_sync(kFull, sum, 31);
+            continue;
+        }
+        const int l = hit ? __ffs(hit) - 1 : 31;
+        before += __shfl_sync(kFull, sum - t, l);
+        Place<KT> p;
+        p.b = min(b0 + l, a.B - 1);
+        p.v = visible<KT>(a, p.b);
+        const int64_t in = at - before;
+        p.hk = (int)(in / p.v.tiles);
+        p.k = (int)(in % p.v.tiles);
+        return p;
+    }
+}
+
+// The slots of one tile into a warp's stage, K then V: 16-byte unit u of row r at unit
+// u ^ (r % 8); zeros for rows behind the last visible one.
+template <typename T, int D, int KT>
+__device__ __forceinline__ void load_kv(const SinkDecodeArgs &a, const Place<KT> &p, uint8_t *dst) {
+    constexpr int kU = D * (int)sizeof(T) / 16, kPer = 32 / kU == 0 ? 1 : 32 / kU, kRounds = KT / kPer;
+    static_assert(kU <= 32, "a row is one round of the warp at most");
+    const int lane = threadIdx.x % 32, u = lane % kU, r0 = lane / kU;
+    const int v0 = p.k * KT;
+    const T *kc = static_cast<const T *>(a.K.ptr) + p.b * a.K.sb + p.hk * a.K.sh;
+    const T *vc = static_cast<const T *>(a.V.ptr) + p.b * a.V.sb + p.hk * a.V.sh;
+#pragma unroll 4
+    for (int i = 0; i < kRounds; ++i) {
+        const int r = i * kPer + r0;
+        int v = v0 + r;
+        const bool in = v < p.v.n;
+        const T *k = static_cast<const T *>(a.Q.ptr), *w = k;  // not read
+        if (v < p.v.prefix) {
+            k = static_cast<const T *>(a.Kp.ptr) + p.hk * a.Kp.sh + v * a.Kp.st;
+            w = static_cast<const T *>(a.Vp.ptr) + p.hk * a.Vp.sh + v * a.Vp.st;
+        } else if (in) {
+            v -= p.v.prefix;
+            const int64_t j = v < p.v.sinks ? v : p.v.lo + (v - p.v.sinks);
+            k = kc + j * a.K.st;
+            w = vc + j * a.V.st;
+        }
+        const int at = r * (kU * 16) + ((u ^ (r & 7)) * 16);
+        cp_async16_zfill(dst + at, reinterpret_cast<const uint8_t *>(k) + u * 16, in);
+        cp_async16_zfill(dst + tile_bytes<T, D>() + at, reinterpret_cast<const uint8_t *>(w) + u * 16, in);
+    }
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {  // an 8 x 8 matrix of 16-bit elements
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float max8(float v) {  // over the lanes of equal lane % 4
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+__device__ __forceinline__ float sum8(float v) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// One warp's running softmax of a group's heads over its tiles: bf16 with mma.sync, the up to
+// eight heads as the N of S^T = K Q^T and O^T = V^T P^T (a decode step reads each key once and
+// is bound by that; tcgen05's 128 rows would be 15/16 padding).
+template <typename T, int D>
+struct Rows;
+
+template <int D>
+struct Rows<bf16, D> {
+    uint32_t q[D / 16][2];  // Q^T fragments of head lane / 4
+    float o[D / 16][4];     // O^T: dims lane / 4 (+ 8) of each 16, heads 2 (lane % 4) + {0, 1}
+    float m[2], l[2];       // of those heads; l of this lane's keys only
+
+    __device__ __forceinline__ void start(const SinkDecodeArgs &a, int b, int hk, float *) {
+        const int lane = threadIdx.x % 32, g = lane / 4;
+        const bf16 *p = static_cast<const bf16 *>(a.Q.ptr) + b * a.Q.sb + (int64_t)(hk * a.G + min(g, a.G - 1)) * a.Q.sh;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(p + s * 16 + (lane % 4) * 2);
+            q[s][0] = g < a.G ? __ldg(w) : 0u;
+            q[s][1] = g < a.G ? __ldg(w + 4) : 0u;
+        }
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) o[s][0] = o[s][1] = o[s][2] = o[s][3] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+    }
+    __device__ __forceinline__ void tile(const SinkDecodeArgs &a, const Place<32> &p, const uint8_t *stage, float scale2,
+                                         float *) {
+        const int lane = threadIdx.x % 32, id = lane / 8;
+        const uint32_t kb = (uint32_t)__cvta_generic_to_shared(stage), vb = kb + tile_bytes<bf16, D>();
+        float s[2][4];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+            s[mt][0] = s[mt][1] = s[mt][2] = s[mt][3] = 0.f;
+            const int r = mt * 16 + (lane & 7) + (id & 1) * 8;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t f[4];
+                ldsm4(f, kb + r * (D * 2) + (((2 * k + (id >> 1)) ^ (r & 7)) * 16));
+                mma16816(s[mt], f, q[k][0], q[k][1]);
+            }
+        }
+        const int left = p.v.n - p.k * 32;  // visible slots from this tile's first
+        float mt2[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = mt * 16 + lane / 4 + (e >> 1) * 8;
+                s[mt][e] = r < left ? s[mt][e] * scale2 : -INFINITY;
+                mt2[e & 1] = fmaxf(mt2[e & 1], s[mt][e]);
+            }
+        if (a.logits) {
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = mt * 16 + lane / 4 + (e >> 1) * 8, g = 2 * (lane % 4) + (e & 1);
+                    if (r < left && g < a.G)
+                        a.logits[((int64_t)p.b * a.H + p.hk * a.G + g) * a.logit_stride + p.k * 32 + r] = s[mt][e];
+                }
+        }
+        float f[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float mx = fmaxf(m[i], max8(mt2[i])), ref = mx == -INFINITY ? 0.f : mx;
+            f[i] = exp2f(m[i] - ref);
+            m[i] = mx;
+            l[i] *= f[i];
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int e = i; e < 4; e += 2) {
+                    s[mt][e] = exp2f(s[mt][e] - ref);
+                    l[i] += s[mt][e];
+                }
+        }
+        if (__any_sync(kFull, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+                o[c][0] *= f[0];
+                o[c][1] *= f[1];
+                o[c][2] *= f[0];
+                o[c][3] *= f[1];
+            }
+        }
+        // the probabilities rounded to bf16 as operands
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+            const uint32_t b0 = transpose8(pack2(s[mt][0], s[mt][1])), b1 = transpose8(pack2(s[mt][2], s[mt][3]));
+            const int r = mt * 16 + (lane & 7) + (id >> 1) * 8;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+                uint32_t v[4];
+                ldsm4_t(v, vb + r * (D * 2) + (((2 * c + (id & 1)) ^ (r & 7)) * 16));
+                mma16816(o[c], v, b0, b1);
+            }
+        }
+    }
+    // this warp's results: row g of so [8][D], sm, sl [8]
+    __device__ __forceinline__ void finish(float *sm, float *sl, float *so) {
+        const int lane = threadIdx.x % 32, g = 2 * (lane % 4);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float z = sum8(l[i]);
+            if (lane < 4) {
+                sm[g + i] = m[i];
+                sl[g + i] = z;
+            }
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+                so[(g + i) * D + c * 16 + lane / 4] = o[c][i];
+                so[(g + i) * D + c * 16 + lane / 4 + 8] = o[c][2 + i];
+            }
+        }
+    }
+};
+
+// float32 on the CUDA cores: a key's logits are two lanes' halves of the dimensions; then a
+// lane owns D / 32 dimensions of the output and runs over the keys.
+template <int D>
+struct Rows<float, D> {
+    static constexpr int kE = D / 32;
+    float o[kMaxGroupHeads][kE], m[kMaxGroupHeads], l[kMaxGroupHeads];  // m and l: of every lane alike
+
+    __device__ __forceinline__ void start(const SinkDecodeArgs &a, int b, int hk, float *) {
+#pragma unroll
+        for (int g = 0; g < kMaxGroupHeads; ++g) {
+            m[g] = -INFINITY;
+            l[g] = 0.f;
+#pragma unroll
+            for (int e = 0; e < kE; ++e) o[g][e] = 0.f;
+        }
+    }
+    __device__ __forceinline__ void tile(const SinkDecodeArgs &a, const Place<16> &p, const uint8_t *stage, float scale2,
+                                         float *qs) {
+        const int lane = threadIdx.x % 32, key = lane % 16, half = lane / 16;
+        const float *kt = reinterpret_cast<const float *>(stage), *vt = kt + 16 * D;
+        float s[kMaxGroupHeads];
+#pragma unroll
+        for (int g = 0; g < kMaxGroupHeads; ++g) s[g] = 0.f;
+#pragma unroll 4
+        for (int u = 0; u < D / 8; ++u) {
+            const int uu = half * (D / 8) + u;
+            const float4 k = *reinterpret_cast<const float4 *>(kt + key * D + ((uu ^ (key & 7)) * 4));
+#pragma unroll
+            for (int g = 0; g < kMaxGroupHeads; ++g) {
+                if (g >= a.G) break;
+                const float4 x = *reinterpret_cast<const float4 *>(qs + g * D + uu * 4);
+                s[g] = fmaf(k.x, x.x, fmaf(k.y, x.y, fmaf(k.z, x.z, fmaf(k.w, x.w, s[g]))));
+            }
+        }
+        const bool in = key < p.v.n - p.k * 16;
 #pragma unroll
         for (int g = 0; g < kMaxGroupHeads; ++g) {
             if (g >= a.G) break;
-            float s = 0.f;
+            s[g] += __shfl_xor_sync(kFull, s[g], 16);
+            s[g] = in ? s[g] * scale2 : -INFINITY;
+            if (a.logits && in && half == 0)
+                a.logits[((int64_t)p.b * a.H + p.hk * a.G + g) * a.logit_stride + p.k * 16 + key] = s[g];
+            float mx = s[g];
 #pragma unroll
-            for (int e = 0; e < kE; ++e) s = fmaf(q[g][e], k[e], s);
-            s = warp_sum(s) * scale2;
-            if (a.logits && lane == 0) a.logits[((int64_t)b * a.H + hk * a.G + g) * a.logit_stride + v] = s;
-            const float mt = fmaxf(m[g], s);
-            const float ref = mt == -INFINITY ? 0.f : mt;
-            const float f = exp2f(m[g] - ref), p = exp2f(s - ref);
-            m[g] = mt;
-            l[g] = fmaf(l[g], f, p);
+            for (int o_ = 8; o_ > 0; o_ >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o_));
+            mx = fmaxf(mx, m[g]);
+            const float ref = mx == -INFINITY ? 0.f : mx, f = exp2f(m[g] - ref);
+            s[g] = exp2f(s[g] - ref);
+            float z = s[g];
 #pragma unroll
-            for (int e = 0; e < kE; ++e) o[g][e] = fmaf(o[g][e], f, p * u[e]);
+            for (int o_ = 8; o_ > 0; o_ >>= 1) z += __shfl_xor_sync(kFull, z, o_);
+            m[g] = mx;
+            l[g] = fmaf(l[g], f, z);
+#pragma unroll
+            for (int e = 0; e < kE; ++e) o[g][e] *= f;
+        }
+#pragma unroll 4
+        for (int k = 0; k < 16; ++k) {
+            float v[kE];
+            const int unit = lane * kE / 4, at = k * D + ((unit ^ (k & 7)) * 4) + (lane * kE) % 4;
+            if (kE == 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(vt + at);
+                v[0] = x.x;
+                v[1] = x.y;
+                v[kE - 2] = x.z;
+                v[kE - 1] = x.w;
+            } else {
+                const float2 x = *reinterpret_cast<const float2 *>(vt + at);
+                v[0] = x.x;
+                v[1] = x.y;
+            }
+#pragma unroll
+            for (int g = 0; g < kMaxGroupHeads; ++g) {
+                if (g >= a.G) break;
+                const float w = __shfl_sync(kFull, s[g], k);
+#pragma unroll
+                for (int e = 0; e < kE; ++e) o[g][e] = fmaf(w, v[e], o[g][e]);
+            }
         }
     }
+    __device__ __forceinline__ void finish(float *sm, float *sl, float *so) {
+        const int lane = threadIdx.x % 32;
 #pragma unroll
-    for (int g = 0; g < kMaxGroupHeads; ++g) {
-        if (lane == 0) {
-            sm[warp][g] = m[g];
-            sl[warp][g] = l[g];
+        for (int g = 0; g < kMaxGroupHeads; ++g) {
+            if (lane == 0) {
+                sm[g] = m[g];
+                sl[g] = l[g];
+            }
+#pragma unroll
+            for (int e = 0; e < kE; ++e) so[g * D + lane * kE + e] = o[g][e];
         }
-#pragma unroll
-        for (int e = 0; e < kE; ++e) so[warp][g][lane * kE + e] = o[g][e];
     }
-    __syncthreads();
-    for (int g = warp; g < a.G; g += kWarps) {
-        float mx = -INFINITY, z = 0.f;
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm[w][g]);
-        float r[kE] = {};
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = sl[w][g] > 0.f ? exp2f(sm[w][g] - mx) : 0.f;
-            z = fmaf(f, sl[w][g], z);
-#pragma unroll
-            for (int e = 0; e < kE; ++e) r[e] = fmaf(f, so[w][g][lane * kE + e], r[e]);
+};
+
+// The tiles of all rows are cut into one even share for each CTA, whatever the sequences'
+// lengths. A row that several CTAs share, or that has partial results of the prefix kernel,
+// is joined, in order, by the last of its CTAs to arrive.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThr) sink_decode_kernel(SinkDecodeArgs a) {
+    constexpr int KT = tile_keys<T>(), kE = D / 32;
+    constexpr int kStage = 2 * tile_bytes<T, D>();
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int Hk = a.H / a.G, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    uint8_t *ring = smem + warp * kStages * kStage;
+    float *merge = reinterpret_cast<float *>(smem + kWarps * kStages * kStage);
+    float *sm = merge, *sl = sm + kWarps * kMaxGroupHeads, *so = sl + kWarps * kMaxGroupHeads;
+    float *qs = so + kWarps * kMaxGroupHeads * D;  // float32: the row's queries
+    int *flag = reinterpret_cast<int *>(qs + kMaxGroupHeads * D);
+    const float scale2 = a.scale * kLog2e;
+    const int64_t total = all_tiles<KT>(a, Hk), n_cta = min((int64_t)gridDim.x, total), c = blockIdx.x;
+    if (c >= n_cta) return;  // every other CTA has a tile: each of a row's CTAs arrives
+    const int64_t t0 = total * c / n_cta, t1 = total * (c + 1) / n_cta;
+    auto cta_of = [&](int64_t tile) { return ((tile + 1) * n_cta - 1) / total; };
+    Place<KT> cur = find_tile<KT>(a, Hk, t0);  // the CTA's current row, at its first tile here
+    Place<KT> ld = cur;
+    ld.advance(a, Hk, warp);
+    int64_t at = t0 + warp;
+    int put = 0, got = 0;  // stages written, read
+    auto next_load = [&] {
+        if (at < t1) {
+            load_kv<T, D, KT>(a, ld, ring + put % kStages * kStage);
+            ld.advance(a, Hk, kWarps);
+            at += kWarps;
         }
-        const int64_t slot = ((int64_t)b * a.H + hk * a.G + g) * a.slots + a.slot0 + split;
-        const float inv = z > 0.f ? 1.f / z : 0.f;
+        ++put;
+        cp_async_commit();
+    };
 #pragma unroll
-        for (int e = 0; e < kE; ++e) a.part_o[slot * D + lane * kE + e] = r[e] * inv;
-        if (lane == 0) a.part_lse[slot] = z > 0.f ? (mx + log2f(z)) * 0.6931471805599453f : -INFINITY;
+    for (int i = 0; i < kStages - 1; ++i) next_load();
+    for (int64_t t = t0; t < t1;) {  // a row, or what of it is this CTA's
+        const int64_t row0 = t - cur.k;  // the row's first tile
+        const int64_t end = min(t1, row0 + cur.v.tiles);
+        if (sizeof(T) == 4) {
+            __syncthreads();  // the row before is joined
+            for (int e = threadIdx.x; e < a.G * D; e += kThr) {
+                const int g = e / D;
+                qs[e] = static_cast<const float *>(a.Q.ptr)[cur.b * a.Q.sb + (int64_t)(cur.hk * a.G + g) * a.Q.sh + e % D];
+            }
+            __syncthreads();
+        }
+        Rows<T, D> rows;
+        rows.start(a, cur.b, cur.hk, qs);
+        Place<KT> p = cur;
+        // this warp's first tile at or after t
+        const int skip = (int)((warp - (t - t0)) % kWarps + kWarps) % kWarps;
+        p.k += skip;
+        for (int64_t x = t + skip; x < end; x += kWarps, p.k += kWarps) {
+            next_load();
+            cp_async_wait<kStages - 1>();
+            __syncwarp();
+            rows.tile(a, p, ring + got % kStages * kStage, scale2, qs);
+            ++got;
+            __syncwarp();
+        }
+        rows.finish(sm + warp * kMaxGroupHeads, sl + warp * kMaxGroupHeads, so + warp * kMaxGroupHeads * D);
+        __syncthreads();
+        const int64_t rowidx = (int64_t)cur.b * Hk + cur.hk;
+        const int64_t c0 = cta_of(row0), c1 = cta_of(row0 + cur.v.tiles - 1);
+        const bool alone = c0 == c1 && a.slots == 0;
+        for (int g = warp; g < a.G; g += kWarps) {
+            float mx = -INFINITY, z = 0.f, r[kE] = {};
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm[w * kMaxGroupHeads + g]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float lw = sl[w * kMaxGroupHeads + g], f = lw > 0.f ? exp2f(sm[w * kMaxGroupHeads + g] - mx) : 0.f;
+                z = fmaf(f, lw, z);
+#pragma unroll
+                for (int e = 0; e < kE; ++e) r[e] = fmaf(f, so[(w * kMaxGroupHeads + g) * D + lane * kE + e], r[e]);
+            }
+            const float inv = z > 0.f ? 1.f / z : 0.f, lse = z > 0.f ? (mx + log2f(z)) * kLn2 : -INFINITY;
+            const int h = cur.hk * a.G + g;
+            if (alone) {
+                T *dst = static_cast<T *>(a.O.ptr) + cur.b * a.O.sb + h * a.O.sh + lane * kE;
+#pragma unroll
+                for (int e = 0; e < kE; e += 2) store2(dst + e, r[e] * inv, r[e + 1] * inv);
+                if (lane == 0) a.lse[(int64_t)cur.b * a.H + h] = lse;
+            } else {
+                const int64_t seg = (c + rowidx) * a.G + g;
+#pragma unroll
+                for (int e = 0; e < kE; e += 2) store2(a.seg_o + seg * D + lane * kE + e, r[e] * inv, r[e + 1] * inv);
+                if (lane == 0) a.seg_lse[seg] = lse;
+            }
+        }
+        if (!alone) {
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                const int before = atomicAdd(a.counters + rowidx, 1);
+                *flag = before == (int)(c1 - c0);
+                if (*flag) a.counters[rowidx] = 0;  // as the next call finds it
+            }
+            __syncthreads();
+            if (*flag) {
+                __threadfence();
+                for (int g = warp; g < a.G; g += kWarps) {
+                    const int h = cur.hk * a.G + g, ns = (int)(c1 - c0) + 1, all = ns + a.slots;
+                    const int64_t row = (int64_t)cur.b * a.H + h;
+                    // partial s: the prefix kernel's slots, then the CTAs' segments in order
+                    auto lse_of = [&](int s) {
+                        return s < a.slots ? __ldcg(a.part_lse + row * a.slots + s)
+                                           : __ldcg(a.seg_lse + (c0 + (s - a.slots) + rowidx) * a.G + g);
+                    };
+                    float mx = -INFINITY, z = 0.f;
+                    for (int s = lane; s < all; s += 32) mx = fmaxf(mx, lse_of(s));
+                    mx = warp_max(mx);
+                    const float ref = mx == -INFINITY ? 0.f : mx;
+                    float r[kE] = {};
+                    for (int s0 = 0; s0 < all; s0 += 32) {
+                        const float wl = s0 + lane < all ? expf(lse_of(s0 + lane) - ref) : 0.f;
+                        z += wl;
+                        const int m = min(32, all - s0);
+#pragma unroll 4
+                        for (int i = 0; i < m; ++i) {
+                            const int s = s0 + i;
+                            const float w = __shfl_sync(kFull, wl, i);
+                            const float *src = s < a.slots ? a.part_o + (row * a.slots + s) * D
+                                                           : a.seg_o + ((c0 + (s - a.slots) + rowidx) * a.G + g) * D;
+#pragma unroll
+                            for (int e = 0; e < kE; e += 2) {
+                                const float2 x = __ldcg(reinterpret_cast<const float2 *>(src + lane * kE + e));
+                                r[e] = fmaf(w, x.x, r[e]);
+                                r[e + 1] = fmaf(w, x.y, r[e + 1]);
+                            }
+                        }
+                    }
+                    z = warp_sum(z);
+                    const float inv = z > 0.f ? 1.f / z : 0.f;
+                    T *dst = static_cast<T *>(a.O.ptr) + cur.b * a.O.sb + h * a.O.sh + lane * kE;
+#pragma unroll
+                    for (int e = 0; e < kE; e += 2) store2(dst + e, r[e] * inv, r[e + 1] * inv);
+                    if (lane == 0) a.lse[row] = z > 0.f ? mx + logf(z) : -INFINITY;
+                }
+            }
+        }
+        __syncthreads();  // sm, sl, so are free again
+        cur.advance(a, Hk, (int)(end - t));
+        t = end;
     }
+    cp_async_wait<0>();
 }
 
 // One warp per row: weights exp(lse_s - max) over the row's slots, in slot order.
@@ -150,26 +569,29 @@ __global__ void __launch_bounds__(256) sink_acc_kernel(SinkDecodeArgs a, const f
 
 }  // namespace
 
-// Splits of a sequence's visible slots: about two CTAs per SM, 64 slots or more each.
-int sink_decode_splits(int B, int Hk, int64_t keys, int sms) {
-    const int64_t rows = (int64_t)B * Hk;
-    int64_t s = rows > 0 ? (2 * (int64_t)sms + rows - 1) / rows : 1;
-    if (s > keys / 64) s = keys / 64;
-    return (int)(s < 1 ? 1 : s > 128 ? 128 : s);
+// CTAs of a decode: one per SM, no more than there are tiles.
+int sink_decode_ctas(hils_dtype dt, int B, int Hk, int64_t keys, int sms) {
+    const int kt = dt == HILS_BF16 ? tile_keys<bf16>() : tile_keys<float>();
+    const int64_t tiles = (int64_t)B * Hk * (keys > kt ? (keys + kt - 1) / kt : 1);
+    return (int)(tiles < sms ? tiles : sms);
 }
 
-hils_status launch_sink_decode(hils_dtype dt, int d, const SinkDecodeArgs &a, cudaStream_t s) {
-    const int64_t grid = (int64_t)a.B * (a.H / a.G) * a.splits;
-    if (grid == 0) return HILS_OK;
-    if (grid > 0x7fffffffll) return HILS_ERR_UNSUPPORTED;
-    if (dt == HILS_BF16) {
-        if (d == 64) sink_decode_kernel<bf16, 64><<<(unsigned)grid, kThr, 0, s>>>(a);
-        else sink_decode_kernel<bf16, 128><<<(unsigned)grid, kThr, 0, s>>>(a);
-    } else {
-        if (d == 64) sink_decode_kernel<float, 64><<<(unsigned)grid, kThr, 0, s>>>(a);
-        else sink_decode_kernel<float, 128><<<(unsigned)grid, kThr, 0, s>>>(a);
-    }
+namespace {
+template <typename T, int D>
+hils_status decode(const SinkDecodeArgs &a, int ctas, cudaStream_t s) {
+    static KernelSetup setup;
+    const auto k = sink_decode_kernel<T, D>;
+    const hils_status st = kernel_setup(setup, (const void *)k, kThr, decode_smem<T, D>(), nullptr);
+    if (st != HILS_OK) return st;
+    k<<<ctas, kThr, decode_smem<T, D>(), s>>>(a);
     return record_cuda_error(cudaGetLastError());
+}
+}  // namespace
+
+hils_status launch_sink_decode(hils_dtype dt, int d, const SinkDecodeArgs &a, int ctas, cudaStream_t s) {
+    if (ctas == 0) return HILS_OK;
+    if (dt == HILS_BF16) return d == 64 ? decode<bf16, 64>(a, ctas, s) : decode<bf16, 128>(a, ctas, s);
+    return d == 64 ? decode<float, 64>(a, ctas, s) : decode<float, 128>(a, ctas, s);
 }
 
 hils_status launch_sink_combine(hils_dtype dt, int d, const SinkCombineArgs &a, cudaStream_t s) {
