@@ -40,8 +40,8 @@ __device__ __forceinline__ void grad_columns(const uint32_t (&s)[32], const uint
             v0 = (mk >> q) & 1u ? v0 : -INFINITY;
             v1 = (mk >> (q + 1)) & 1u ? v1 : -INFINITY;
         }
-        v0 = ex2(v0);
-        v1 = ex2(v1);
+        v0 = exp2_ftz(v0);
+        v1 = exp2_ftz(v1);
         float d0 = v0 * (__uint_as_float(t[q]) - Dv(q)), d1 = v1 * (__uint_as_float(t[q + 1]) - Dv(q + 1));
         if (!full) {  // t may be anything there
             d0 = (mk >> q) & 1u ? d0 : 0.f;

@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                 const bool none = isinf(mt);  // no visible key in this tile
                 mt = none ? -INFINITY : mt * scale2;
                 const bool raise = !none && (m == -INFINITY || mt > m + 8.f);
-                const float fac = raise ? ex2(m - mt) : 1.f;  // 0 when m is -inf
+                const float fac = raise ? exp2_ftz(m - mt) : 1.f;  // 0 when m is -inf
                 if (__any_sync(kFull, raise && l > 0.f)) {
                     // S of this tile was issued after the PV of the one before had completed
 #pragma unroll 1
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                                 for (int k = 0; k < 4; ++k) v[k] = (mk >> (q + k)) & 1u ? v[k] : -INFINITY;
                             }
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) v[k] = ex2(v[k]);
+                            for (int k = 0; k < 4; ++k) v[k] = exp2_ftz(v[k]);
                             z0 += v[0];
                             z1 += v[1];
                             z2 += v[2];

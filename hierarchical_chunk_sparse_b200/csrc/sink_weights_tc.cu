@@ -259,9 +259,9 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
 #pragma unroll
                             for (int k = 0; k < 4; ++k) e[k] = (mk >> (q + k)) & 1u ? e[k] : -INFINITY;
                         }
-                        z0 += ex2(e[0]);
-                        z1 += ex2(e[1]);
-                        z2 += ex2(e[2]);
+                        z0 += exp2_ftz(e[0]);
+                        z1 += exp2_ftz(e[1]);
+                        z2 += exp2_ftz(e[2]);
                         z3 += exp2_fma(e[3]);
                     }
                 }
