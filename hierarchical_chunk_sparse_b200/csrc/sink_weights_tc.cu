@@ -9,7 +9,9 @@
 // the next steps are loaded meanwhile. The rows' lse (log2 units) are staged in shared memory.
 // The exponentials bound it (16 a cycle and SM on the MUFU against 8192 products): every
 // fourth one is evaluated on the FMA pipe instead.
-// Warps 0-3, 4-7: rows of tile A, B; 8, 9: tcgen05.mma of A, B; 10: TMA and lse.
+// Warps 0-7, 8-15: the keys of tile A, B (TMEM lane quadrant w % 4), each key's columns in two
+// halves: with one warp per quadrant and tile the loads and exponentials waited on their
+// latencies; 16, 17: tcgen05.mma of A, B; 18: TMA and lse.
 // TMEM: S_A [0,128), [128,256); S_B [256,384), [384,512).
 #include "fast_math.cuh"
 #include "sink_tc.cuh"
@@ -19,7 +21,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kM = 128, kKeys = 2 * kM, kRows = 128, kStages = 3, kThreads = 384, kMmaWarp = 8, kLoadWarp = 10;
+constexpr int kM = 128, kKeys = 2 * kM, kRows = 128, kStages = 3, kThreads = 608, kMmaWarp = 16, kLoadWarp = 18;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -27,18 +29,21 @@ enum {
     kBarXfull = 0,   // + buffer: the item's keys
     kBarXfree = 2,   // + buffer (both tiles)
     kBarYfull = 4,   // + stage: query rows (bytes) and lse (32 arrivals)
-    kBarYfree = 7,   // + stage: both tiles' products, and the 8 warps' reads of lse
+    kBarYfree = 7,   // + stage: both tiles' products, and the 16 warps' reads of lse
     kBarS = 10,      // + 2 * tile + buffer: S^T written
-    kBarSfree = 14,  // + 2 * tile + buffer: S^T read (4 warps)
+    kBarSfree = 14,  // + 2 * tile + buffer: S^T read (8 warps)
     kBarDrain = 18,  // + tile
-    kNumBars = 20
+    kBarHalf = 20,   // + 4 tile + quadrant: the second half's sums are in hsum
+    kBarHalfFree = 28,  // + the same: read
+    kNumBars = 36
 };
 template <int D>
 struct Smem {
     static constexpr int kX = kM * D * 2, kY = kRows * D * 2;
     static constexpr int kK = 0, kQ = 4 * kX, kL = kQ + kStages * kY;
-    static constexpr int kBars = kL + kStages * kRows * 4, kMisc = kBars + 8 * kNumBars;
-    static constexpr int kBytes = kMisc + 16 + 1024;  // + alignment slack
+    static constexpr int kH = kL + kStages * kRows * 4;  // sums of the keys' second halves
+    static constexpr int kBars = kH + kKeys * 4, kMisc = kBars + 8 * kNumBars;
+    static constexpr int kBytes = kMisc + 16;
 };
 struct Args {
     SinkBwdArgs a;
@@ -83,15 +88,18 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                                                                       const __grid_constant__ CUtensorMap tmK, Args f,
                                                                       int total) {
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's atoms: no room for slack
     using L = Smem<D>;
     constexpr int kBlocks = D / 64, kBlk = kM * 128;
-    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const SinkBwdArgs &a = f.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = smem_u32(smem);
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + L::kMisc);
-    float *lse = reinterpret_cast<float *>(smem + L::kL);
+    float *lse = reinterpret_cast<float *>(smem + L::kL), *hsum = reinterpret_cast<float *>(smem + L::kH);
+    if (sbase & 1023u) {  // an alignment that the launch has to give
+        if (tid == 0) atomicOr(a.status, 1u);
+        return;
+    }
     const Pipe pipe{sbase + L::kBars, misc + 1, a.status, a.wait_ns};
     const int G = gridDim.x, cta = blockIdx.x;
 
@@ -100,8 +108,8 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
             uint32_t cnt = 1;
             if (i == kBarXfree || i == kBarXfree + 1) cnt = 2;
             if (i >= kBarYfull && i < kBarYfull + kStages) cnt = 33;
-            if (i >= kBarYfree && i < kBarYfree + kStages) cnt = 10;
-            if (i >= kBarSfree && i < kBarSfree + 4) cnt = 4;
+            if (i >= kBarYfree && i < kBarYfree + kStages) cnt = 18;
+            if (i >= kBarSfree && i < kBarSfree + 4) cnt = 8;
             mbar_init(pipe.bar(i), cnt);
         }
         misc[1] = 0u;
@@ -141,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
                     const int row = lane + 32 * m, i = q0 + row % f.qn;
                     float v = -INFINITY;
                     if (i < a.Lq) v = __ldg(a.lse + ((int64_t)it.b * a.H + h0 + row / f.qn) * a.Lq + i);
-                    sc[m] = v == -INFINITY ? INFINITY : v * kLog2e;  // nothing seen: exp2(s - inf) = 0
+                    sc[m] = v == -INFINITY ? v : -v * kLog2e;  // -lse; nothing seen: exp2(s - inf) = 0
                 }
             };
             scalars(it.s0);
@@ -168,61 +176,70 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
         __syncwarp();
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         const int x = warp - kMmaWarp;
-        if (lane == 0) {
-            int n = 0, g = 0, c = 0;  // items with steps, steps, steps of x
-            bool ok = true;
-            for (int r = 0; ok; ++r) {
-                const int j = item_of_round(r, cta, G);
-                if (j >= total) break;
-                const Item it = decode(f, j);
-                if (it.s0 >= it.s1) continue;
-                const int xb = n & 1;
-                const uint32_t kb = sbase + L::kK + (2 * xb + x) * L::kX;
-                if (!(ok = pipe.wait(kBarXfull + xb, (n >> 1) & 1))) break;
-                for (int s = it.s0; s < it.s1; ++s, ++g) {
-                    const int st = g % kStages;
-                    if (!(ok = pipe.wait(kBarYfull + st, (g / kStages) & 1))) break;
-                    if (!it.valid(x, it.i0 + (s % it.tiles) * f.qn, f.qn)) {
-                        pipe.arrive(kBarYfree + st);
-                        continue;
-                    }
-                    const int sb = 2 * x + (c & 1);
-                    if (c >= 2 && !(ok = pipe.wait(kBarSfree + sb, ((c >> 1) - 1) & 1))) break;
-                    tc_fence_after();
-                    const uint32_t qb = sbase + L::kQ + st * L::kY;
+        int n = 0, g = 0, c = 0;  // items with steps, steps, steps of x
+        bool ok = true;
+        const uint64_t kd0 = tile_desc(sbase + L::kK + x * L::kX, 16), qd0 = tile_desc(sbase + L::kQ, 16);
+        for (int r = 0; ok; ++r) {
+            const int j = item_of_round(r, cta, G);
+            if (j >= total) break;
+            const Item it = decode(f, j);
+            if (it.s0 >= it.s1) continue;
+            const int xb = n & 1;
+            const uint64_t kd = kd0 + xb * (2 * L::kX / 16);
+            if (!(ok = pipe.wait_warp(kBarXfull + xb, (n >> 1) & 1))) break;
+            int tile = it.s0 % it.tiles;
+            for (int s = it.s0; s < it.s1; ++s, ++g) {
+                const int st = g % kStages, q0 = it.i0 + tile * f.qn;
+                if (++tile == it.tiles) tile = 0;
+                if (!(ok = pipe.wait_warp(kBarYfull + st, (g / kStages) & 1))) break;
+                if (!it.valid(x, q0, f.qn)) {
+                    if (lane == 0) pipe.arrive(kBarYfree + st);
+                    continue;
+                }
+                const int sb = 2 * x + (c & 1);
+                if (c >= 2 && !(ok = pipe.wait_warp(kBarSfree + sb, ((c >> 1) - 1) & 1))) break;
+                tc_fence_after();
+                const uint64_t qd = qd0 + st * (L::kY / 16);
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t o = (k >> 2) * kBlk + (k & 3) * 32;
-                        mma_ss(tmem + sb * 128, smem_desc(kb + o, 16, 1024), smem_desc(qb + o, 16, 1024),
-                               idesc_bf16(kM, kRows, false), k > 0);
+                        const uint64_t o = ((k >> 2) * kBlk + (k & 3) * 32) / 16;
+                        mma_ss(tmem + sb * 128, kd + o, qd + o, idesc_bf16(kM, kRows, false), k > 0);
                     }
                     mma_commit(pipe.bar(kBarS + sb));
                     mma_commit(pipe.bar(kBarYfree + st));
-                    ++c;
                 }
-                if (!ok) break;
-                mma_commit(pipe.bar(kBarXfree + xb));
-                ++n;
+                __syncwarp();
+                ++c;
             }
+            if (!ok) break;
+            if (elect_one()) mma_commit(pipe.bar(kBarXfree + xb));
+            __syncwarp();
+            ++n;
+        }
+        if (elect_one()) {
             mma_commit(pipe.bar(kBarDrain + x));
             pipe.drain(kBarDrain + x, 1);
         }
         __syncwarp();
-    } else if (warp < 8) {
-        const int x = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
+    } else if (warp < 16) {
+        const int x = warp >> 3, quad = warp & 3, half = (warp >> 2) & 1, row = quad * 32 + lane;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const float scale2 = a.scale * kLog2e;
+        const float scale2 = a.scale * kLog2e, lowest = scale2 > 0.f ? -INFINITY : INFINITY;  // its logit is -inf
+        const float2 scale22 = make_float2(scale2, scale2);
         const int off = a.N - a.Lq, Hk = a.H / a.G;
         bool ok = true;
-        int g = 0, c = 0;
+        int g = 0, c = 0, n = 0;
         for (int r = 0; ok; ++r) {
             const int j = item_of_round(r, cta, G);
             if (j >= total) break;
             const Item it = decode(f, j);
             const int key = it.j0 + x * kM + row;
             float w = 0.f;
+            int tile = it.s0 % max(it.tiles, 1);
             for (int s = it.s0; s < it.s1; ++s, ++g) {
-                const int st = g % kStages, q0 = it.i0 + (s % it.tiles) * f.qn;
+                const int st = g % kStages, q0 = it.i0 + tile * f.qn;
+                if (++tile == it.tiles) tile = 0;
                 if (!(ok = pipe.wait_warp(kBarYfull + st, (g / kStages) & 1))) break;
                 if (!it.valid(x, q0, f.qn)) {
                     if (lane == 0) pipe.arrive(kBarYfree + st);
@@ -235,37 +252,34 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
                 const int sb = 2 * x + (c & 1);
                 if (!(ok = pipe.wait_warp(kBarS + sb, (c >> 1) & 1))) break;
                 tc_fence_after();
-                const uint32_t s_col = tmem + lanes + sb * 128;
-                const float *lr = lse + st * kRows;
-                float z0 = 0.f, z1 = 0.f, z2 = 0.f, z3 = 0.f;
+                const uint32_t s_col = tmem + lanes + sb * 128 + half * 64;
+                const float *lr = lse + st * kRows + half * 64;
+                float2 z0 = make_float2(0.f, 0.f), z1 = z0;
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
+                for (int ch = 0; ch < 2; ++ch) {
                     uint32_t mk = kFull;
                     if (!full) {
-                        mk = range_bits(lo, hi, (ch * 32) & (f.qn - 1));
+                        mk = range_bits(lo, hi, (half * 64 + ch * 32) & (f.qn - 1));
                         if (f.qn == 16) mk |= mk << 16;
                         if (!__any_sync(kFull, mk != 0)) continue;
                     }
                     uint32_t v[32];
                     tmem_ld32(s_col + ch * 32, v);
                     tmem_wait_ld();
+                    if (!full) {
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) v[q] = (mk >> q) & 1u ? v[q] : __float_as_uint(lowest);
+                    }
 #pragma unroll
                     for (int q = 0; q < 32; q += 4) {
                         const float4 L4 = *reinterpret_cast<const float4 *>(lr + ch * 32 + q);
-                        float e[4] = {fmaf(__uint_as_float(v[q]), scale2, -L4.x), fmaf(__uint_as_float(v[q + 1]), scale2, -L4.y),
-                                      fmaf(__uint_as_float(v[q + 2]), scale2, -L4.z),
-                                      fmaf(__uint_as_float(v[q + 3]), scale2, -L4.w)};
-                        if (!full) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) e[k] = (mk >> (q + k)) & 1u ? e[k] : -INFINITY;
-                        }
-                        z0 += exp2_ftz(e[0]);
-                        z1 += exp2_ftz(e[1]);
-                        z2 += exp2_ftz(e[2]);
-                        z3 += exp2_fma(e[3]);
+                        const float2 e0 = fma2(as2(v + q), scale22, make_float2(L4.x, L4.y));
+                        const float2 e1 = fma2(as2(v + q + 2), scale22, make_float2(L4.z, L4.w));
+                        z0 = add2(z0, make_float2(exp2_ftz(e0.x), exp2_ftz(e0.y)));
+                        z1 = add2(z1, make_float2(exp2_ftz(e1.x), exp2_fma(e1.y)));
                     }
                 }
-                w += (z0 + z1) + (z2 + z3);
+                w += (z0.x + z0.y) + (z1.x + z1.y);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -275,6 +289,21 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
                 ++c;
             }
             if (!ok) break;
+            // the two halves of a key, the first one's sum first
+            const int pair = 4 * x + quad;
+            if (half == 1) {
+                if (n > 0 && !(ok = pipe.wait_warp(kBarHalfFree + pair, (n - 1) & 1))) break;
+                hsum[x * kM + row] = w;
+                __syncwarp();
+                if (lane == 0) pipe.arrive(kBarHalf + pair);
+                ++n;
+                continue;
+            }
+            if (!(ok = pipe.wait_warp(kBarHalf + pair, n & 1))) break;
+            w += hsum[x * kM + row];
+            __syncwarp();
+            if (lane == 0) pipe.arrive(kBarHalfFree + pair);
+            ++n;
             if (key >= a.N) continue;
             if (it.nseg > 1) {
                 a.part[(int64_t)it.index * kKeys + x * kM + row] = w;
