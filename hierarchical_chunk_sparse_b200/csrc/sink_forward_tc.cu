@@ -2,8 +2,8 @@
 // shared prefix of a decode batch (formulas in sink_common.cuh).
 //
 // A persistent CTA (one per SM) takes items of two 128-row query tiles A and B and walks
-// 128-key tiles with an online softmax: S = Q K^T (M = 128 rows, N = keys, K = d) into
-// TMEM, the softmax over it with P (bf16) written over S, O += P V with P read from TMEM.
+// 64-key tiles with an online softmax: S = Q K^T (M = 128 rows, N = keys, K = d) into TMEM,
+// the softmax over it with P (bf16) written over S, O += P V with P read from TMEM.
 //   prefill  a tile is P heads of a group (the largest power of two <= 8 that divides G)
 //            with 128 / P consecutive queries each; A and B are neighbours and share each
 //            key tile; a tile that only one of them sees is skipped by the other. The
@@ -12,16 +12,20 @@
 //            loaded. The last tile's products cover only its keys, rounded up to 16.
 //   prefix   a tile is 128 / G sequences with the G heads of a group each, so that the
 //            prefix is read once for all of them; A and B are the same rows over two key
-//            ranges, which the combine joins.
-// Warp roles (384 threads), hand-offs through mbarriers:
-//   warps 0-3, 4-7  softmax of tile A, B: a thread owns a row (TMEM lane); its reference
-//                   maximum is raised, and O rescaled, only when the tile's maximum passes
-//                   it by more than 8 in log2 units (P <= 2^8: exact in the float32 sums,
-//                   no worse rounded in bf16);
-//   warps 8, 9      tcgen05.mma of tile A, B;   warp 10  TMA.
-// S of a tile is single-buffered and its next S is issued once the PV that read P has
-// completed: while A is in its softmax the tensor cores work for B, and the other way.
-// TMEM: S_A [0,128), S_B [128,256), O_A [256,384), O_B [384,512).
+//            ranges, which are joined later.
+// Warp roles (608 threads), hand-offs through mbarriers:
+//   warps 0-15   softmax: two warpgroups for each of A and B, which take its key tiles in turn;
+//                a thread owns a row (TMEM lane). Their maxima and sums are their own; the
+//                row's reference goes from one to the other through shared memory, before the
+//                exponentials, so that they overlap. It is raised, and O rescaled, only when a
+//                tile's maximum passes it by more than 8 in log2 units (P <= 2^8: exact in the
+//                float32 sums, rounded in bf16 as well as below 1).
+//   warps 16, 17 tcgen05.mma of A, B;   warp 18  TMA.
+// S is double-buffered: S of the next tile is computed during the softmax of this one, once
+// the PV that read the buffer has completed. A quarter of the exponentials is evaluated on the
+// FMA pipe, since the MUFU's 16 a cycle would take as long as the products.
+// TMEM: S_A [0,64), [64,128); S_B [128,192), [192,256); O_A [256,384), O_B [384,512).
+#include "fast_math.cuh"
 #include "sink_tc.cuh"
 
 namespace hils {
@@ -29,24 +33,24 @@ namespace {
 
 using namespace tc;
 
-constexpr int kM = 128, kKeys = 128, kThreads = 384;
-constexpr int kMmaWarp = 8, kLoadWarp = 10;
+constexpr int kM = 128, kKeys = 64, kThreads = 608;
+constexpr int kMmaWarp = 16, kLoadWarp = 18;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 enum {
     kBarQfull = 0,    // + tile (prefix: 0 for both)
     kBarQfree = 2,    // + tile
-    kBarKfull = 4,    // + slot
-    kBarKfree = 8,    // + slot
-    kBarVfull = 12,   // + slot
-    kBarVfree = 14,   // + slot
-    kBarS = 16,       // + tile: S written
-    kBarP = 18,       // + tile: P written over it (4 warps)
-    kBarPV = 20,      // + tile: PV, and every MMA before it, completed
-    kBarOfree = 22,   // + tile: O read (4 warps)
-    kBarDrain = 24,   // + tile
-    kNumBars = 26
+    kBarFull = 4,     // + stage: K and V landed
+    kBarFree = 10,    // + stage: the products that read them completed
+    kBarS = 16,       // + 2 tile + buffer: S written
+    kBarP = 20,       // + 2 tile + buffer: P written over it (4 warps)
+    kBarPV = 24,      // + 2 tile + buffer: its PV, and every MMA before that, completed
+    kBarOfree = 28,   // + tile: O read (8 warps)
+    kBarRef = 30,     // + 4 tile + quadrant: the rows' reference after a tile (1 warp)
+    kBarEnd = 38,     // + 4 tile + quadrant: both warpgroups' sums of an item (2 warps)
+    kBarDrain = 46,   // + tile
+    kNumBars = 48
 };
 
 struct FwdTc {
@@ -56,22 +60,28 @@ struct FwdTc {
     int items, sink_box;
 };
 
+template <int D, bool PREFIX>
+struct Smem {
+    static constexpr int kX = kM * D * 2, kY = kKeys * D * 2;
+    static constexpr int kStages = 4;  // prefix: two for each range
+    static constexpr int kQ = 0, kK = (PREFIX ? 1 : 2) * kX, kV = kK + kStages * kY;
+    static constexpr int kRef = kV + kStages * kY;   // [2 tiles][128] references
+    static constexpr int kEnd = kRef + 2 * kM * 4;   // [2 by item][2 tiles][2 warpgroups][128] reference, sum
+    static constexpr int kBars = kEnd + 8 * kM * 8, kMisc = kBars + 8 * kNumBars;
+    static constexpr int kBytes = kMisc + 16;
+};
+
+// The key tiles of one row tile x of an item, in order: entries [a0, a1), then [b0, b1).
+struct Own {
+    int a0, n1, b0, n;  // n in all, n1 of them in the first run
+    __device__ __forceinline__ int entry(int i) const { return i < n1 ? a0 + i : b0 + (i - n1); }
+};
+
 struct PrefixItem {
     int hk, h, i0;      // key-value head, its first query head, first sequence
     int split;
     bool hasB;          // there is a second key range
-    int r0[2], r1[2];   // the key tiles of A's and B's range
-};
-
-template <int D, bool PREFIX>
-struct Smem {
-    static constexpr int kTileBytes = kM * D * 2;
-    static constexpr int kQ = 0;
-    static constexpr int kK = (PREFIX ? 1 : 2) * kTileBytes;
-    static constexpr int kV = kK + (PREFIX ? 4 : 2) * kTileBytes;
-    static constexpr int kBars = kV + 2 * kTileBytes;
-    static constexpr int kMisc = kBars + 8 * kNumBars;
-    static constexpr int kBytes = kMisc + 16 + 1024;  // + alignment slack
+    int r0, r1, r2;     // A's key tiles [r0, r1), B's [r1, r2)
 };
 
 template <bool PREFIX>
@@ -86,17 +96,35 @@ __device__ __forceinline__ auto decode_item(const FwdTc &f, int j) {
         it.hk = u / f.tiles;
         it.h = it.hk * a.G;
         it.hasB = 2 * it.split + 1 < a.splits;
-        const int nt = (a.N + kKeys - 1) / kKeys;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int r = 2 * it.split + x;
-            it.r0[x] = x == 0 || it.hasB ? (int)((int64_t)nt * r / a.splits) : 0;
-            it.r1[x] = x == 0 || it.hasB ? (int)((int64_t)nt * (r + 1) / a.splits) : 0;
-        }
+        const int nt = (a.N + kKeys - 1) / kKeys, r = 2 * it.split;
+        it.r0 = (int)((int64_t)nt * r / a.splits);
+        it.r1 = (int)((int64_t)nt * (r + 1) / a.splits);
+        it.r2 = it.hasB ? (int)((int64_t)nt * (r + 2) / a.splits) : it.r1;
         return it;
     } else {
         return RowItem<kKeys>(j, a.B, a.H, a.G, f.P, f.qt, f.nqb, a.Lq, a.N, a.W, a.A, a.splits);
     }
+}
+template <bool PREFIX, typename I>
+__device__ __forceinline__ Own own_tiles(const I &it, int x) {
+    Own o;
+    if constexpr (PREFIX) {
+        o.a0 = x ? it.r1 : it.r0;
+        o.n = o.n1 = (x ? it.r2 : it.r1) - o.a0;
+        o.b0 = 0;
+    } else if (x == 0) {
+        o.a0 = it.e0;
+        o.n = o.n1 = max(0, min(it.e1, it.eA) - it.e0);
+        o.b0 = 0;
+    } else {
+        const int w0 = it.sp.ns + it.wB;
+        o.a0 = it.e0;
+        o.n1 = max(0, min(it.e1, it.sp.ns) - it.e0);
+        o.b0 = max(it.e0, w0);
+        o.n = it.hasB ? o.n1 + max(0, it.e1 - o.b0) : 0;
+        if (!it.hasB) o.n1 = 0;
+    }
+    return o;
 }
 
 template <int D, bool PREFIX>
@@ -105,26 +133,29 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                                                                   const __grid_constant__ CUtensorMap tmV,
                                                                   const __grid_constant__ CUtensorMap tmKs,
                                                                   const __grid_constant__ CUtensorMap tmVs, FwdTc f) {
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     using L = Smem<D, PREFIX>;
-    constexpr int kBlocks = D / 64;           // 64-column blocks of a row tile, 16 KB each
-    constexpr int kBlk = kM * 128;
-    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    constexpr int kBlocks = D / 64;  // 64-column blocks of a row tile
+    constexpr int kXBlk = kM * 128, kYBlk = kKeys * 128;
+    constexpr int kRing = PREFIX ? L::kStages / 2 : L::kStages;  // stages of one ring
     const SinkArgs &a = f.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = smem_u32(smem);
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + L::kMisc);
     const Pipe pipe{sbase + L::kBars, misc + 1, a.status, a.wait_ns};
     const int G = gridDim.x, cta = blockIdx.x;
-
+    if (sbase & 1023u) {  // an alignment that the launch has to give
+        if (tid == 0) atomicOr(a.status, 1u);
+        return;
+    }
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i) {
             uint32_t cnt = 1;
-            if (i >= kBarP && i < kBarP + 2) cnt = 4;
-            if (i >= kBarOfree && i < kBarOfree + 2) cnt = 4;
+            if (i >= kBarP && i < kBarP + 4) cnt = 4;
+            if (i >= kBarOfree && i < kBarOfree + 2) cnt = 8;
+            if (i >= kBarEnd && i < kBarEnd + 8) cnt = 2;
             // both tiles release what they share
-            if (PREFIX && i == kBarQfree) cnt = 2;
-            if (!PREFIX && ((i >= kBarKfree && i < kBarKfree + 4) || (i >= kBarVfree && i < kBarVfree + 2))) cnt = 2;
+            if (PREFIX ? i == kBarQfree : i >= kBarFree && i < kBarFree + L::kStages) cnt = 2;
             mbar_init(pipe.bar(i), cnt);
         }
         misc[1] = 0u;
@@ -138,304 +169,314 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
 
     if (warp == kLoadWarp) {
         // ---------------------------------------------------------------- TMA
-        int nq[2] = {0, 0}, nk[4] = {0, 0, 0, 0}, nv[2] = {0, 0};  // copies into each slot
-        if (lane == 0) {
-            bool ok = true;
-            auto tile = [&](uint32_t dst, const CUtensorMap *m, int bar, int y, int z, int w) {
-#pragma unroll
-                for (int c = 0; c < kBlocks; ++c) tma_load_4d(dst + c * kBlk, m, pipe.bar(bar), c * 64, y, z, w);
-            };
-            auto load_kv = [&](int ks, int vs, int k0, bool sink, int hk, int b) {
-                const uint32_t bytes = (uint32_t)(sink ? f.sink_box : kKeys) * D * 2;
-                if (nk[ks] > 0 && !(ok = pipe.wait(kBarKfree + ks, (nk[ks] - 1) & 1))) return;
-                mbar_expect_tx(pipe.bar(kBarKfull + ks), bytes);
-                ++nk[ks];
-                tile(sbase + L::kK + ks * L::kTileBytes, sink ? &tmKs : &tmK, kBarKfull + ks, k0, hk, b);
-                if (nv[vs] > 0 && !(ok = pipe.wait(kBarVfree + vs, (nv[vs] - 1) & 1))) return;
-                mbar_expect_tx(pipe.bar(kBarVfull + vs), bytes);
-                ++nv[vs];
-                tile(sbase + L::kV + vs * L::kTileBytes, sink ? &tmVs : &tmV, kBarVfull + vs, k0, hk, b);
-            };
-            int g = 0;
-            for (int r = 0; ok; ++r) {
-                const int j = item_of_round(r, cta, G);
-                if (j >= f.items) break;
-                const auto it = decode_item<PREFIX>(f, j);
-                if constexpr (PREFIX) {
-                    if (nq[0] > 0 && !(ok = pipe.wait(kBarQfree, (nq[0] - 1) & 1))) break;
-                    mbar_expect_tx(pipe.bar(kBarQfull), (uint32_t)(f.nb * a.G) * D * 2);
-                    ++nq[0];
-                    tile(sbase + L::kQ, &tmQ, kBarQfull, it.h, it.i0, 0);
-                    const int n0 = it.r1[0] - it.r0[0], n1 = it.r1[1] - it.r0[1];
-                    for (int i = 0; i < max(n0, n1) && ok; ++i) {
-                        if (i < n0) load_kv((nv[0] & 1), 0, (it.r0[0] + i) * kKeys, false, it.hk, 0);
-                        if (ok && i < n1) load_kv(2 + (nv[1] & 1), 1, (it.r0[1] + i) * kKeys, false, it.hk, 0);
-                    }
-                } else {
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (it.last(x) < 0) continue;
-                    if (nq[x] > 0 && !(ok = pipe.wait(kBarQfree + x, (nq[x] - 1) & 1))) break;
-                    mbar_expect_tx(pipe.bar(kBarQfull + x), kM * D * 2);
-                    ++nq[x];
-                    tile(sbase + L::kQ + x * L::kTileBytes, &tmQ, kBarQfull + x, it.i0 + x * f.qt, it.h, it.b);
-                }
-                for (int e = it.e0; e < it.e1 && ok; ++e, ++g) {
-                    load_kv(g & 1, g & 1, it.first_key(e), e < it.sp.ns, it.hk, it.b);
-                }
-                }
-            }
-            // what was started lands before the CTA's memory is released
-            for (int x = 0; x < 2; ++x) pipe.drain(kBarQfull + x, nq[x]);
-            for (int x = 0; x < 4; ++x) pipe.drain(kBarKfull + x, nk[x]);
-            for (int x = 0; x < 2; ++x) pipe.drain(kBarVfull + x, nv[x]);
-        }
-        __syncwarp();
-    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-        // ---------------------------------------------------------------- MMA of tile x
-        const int x = warp - kMmaWarp;
-        if (lane == 0) {
-            bool ok = true;
-            int g = 0;   // entries, over all items (prefill)
-            int c = 0;   // tiles of x
-            int n = 0;   // items with tiles of x
-            const uint32_t q = sbase + L::kQ + (PREFIX ? 0 : x * L::kTileBytes);
-            const int bq = PREFIX ? 0 : x;
-            auto run_tile = [&](int ks, uint32_t kpar, int vs, uint32_t vpar, int nkeys, bool first, bool last) {
-                const int n16 = (nkeys + 15) & ~15;
-                const uint32_t kb = sbase + L::kK + ks * L::kTileBytes, vb = sbase + L::kV + vs * L::kTileBytes;
-                if (!(ok = pipe.wait(kBarKfull + ks, kpar))) return;
-                if (c > 0 && !(ok = pipe.wait(kBarPV + x, (c - 1) & 1))) return;
-                tc_fence_after();
-                const uint32_t idS = idesc_bf16(kM, n16, false);
-#pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                    const uint32_t o = (s >> 2) * kBlk + (s & 3) * 32;
-                    mma_ss(tmem + x * 128, smem_desc(q + o, 16, 1024), smem_desc(kb + o, 16, 1024), idS, s > 0);
-                }
-                mma_commit(pipe.bar(kBarS + x));
-                mma_commit(pipe.bar(kBarKfree + ks));
-                if (last) mma_commit(pipe.bar(kBarQfree + bq));
-                if (!(ok = pipe.wait(kBarP + x, c & 1))) return;
-                if (!(ok = pipe.wait(kBarVfull + vs, vpar))) return;
-                if (first && n > 0 && !(ok = pipe.wait(kBarOfree + x, (n - 1) & 1))) return;
-                tc_fence_after();
-                for (int s = 0; s < n16 / 16; ++s)
-                    mma_ts(tmem + 256 + x * 128, tmem + x * 128 + s * 8, smem_desc(vb + s * 2048, kBlk, 1024),
-                           idesc_bf16(kM, D, true), !first || s > 0);
-                mma_commit(pipe.bar(kBarVfree + vs));
-                mma_commit(pipe.bar(kBarPV + x));
-                ++c;
-            };
-            int nqx = 0;
-            for (int r = 0; ok; ++r) {
-                const int j = item_of_round(r, cta, G);
-                if (j >= f.items) break;
-                const auto it = decode_item<PREFIX>(f, j);
-                if constexpr (PREFIX) {
-                    if (!(ok = pipe.wait(kBarQfull, r & 1))) break;
-                    const int nt = it.r1[x] - it.r0[x];
-                    if (nt == 0) {
-                        pipe.arrive(kBarQfree);
-                        continue;
-                    }
-                    tc_fence_after();
-                    for (int i = 0; i < nt && ok; ++i)
-                        run_tile(2 * x + (c & 1), (c >> 1) & 1, x, c & 1, min(kKeys, a.N - (it.r0[x] + i) * kKeys), i == 0,
-                                 i + 1 == nt);
-                    ++n;
-                } else {
-                const int last = it.last(x);
-                if (last >= 0) {
-                    if (!(ok = pipe.wait(kBarQfull + x, nqx & 1))) break;
-                    ++nqx;
-                    tc_fence_after();
-                }
-                bool first = true;
-                for (int e = it.e0; e < it.e1 && ok; ++e, ++g) {
-                    const int nk = it.keys(x, e), s = g & 1;
-                    const uint32_t par = (g >> 1) & 1;
-                    if (nk > 0) {
-                        run_tile(s, par, s, par, nk, first, e == last);
-                        first = false;
-                    } else {  // not this tile's: release it once it has landed
-                        if (!(ok = pipe.wait(kBarKfull + s, par))) break;
-                        pipe.arrive(kBarKfree + s);
-                        if (!(ok = pipe.wait(kBarVfull + s, par))) break;
-                        pipe.arrive(kBarVfree + s);
-                    }
-                }
-                if (last >= 0) ++n;
-                }
-            }
-            mma_commit(pipe.bar(kBarDrain + x));  // what was issued completes before TMEM is released
-            pipe.drain(kBarDrain + x, 1);
-        }
-        __syncwarp();
-    } else if (warp < 8) {
-        // ---------------------------------------------------------------- softmax rows of tile x
-        const int x = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const uint32_t s_col = tmem + lanes + x * 128, o_col = tmem + lanes + 256 + x * 128;
-        const float scale2 = a.scale * kLog2e;
+        int nq[2] = {0, 0};
         bool ok = true;
-        int c = 0;
+        auto tile = [&](uint32_t dst, int blk, const CUtensorMap *m, int bar, int y, int z, int w) {
+#pragma unroll
+            for (int c = 0; c < kBlocks; ++c) tma_load_4d(dst + c * blk, m, pipe.bar(bar), c * 64, y, z, w);
+        };
+        // ring i: its stages, the next one and how often the ring went round
+        int st[2] = {0, 0};
+        uint32_t round[2] = {0, 0};
+        auto load_kv = [&](int ring, int k0, bool sink, int hk, int b) {
+            const int s = ring * kRing + st[ring];
+            if (round[ring] > 0 && !(ok = pipe.wait_warp(kBarFree + s, (round[ring] - 1) & 1))) return;
+            if (elect_one()) {
+                mbar_expect_tx(pipe.bar(kBarFull + s), 2u * (sink ? f.sink_box : kKeys) * D * 2);
+                tile(sbase + L::kK + s * L::kY, kYBlk, sink ? &tmKs : &tmK, kBarFull + s, k0, hk, b);
+                tile(sbase + L::kV + s * L::kY, kYBlk, sink ? &tmVs : &tmV, kBarFull + s, k0, hk, b);
+            }
+            __syncwarp();
+            if (++st[ring] == kRing) {
+                st[ring] = 0;
+                ++round[ring];
+            }
+        };
         for (int r = 0; ok; ++r) {
             const int j = item_of_round(r, cta, G);
             if (j >= f.items) break;
             const auto it = decode_item<PREFIX>(f, j);
+            if constexpr (PREFIX) {
+                if (nq[0] > 0 && !(ok = pipe.wait_warp(kBarQfree, (nq[0] - 1) & 1))) break;
+                if (elect_one()) {
+                    mbar_expect_tx(pipe.bar(kBarQfull), (uint32_t)(f.nb * a.G) * D * 2);
+                    tile(sbase + L::kQ, kXBlk, &tmQ, kBarQfull, it.h, it.i0, 0);
+                }
+                __syncwarp();
+                ++nq[0];
+                const int n0 = it.r1 - it.r0, n1 = it.r2 - it.r1;
+                for (int i = 0; i < max(n0, n1) && ok; ++i) {
+                    if (i < n0) load_kv(0, (it.r0 + i) * kKeys, false, it.hk, 0);
+                    if (ok && i < n1) load_kv(1, (it.r1 + i) * kKeys, false, it.hk, 0);
+                }
+            } else {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (own_tiles<PREFIX>(it, x).n == 0) continue;
+                    if (nq[x] > 0 && !(ok = pipe.wait_warp(kBarQfree + x, (nq[x] - 1) & 1))) break;
+                    if (elect_one()) {
+                        mbar_expect_tx(pipe.bar(kBarQfull + x), L::kX);
+                        tile(sbase + L::kQ + x * L::kX, kXBlk, &tmQ, kBarQfull + x, it.i0 + x * f.qt, it.h, it.b);
+                    }
+                    __syncwarp();
+                    ++nq[x];
+                }
+                for (int e = it.e0; e < it.e1 && ok; ++e) load_kv(0, it.first_key(e), e < it.sp.ns, it.hk, it.b);
+            }
+        }
+        // what was started lands before the CTA's memory is released
+        if (lane == 0) {
+            for (int x = 0; x < 2; ++x) pipe.drain(kBarQfull + x, nq[x]);
+            for (int ring = 0; ring < (PREFIX ? 2 : 1); ++ring)
+                for (int s = 0; s < kRing; ++s)
+                    pipe.drain(kBarFull + ring * kRing + s, (int)round[ring] + (s < st[ring] ? 1 : 0));
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+        // ---------------------------------------------------------------- MMA of tile x
+        const int x = warp - kMmaWarp, ring0 = PREFIX ? x * kRing : 0, bq = PREFIX ? 0 : x;
+        const uint64_t qd = tile_desc(sbase + L::kQ + (PREFIX ? 0 : x * L::kX), 16);
+        const uint64_t kd0 = tile_desc(sbase + L::kK + ring0 * L::kY, 16), vd0 = tile_desc(sbase + L::kV + ring0 * L::kY, kYBlk);
+        bool ok = true;
+        int c = 0, n = 0;     // tiles and items of x
+        int st = 0;           // ring: the next stage and its phase
+        uint32_t ph = 0;
+        auto next_stage = [&] {
+            if (++st == kRing) {
+                st = 0;
+                ph ^= 1u;
+            }
+        };
+        for (int r = 0; ok; ++r) {
+            const int j = item_of_round(r, cta, G);
+            if (j >= f.items) break;
+            const auto it = decode_item<PREFIX>(f, j);
+            const Own own = own_tiles<PREFIX>(it, x);
+            int e = 0, e_end = 0;  // prefill: the next entry in the ring
+            if constexpr (!PREFIX) {
+                e = it.e0;
+                e_end = it.e1;
+            }
+            // entries of the ring that are not this tile's: released once they have landed
+            auto skip_to = [&](int to) {
+                for (; e < to && ok; ++e) {
+                    if (!(ok = pipe.wait_warp(kBarFull + st, ph))) return;
+                    if (lane == 0) pipe.arrive(kBarFree + st);
+                    next_stage();
+                }
+            };
+            if (PREFIX || own.n > 0) {
+                if (!(ok = pipe.wait_warp(kBarQfull + bq, (PREFIX ? r : n) & 1))) break;
+                if (PREFIX && own.n == 0 && lane == 0) pipe.arrive(kBarQfree);
+            }
+            int s_cur = 0, s_next = 0, n_cur = 0, n_next = 0;  // stage and keys of tile i and of tile i + 1
+            auto issue_s = [&](int i) {  // S of tile i into buffer (c + i) % 2
+                const int en = own.entry(i), cc = c + i, buf = 2 * x + (cc & 1);
+                if constexpr (PREFIX) {
+                    n_next = min(kKeys, a.N - en * kKeys);
+                } else {
+                    skip_to(en);
+                    ++e;
+                    n_next = it.keys(x, en);
+                }
+                if (!ok || !(ok = pipe.wait_warp(kBarFull + ring0 + st, ph))) return;
+                if (cc >= 2 && !(ok = pipe.wait_warp(kBarPV + buf, ((cc >> 1) - 1) & 1))) return;
+                tc_fence_after();
+                const uint32_t id = idesc_bf16(kM, (n_next + 15) & ~15, false);
+                const uint64_t kd = kd0 + st * (L::kY / 16);
+                if (elect_one()) {
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s)
+                        mma_ss(tmem + buf * 64, qd + ((s >> 2) * kXBlk + (s & 3) * 32) / 16,
+                               kd + ((s >> 2) * kYBlk + (s & 3) * 32) / 16, id, s > 0);
+                    mma_commit(pipe.bar(kBarS + buf));
+                    if (i + 1 == own.n) mma_commit(pipe.bar(kBarQfree + bq));
+                }
+                __syncwarp();
+                s_next = st;
+                next_stage();
+            };
+            if (own.n > 0) issue_s(0);
+            for (int i = 0; i < own.n && ok; ++i) {
+                s_cur = s_next;
+                n_cur = n_next;
+                if (i + 1 < own.n) issue_s(i + 1);
+                const int cc = c + i, buf = 2 * x + (cc & 1);
+                if (!ok || !(ok = pipe.wait_warp(kBarP + buf, (cc >> 1) & 1))) break;
+                if (i == 0 && n > 0 && !(ok = pipe.wait_warp(kBarOfree + x, (n - 1) & 1))) break;
+                tc_fence_after();
+                const int k16 = (n_cur + 15) / 16;
+                const uint64_t vd = vd0 + s_cur * (L::kY / 16);
+                if (elect_one()) {
+#pragma unroll
+                    for (int s = 0; s < kKeys / 16; ++s)
+                        if (s < k16)
+                            mma_ts(tmem + 256 + x * 128, tmem + buf * 64 + s * 8, vd + s * (2048 / 16),
+                                   idesc_bf16(kM, D, true), i > 0 || s > 0);
+                    mma_commit(pipe.bar(kBarPV + buf));
+                    mma_commit(pipe.bar(kBarFree + ring0 + s_cur));
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            skip_to(e_end);
+            c += own.n;
+            if (own.n > 0) ++n;
+        }
+        if (elect_one()) {
+            mma_commit(pipe.bar(kBarDrain + x));  // what was issued completes before TMEM is released
+            pipe.drain(kBarDrain + x, 1);
+        }
+        __syncwarp();
+    } else if (warp < 16) {
+        // ---------------------------------------------------------------- softmax rows of tile x
+        const int x = warp >> 3, w = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane, pair = 4 * x + quad;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        const uint32_t s_col = tmem + lanes + x * 128 + w * 64, o_col = tmem + lanes + 256 + x * 128;
+        float *refs = reinterpret_cast<float *>(smem + L::kRef) + x * kM + row;
+        float2 *ends = reinterpret_cast<float2 *>(smem + L::kEnd) + x * 2 * kM + row;  // + item parity * 4 kM + warpgroup * kM
+        const float scale2 = a.scale * kLog2e;
+        const float2 scale22 = make_float2(scale2, scale2);
+        bool ok = true;
+        int c = 0, n_items = 0;  // tiles and items of x
+        for (int r = 0; ok; ++r) {
+            const int j = item_of_round(r, cta, G);
+            if (j >= f.items) break;
+            const auto it = decode_item<PREFIX>(f, j);
+            const Own own = own_tiles<PREFIX>(it, x);
             int b, h, i, t;
             bool have;
-            int first_e, end_e;
             if constexpr (PREFIX) {
-                first_e = it.r0[x];
-                end_e = it.r1[x];
                 b = it.i0 + row / a.G;
                 h = it.h + row % a.G;
                 i = 0;
                 t = a.N;
                 have = row < f.nb * a.G && b < a.B && (x == 0 || it.hasB);
             } else {
-                first_e = it.e0;
-                end_e = it.e1;
                 b = it.b;
                 h = it.h + row / f.qt;
                 i = it.i0 + x * f.qt + row % f.qt;
                 t = a.N - a.Lq + i;
                 have = i < a.Lq;
             }
-            float m = -INFINITY, l = 0.f;
-            bool any_tile = false;
-            for (int e = first_e; e < end_e; ++e) {
+            float m = -INFINITY, l = 0.f;  // the reference of this warpgroup's last tile, and its sum
+            for (int k = (c ^ w) & 1; k < own.n; k += 2) {  // tiles c + k of this warpgroup's parity
+                const int cc = c + k;
                 int n, lo, hi, as;  // visible columns: [lo, hi) and [0, as)
                 if constexpr (PREFIX) {
-                    n = hi = min(kKeys, a.N - e * kKeys);
+                    n = hi = min(kKeys, a.N - own.entry(k) * kKeys);
                     lo = as = 0;
                 } else {
+                    const int e = own.entry(k);
                     n = it.keys(x, e);
-                    if (n <= 0) continue;
                     it.columns(e, n, t, a.W, &lo, &hi, &as);
                     if (!have) hi = as = 0;
                 }
-                any_tile = true;
                 const bool full = __all_sync(kFull, lo <= 0 && hi == kKeys);
-                if (!(ok = pipe.wait_warp(kBarS + x, c & 1))) break;
+                if (!(ok = pipe.wait_warp(kBarS + 2 * x + w, (cc >> 1) & 1))) break;
                 tc_fence_after();
+                uint32_t s[64];
+                tmem_ld32(s_col, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                if (n > 32) tmem_ld32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+                tmem_wait_ld();
+                if (!full) {
+                    const uint32_t mk0 = range_bits(lo, hi, 0) | range_bits(0, as, 0);
+                    const uint32_t mk1 = range_bits(lo, hi, 32) | range_bits(0, as, 32);
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) {
+                        s[q] = (mk0 >> q) & 1u ? s[q] : __float_as_uint(-INFINITY);
+                        s[32 + q] = (mk1 >> q) & 1u ? s[32 + q] : __float_as_uint(-INFINITY);
+                    }
+                }
                 float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
-                uint32_t seen = 0;  // 32-column chunks that some row of the warp sees
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    const uint32_t mk = full ? kFull : range_bits(lo, hi, ch * 32) | range_bits(0, as, ch * 32);
-                    if (!__any_sync(kFull, mk != 0)) continue;
-                    seen |= 1u << ch;
-                    uint32_t s[32];
-                    tmem_ld32(s_col + ch * 32, s);
-                    tmem_wait_ld();
-                    if (!full) {
-#pragma unroll
-                        for (int q = 0; q < 32; ++q) s[q] = (mk >> q) & 1u ? s[q] : __float_as_uint(-INFINITY);
-                    }
-#pragma unroll
-                    for (int q = 0; q < 32; q += 8) {
-                        m0 = fmax3(m0, __uint_as_float(s[q]), __uint_as_float(s[q + 1]));
-                        m1 = fmax3(m1, __uint_as_float(s[q + 2]), __uint_as_float(s[q + 3]));
-                        m2 = fmax3(m2, __uint_as_float(s[q + 4]), __uint_as_float(s[q + 5]));
-                        m3 = fmax3(m3, __uint_as_float(s[q + 6]), __uint_as_float(s[q + 7]));
-                    }
+                for (int q = 0; q < 64; q += 8) {
+                    m0 = fmax3(m0, __uint_as_float(s[q]), __uint_as_float(s[q + 1]));
+                    m1 = fmax3(m1, __uint_as_float(s[q + 2]), __uint_as_float(s[q + 3]));
+                    m2 = fmax3(m2, __uint_as_float(s[q + 4]), __uint_as_float(s[q + 5]));
+                    m3 = fmax3(m3, __uint_as_float(s[q + 6]), __uint_as_float(s[q + 7]));
                 }
-                float mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
-                if (scale2 < 0.f) {  // the largest logit is the smallest product: no reference from the maximum
-                    mt = INFINITY;
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        if (!((seen >> ch) & 1u)) continue;
-                        const uint32_t mk = full ? kFull : range_bits(lo, hi, ch * 32) | range_bits(0, as, ch * 32);
-                        uint32_t s[32];
-                        tmem_ld32(s_col + ch * 32, s);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int q = 0; q < 32; ++q) mt = fminf(mt, (mk >> q) & 1u ? __uint_as_float(s[q]) : INFINITY);
-                    }
-                }
-                const bool none = isinf(mt);  // no visible key in this tile
-                mt = none ? -INFINITY : mt * scale2;
-                const bool raise = !none && (m == -INFINITY || mt > m + 8.f);
-                const float fac = raise ? exp2_ftz(m - mt) : 1.f;  // 0 when m is -inf
-                if (__any_sync(kFull, raise && l > 0.f)) {
-                    // S of this tile was issued after the PV of the one before had completed
+                const float mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * scale2;
+                // the row's reference after the tile before, and after this one
+                if (cc > 0 && !(ok = pipe.wait_warp(kBarRef + pair, (cc - 1) & 1))) break;
+                const float ref = k > 0 ? *refs : -INFINITY;
+                const bool raise = mt > ref + 8.f || (ref == -INFINITY && mt != -INFINITY);
+                const float m_new = raise ? mt : ref;
+                *refs = m_new;
+                __syncwarp();
+                if (lane == 0) pipe.arrive(kBarRef + pair);
+                if (__any_sync(kFull, raise && ref != -INFINITY)) {
+                    // O holds the tiles before this one
+                    if (!(ok = pipe.wait_warp(kBarPV + 2 * x + (w ^ 1), ((cc - 1) >> 1) & 1))) break;
+                    tc_fence_after();
+                    const float fac = raise && ref != -INFINITY ? exp2_ftz(ref - m_new) : 1.f;
 #pragma unroll 1
-                    for (int part = 0; part < D / 32; ++part) {
-                        uint32_t o[32];
-                        tmem_ld32(o_col + part * 32, o);
+                    for (int part = 0; part < D / 8; ++part) {
+                        uint32_t o[8];
+                        tmem_ld8(o_col + part * 8, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * fac);
-                        tmem_st32(o_col + part * 32, o);
+                        for (int q = 0; q < 8; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * fac);
+                        tmem_st8(o_col + part * 8, o);
                     }
                 }
-                if (raise) {
-                    l *= fac;
-                    m = mt;
+                if (m_new != m) {
+                    l = l > 0.f ? l * exp2_ftz(m - m_new) : 0.f;
+                    m = m_new;
                 }
                 const float nb = m == -INFINITY ? 0.f : -m;
-                float z0 = 0.f, z1 = 0.f, z2 = 0.f, z3 = 0.f;
+                const float2 nb2 = make_float2(nb, nb);
+                float2 z0 = make_float2(0.f, 0.f), z1 = z0;
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    if (ch * 32 >= n) continue;
-                    uint32_t p[16];
-                    if ((seen >> ch) & 1u) {
-                        const uint32_t mk = full ? kFull : range_bits(lo, hi, ch * 32) | range_bits(0, as, ch * 32);
-                        uint32_t s[32];
-                        tmem_ld32(s_col + ch * 32, s);
-                        tmem_wait_ld();
+                for (int q = 0; q < 64; q += 8) {
+                    float2 v[4];
 #pragma unroll
-                        for (int q = 0; q < 32; q += 4) {
-                            float v[4];
+                    for (int u = 0; u < 4; ++u) v[u] = fma2(as2(s + q + 2 * u), scale22, nb2);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) v[k] = fmaf(__uint_as_float(s[q + k]), scale2, nb);
-                            if (!full) {
+                    for (int u = 0; u < 3; ++u) v[u] = make_float2(exp2_ftz(v[u].x), exp2_ftz(v[u].y));
+                    v[3] = exp2_fma2(v[3]);
+                    z0 = add2(z0, add2(v[0], v[1]));
+                    z1 = add2(z1, add2(v[2], v[3]));
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) v[k] = (mk >> (q + k)) & 1u ? v[k] : -INFINITY;
-                            }
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) v[k] = exp2_ftz(v[k]);
-                            z0 += v[0];
-                            z1 += v[1];
-                            z2 += v[2];
-                            z3 += v[3];
-                            p[q / 2] = pack_bf16(v[0], v[1]);
-                            p[q / 2 + 1] = pack_bf16(v[2], v[3]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) p[q] = 0u;
-                    }
-                    tmem_st16(s_col + ch * 16, p);  // columns whose S has been read
+                    for (int u = 0; u < 4; ++u) s[q / 2 + u] = pack_bf16(v[u].x, v[u].y);  // s[q / 2 ..] has been read
                 }
-                l += (z0 + z1) + (z2 + z3);
+                l += (z0.x + z0.y) + (z1.x + z1.y);
+                tmem_st32(s_col, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) pipe.arrive(kBarP + x);
-                ++c;
+                if (lane == 0) pipe.arrive(kBarP + 2 * x + w);
             }
             if (!ok) break;
-            // ---- O / l and lse
-            if (any_tile) {
-                if (!(ok = pipe.wait_warp(kBarPV + x, (c - 1) & 1))) break;
+            c += own.n;
+            // ---- O / l and lse: each warpgroup half of the columns
+            if (own.n > 0) {
+                float2 *e = ends + (n_items & 1) * 4 * kM;
+                e[w * kM] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0) pipe.arrive(kBarEnd + pair);
+                if (!(ok = pipe.wait_warp(kBarEnd + pair, n_items & 1))) break;
+                const float2 y = e[(w ^ 1) * kM];
+                const float mf = fmaxf(m, y.x);  // references only rise
+                if (mf != -INFINITY) l = l * exp2_ftz(m - mf) + y.y * exp2_ftz(y.x - mf);
+                m = mf;
+                ++n_items;
+                if (!(ok = pipe.wait_warp(kBarPV + 2 * x + ((c - 1) & 1), ((c - 1) >> 1) & 1))) break;
                 tc_fence_after();
             }
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            const float lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            const bool some = m != -INFINITY && l > 0.f;  // a split may hold nothing that the row sees
+            const float inv = some ? 1.f / l : 0.f;
+            const float lse = some ? (m + log2f(l)) * kLn2 : -INFINITY;
             const int64_t place = ((int64_t)b * a.H + h) * a.Lq + i;
             const int slot = PREFIX ? 2 * it.split + x : it.split;
-            bf16 *orow = static_cast<bf16 *>(a.O.ptr) + b * a.O.sb + h * a.O.sh + (int64_t)i * a.O.st;
-            float *prow = a.part_o ? a.part_o + (place * a.slots + slot) * D : nullptr;
+            constexpr int kHalf = D / 2;
+            bf16 *orow = static_cast<bf16 *>(a.O.ptr) + b * a.O.sb + h * a.O.sh + (int64_t)i * a.O.st + w * kHalf;
+            float *prow = a.part_o ? a.part_o + (place * a.slots + slot) * D + w * kHalf : nullptr;
 #pragma unroll
-            for (int part = 0; part < D / 32; ++part) {
+            for (int part = 0; part < kHalf / 32; ++part) {
                 uint32_t o[32];
-                if (any_tile) {  // every lane loads
-                    tmem_ld32(o_col + part * 32, o);
+                if (own.n > 0) {  // every lane loads
+                    tmem_ld32(o_col + w * kHalf + part * 32, o);
                     tmem_wait_ld();
                 } else {
 #pragma unroll
@@ -461,11 +502,11 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                     }
                 }
             }
-            if (have) {
+            if (have && w == 0) {
                 if (prow) a.part_lse[place * a.slots + slot] = lse;
                 else if (a.lse) a.lse[place] = lse;
             }
-            if (any_tile) {
+            if (own.n > 0) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) pipe.arrive(kBarOfree + x);
@@ -496,7 +537,7 @@ hils_status run(const FwdTc &f, const CUtensorMap (&m)[5], cudaStream_t s) {
 }  // namespace
 
 bool launch_sink_forward_tc(hils_dtype dt, int d, const SinkArgs &a, cudaStream_t s, hils_status *st) {
-    if (dt != HILS_BF16 || a.N == 0) return false;
+    if (dt != HILS_BF16 || a.N == 0 || !(a.scale > 0.f)) return false;  // (a negative scale: the largest product is not the largest logit)
     const int Hk = a.H / a.G;
     FwdTc f{};
     f.a = a;

@@ -20,7 +20,9 @@ struct Pipe {
     __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
         const uint32_t b = bar(i);
         if (wait_ns > 0) {
-            if (mbar_try_wait(b, parity)) return true;
+            // a short wait never reads the timer
+            for (int it = 0; it < 64; ++it)
+                if (mbar_try_wait(b, parity)) return true;
             const uint64_t t0 = global_ns();
             for (int it = 0;; ++it) {
                 if (mbar_try_wait(b, parity)) return true;
@@ -40,6 +42,9 @@ struct Pipe {
     }
     __device__ __forceinline__ void arrive(int i) const {
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar(i)) : "memory");
+    }
+    __device__ __forceinline__ void arrive(int i, uint32_t count) const {
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar(i)), "r"(count) : "memory");
     }
     // bounded wait for this CTA's own copies or MMAs while it stops: `uses` phases of barrier i
     __device__ __forceinline__ void drain(int i, int uses) const {
