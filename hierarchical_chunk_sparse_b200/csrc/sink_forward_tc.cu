@@ -21,11 +21,10 @@
 //                tile's maximum passes it by more than 8 in log2 units (P <= 2^8: exact in the
 //                float32 sums, rounded in bf16 as well as below 1).
 //   warps 16, 17 tcgen05.mma of A, B;   warp 18  TMA.
-// S is double-buffered: S of the next tile is computed during the softmax of this one, once
-// the PV that read the buffer has completed. A quarter of the exponentials is evaluated on the
-// FMA pipe, since the MUFU's 16 a cycle would take as long as the products.
-// TMEM: S_A [0,64), [64,128); S_B [128,192), [192,256); O_A [256,384), O_B [384,512).
-#include "fast_math.cuh"
+// A softmax warp takes its 64 scores into registers and hands S back before anything else, and
+// P has two buffers of its own, so that neither S of the next tile nor the next softmax waits
+// for a PV. The MMA warp issues whatever product is ready, over the borders of items.
+// TMEM of tile x, from 128 x: S [0,64), P [64,96), [96,128); O_A [256,384), O_B [384,512).
 #include "sink_tc.cuh"
 
 namespace hils {
@@ -41,16 +40,19 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 enum {
     kBarQfull = 0,    // + tile (prefix: 0 for both)
     kBarQfree = 2,    // + tile
-    kBarFull = 4,     // + stage: K and V landed
-    kBarFree = 10,    // + stage: the products that read them completed
-    kBarS = 16,       // + 2 tile + buffer: S written
-    kBarP = 20,       // + 2 tile + buffer: P written over it (4 warps)
-    kBarPV = 24,      // + 2 tile + buffer: its PV, and every MMA before that, completed
-    kBarOfree = 28,   // + tile: O read (8 warps)
-    kBarRef = 30,     // + 4 tile + quadrant: the rows' reference after a tile (1 warp)
-    kBarEnd = 38,     // + 4 tile + quadrant: both warpgroups' sums of an item (2 warps)
-    kBarDrain = 46,   // + tile
-    kNumBars = 48
+    kBarKfull = 4,    // + stage
+    kBarKfree = 10,   // + stage: the S products that read it completed
+    kBarVfull = 16,   // + stage
+    kBarVfree = 20,   // + stage: the PV products that read it completed
+    kBarS = 24,       // + 2 tile + warpgroup: S written
+    kBarSfree = 28,   // + tile: S read (4 warps)
+    kBarP = 30,       // + 2 tile + buffer: P written (4 warps)
+    kBarPV = 34,      // + 2 tile + buffer: its PV, and every MMA before that, completed
+    kBarOfree = 38,   // + tile: O read (8 warps)
+    kBarRef = 40,     // + 4 tile + quadrant: the rows' reference after a tile (1 warp)
+    kBarEnd = 48,     // + 4 tile + quadrant: both warpgroups' sums of an item (2 warps)
+    kBarDrain = 56,   // + tile
+    kNumBars = 58
 };
 
 struct FwdTc {
@@ -63,12 +65,25 @@ struct FwdTc {
 template <int D, bool PREFIX>
 struct Smem {
     static constexpr int kX = kM * D * 2, kY = kKeys * D * 2;
-    static constexpr int kStages = 4;  // prefix: two for each range
-    static constexpr int kQ = 0, kK = (PREFIX ? 1 : 2) * kX, kV = kK + kStages * kY;
-    static constexpr int kRef = kV + kStages * kY;   // [2 tiles][128] references
-    static constexpr int kEnd = kRef + 2 * kM * 4;   // [2 by item][2 tiles][2 warpgroups][128] reference, sum
-    static constexpr int kBars = kEnd + 8 * kM * 8, kMisc = kBars + 8 * kNumBars;
+    // stages of one ring: one ring of each of K and V for both tiles, for a prefix one for each
+    static constexpr int kKst = PREFIX ? 3 : 4, kVst = PREFIX ? 2 : 4, kRings = PREFIX ? 2 : 1;
+    static constexpr int kQ = 0, kK = (PREFIX ? 1 : 2) * kX, kV = kK + kRings * kKst * kY;
+    static constexpr int kRef = kV + kRings * kVst * kY;  // [2 tiles][128] references
+    static constexpr int kEnd = kRef + 2 * kM * 4;        // [2 tiles][2 warpgroups][128] reference, sum
+    static constexpr int kBars = kEnd + 4 * kM * 8, kMisc = kBars + 8 * kNumBars;
     static constexpr int kBytes = kMisc + 16;
+};
+
+// The next stage of a ring and the phase of its full barrier.
+struct Ring {
+    int st = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++st == stages) {
+            st = 0;
+            ph ^= 1u;
+        }
+    }
 };
 
 // The key tiles of one row tile x of an item, in order: entries [a0, a1), then [b0, b1).
@@ -137,7 +152,6 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
     using L = Smem<D, PREFIX>;
     constexpr int kBlocks = D / 64;  // 64-column blocks of a row tile
     constexpr int kXBlk = kM * 128, kYBlk = kKeys * 128;
-    constexpr int kRing = PREFIX ? L::kStages / 2 : L::kStages;  // stages of one ring
     const SinkArgs &a = f.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = smem_u32(smem);
@@ -151,11 +165,11 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i) {
             uint32_t cnt = 1;
-            if (i >= kBarP && i < kBarP + 4) cnt = 4;
+            if ((i >= kBarP && i < kBarP + 4) || (i >= kBarSfree && i < kBarSfree + 2)) cnt = 4;
             if (i >= kBarOfree && i < kBarOfree + 2) cnt = 8;
             if (i >= kBarEnd && i < kBarEnd + 8) cnt = 2;
             // both tiles release what they share
-            if (PREFIX ? i == kBarQfree : i >= kBarFree && i < kBarFree + L::kStages) cnt = 2;
+            if (PREFIX ? i == kBarQfree : (i >= kBarKfree && i < kBarKfree + 6) || (i >= kBarVfree && i < kBarVfree + 4)) cnt = 2;
             mbar_init(pipe.bar(i), cnt);
         }
         misc[1] = 0u;
@@ -175,22 +189,29 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
 #pragma unroll
             for (int c = 0; c < kBlocks; ++c) tma_load_4d(dst + c * blk, m, pipe.bar(bar), c * 64, y, z, w);
         };
-        // ring i: its stages, the next one and how often the ring went round
-        int st[2] = {0, 0};
-        uint32_t round[2] = {0, 0};
+        Ring kr[2], vr[2];  // of each ring: the next stage
+        int loads[2] = {0, 0};
         auto load_kv = [&](int ring, int k0, bool sink, int hk, int b) {
-            const int s = ring * kRing + st[ring];
-            if (round[ring] > 0 && !(ok = pipe.wait_warp(kBarFree + s, (round[ring] - 1) & 1))) return;
+            const int ks = ring * L::kKst + kr[ring].st, vs = ring * L::kVst + vr[ring].st;
+            const uint32_t bytes = (uint32_t)(sink ? f.sink_box : kKeys) * D * 2;
+            if (loads[ring] >= L::kKst && !(ok = pipe.wait_warp(kBarKfree + ks, kr[ring].ph ^ 1u))) return;
             if (elect_one()) {
-                mbar_expect_tx(pipe.bar(kBarFull + s), 2u * (sink ? f.sink_box : kKeys) * D * 2);
-                tile(sbase + L::kK + s * L::kY, kYBlk, sink ? &tmKs : &tmK, kBarFull + s, k0, hk, b);
-                tile(sbase + L::kV + s * L::kY, kYBlk, sink ? &tmVs : &tmV, kBarFull + s, k0, hk, b);
+                mbar_expect_tx(pipe.bar(kBarKfull + ks), bytes);
+                tile(sbase + L::kK + ks * L::kY, kYBlk, sink ? &tmKs : &tmK, kBarKfull + ks, k0, hk, b);
             }
             __syncwarp();
-            if (++st[ring] == kRing) {
-                st[ring] = 0;
-                ++round[ring];
+            kr[ring].next(L::kKst);
+            if (loads[ring] >= L::kVst && !(ok = pipe.wait_warp(kBarVfree + vs, vr[ring].ph ^ 1u))) {
+                ++loads[ring];
+                return;
             }
+            if (elect_one()) {
+                mbar_expect_tx(pipe.bar(kBarVfull + vs), bytes);
+                tile(sbase + L::kV + vs * L::kY, kYBlk, sink ? &tmVs : &tmV, kBarVfull + vs, k0, hk, b);
+            }
+            __syncwarp();
+            vr[ring].next(L::kVst);
+            ++loads[ring];
         };
         for (int r = 0; ok; ++r) {
             const int j = item_of_round(r, cta, G);
@@ -227,101 +248,132 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
         // what was started lands before the CTA's memory is released
         if (lane == 0) {
             for (int x = 0; x < 2; ++x) pipe.drain(kBarQfull + x, nq[x]);
-            for (int ring = 0; ring < (PREFIX ? 2 : 1); ++ring)
-                for (int s = 0; s < kRing; ++s)
-                    pipe.drain(kBarFull + ring * kRing + s, (int)round[ring] + (s < st[ring] ? 1 : 0));
+            for (int ring = 0; ring < L::kRings; ++ring) {  // (the last load may lack its V: then 100 ms at most)
+                for (int q = 0; q < L::kKst; ++q)
+                    pipe.drain(kBarKfull + ring * L::kKst + q, loads[ring] > q ? (loads[ring] - q + L::kKst - 1) / L::kKst : 0);
+                for (int q = 0; q < L::kVst; ++q)
+                    pipe.drain(kBarVfull + ring * L::kVst + q, loads[ring] > q ? (loads[ring] - q + L::kVst - 1) / L::kVst : 0);
+            }
         }
         __syncwarp();
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         // ---------------------------------------------------------------- MMA of tile x
-        const int x = warp - kMmaWarp, ring0 = PREFIX ? x * kRing : 0, bq = PREFIX ? 0 : x;
+        const int x = warp - kMmaWarp, bq = PREFIX ? 0 : x;
+        const int k_ring = PREFIX ? x * L::kKst : 0, v_ring = PREFIX ? x * L::kVst : 0;
         const uint64_t qd = tile_desc(sbase + L::kQ + (PREFIX ? 0 : x * L::kX), 16);
-        const uint64_t kd0 = tile_desc(sbase + L::kK + ring0 * L::kY, 16), vd0 = tile_desc(sbase + L::kV + ring0 * L::kY, kYBlk);
-        bool ok = true;
-        int c = 0, n = 0;     // tiles and items of x
-        int st = 0;           // ring: the next stage and its phase
-        uint32_t ph = 0;
-        auto next_stage = [&] {
-            if (++st == kRing) {
-                st = 0;
-                ph ^= 1u;
-            }
+        const uint64_t kd0 = tile_desc(sbase + L::kK + k_ring * L::kY, 16), vd0 = tile_desc(sbase + L::kV + v_ring * L::kY, kYBlk);
+        // Two cursors over the tiles of x, for S and for PV: c tiles and n items of x are done
+        struct Cursor {
+            decltype(decode_item<PREFIX>(f, 0)) it;
+            Own own{0, 0, 0, 0};
+            Ring ring;
+            int r = -1, i = 0, e = 0, e_end = 0, c = 0, n = 0;
+            bool done = false;
         };
-        for (int r = 0; ok; ++r) {
-            const int j = item_of_round(r, cta, G);
-            if (j >= f.items) break;
-            const auto it = decode_item<PREFIX>(f, j);
-            const Own own = own_tiles<PREFIX>(it, x);
-            int e = 0, e_end = 0;  // prefill: the next entry in the ring
-            if constexpr (!PREFIX) {
-                e = it.e0;
-                e_end = it.e1;
-            }
-            // entries of the ring that are not this tile's: released once they have landed
-            auto skip_to = [&](int to) {
-                for (; e < to && ok; ++e) {
-                    if (!(ok = pipe.wait_warp(kBarFull + st, ph))) return;
-                    if (lane == 0) pipe.arrive(kBarFree + st);
-                    next_stage();
+        Cursor S, V;
+        bool ok = true;
+        // Brings a cursor to its next tile; false if there is none, or if entries of the ring that
+        // are not this tile's have to land first, to be released.
+        auto at_tile = [&](Cursor &u, int full, int free, int stages) -> bool {
+            while (!u.done) {
+                const bool more = u.i < u.own.n;
+                const int to = more ? u.own.entry(u.i) : u.e_end;
+                while (!PREFIX && u.e < to) {
+                    if (!pipe.ready(full + u.ring.st, u.ring.ph)) return false;
+                    if (lane == 0) pipe.arrive(free + u.ring.st);
+                    u.ring.next(stages);
+                    ++u.e;
                 }
-            };
-            if (PREFIX || own.n > 0) {
-                if (!(ok = pipe.wait_warp(kBarQfull + bq, (PREFIX ? r : n) & 1))) break;
-                if (PREFIX && own.n == 0 && lane == 0) pipe.arrive(kBarQfree);
-            }
-            int s_cur = 0, s_next = 0, n_cur = 0, n_next = 0;  // stage and keys of tile i and of tile i + 1
-            auto issue_s = [&](int i) {  // S of tile i into buffer (c + i) % 2
-                const int en = own.entry(i), cc = c + i, buf = 2 * x + (cc & 1);
-                if constexpr (PREFIX) {
-                    n_next = min(kKeys, a.N - en * kKeys);
-                } else {
-                    skip_to(en);
-                    ++e;
-                    n_next = it.keys(x, en);
+                if (more) return true;
+                if (PREFIX && u.own.n == 0 && &u == &S && u.r >= 0) {  // a range that is not there: its queries are let go
+                    if (!pipe.ready(kBarQfull, u.r & 1)) return false;
+                    if (lane == 0) pipe.arrive(kBarQfree);
                 }
-                if (!ok || !(ok = pipe.wait_warp(kBarFull + ring0 + st, ph))) return;
-                if (cc >= 2 && !(ok = pipe.wait_warp(kBarPV + buf, ((cc >> 1) - 1) & 1))) return;
-                tc_fence_after();
-                const uint32_t id = idesc_bf16(kM, (n_next + 15) & ~15, false);
-                const uint64_t kd = kd0 + st * (L::kY / 16);
-                if (elect_one()) {
+                if (u.own.n > 0) ++u.n;
+                const int j = item_of_round(++u.r, cta, G);
+                if (j >= f.items) {
+                    u.done = true;
+                    return false;
+                }
+                u.it = decode_item<PREFIX>(f, j);
+                u.own = own_tiles<PREFIX>(u.it, x);
+                u.i = 0;
+                if constexpr (!PREFIX) {
+                    u.e = u.it.e0;
+                    u.e_end = u.it.e1;
+                }
+            }
+            return false;
+        };
+        auto keys_of = [&](const Cursor &u) {
+            const int e = u.own.entry(u.i);
+            if constexpr (PREFIX) return min(kKeys, a.N - e * kKeys);
+            else return u.it.keys(x, e);
+        };
+        int spins = 0;
+        uint64_t since = 0;
+        while (true) {
+            bool progress = false;
+            // S of the next tile: its keys and (for an item's first) queries are there, the S before is read
+            if (at_tile(S, kBarKfull, kBarKfree, L::kKst)) {
+                bool go = pipe.ready(kBarKfull + k_ring + S.ring.st, S.ring.ph);
+                if (go && S.i == 0) go = pipe.ready(kBarQfull + bq, (PREFIX ? S.r : S.n) & 1);
+                if (go && S.c > 0) go = pipe.ready(kBarSfree + x, (S.c - 1) & 1);
+                if (go) {
+                    tc_fence_after();
+                    const uint32_t id = idesc_bf16(kM, (keys_of(S) + 15) & ~15, false);
+                    const uint64_t kd = kd0 + S.ring.st * (L::kY / 16);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int s = 0; s < D / 16; ++s)
-                        mma_ss(tmem + buf * 64, qd + ((s >> 2) * kXBlk + (s & 3) * 32) / 16,
-                               kd + ((s >> 2) * kYBlk + (s & 3) * 32) / 16, id, s > 0);
-                    mma_commit(pipe.bar(kBarS + buf));
-                    if (i + 1 == own.n) mma_commit(pipe.bar(kBarQfree + bq));
+                        for (int s = 0; s < D / 16; ++s)
+                            mma_ss(tmem + x * 128, qd + ((s >> 2) * kXBlk + (s & 3) * 32) / 16,
+                                   kd + ((s >> 2) * kYBlk + (s & 3) * 32) / 16, id, s > 0);
+                        mma_commit(pipe.bar(kBarS + 2 * x + (S.c & 1)));
+                        mma_commit(pipe.bar(kBarKfree + k_ring + S.ring.st));
+                        if (S.i + 1 == S.own.n) mma_commit(pipe.bar(kBarQfree + bq));
+                    }
+                    __syncwarp();
+                    S.ring.next(L::kKst);
+                    ++S.i;
+                    ++S.e;
+                    ++S.c;
+                    progress = true;
                 }
-                __syncwarp();
-                s_next = st;
-                next_stage();
-            };
-            if (own.n > 0) issue_s(0);
-            for (int i = 0; i < own.n && ok; ++i) {
-                s_cur = s_next;
-                n_cur = n_next;
-                if (i + 1 < own.n) issue_s(i + 1);
-                const int cc = c + i, buf = 2 * x + (cc & 1);
-                if (!ok || !(ok = pipe.wait_warp(kBarP + buf, (cc >> 1) & 1))) break;
-                if (i == 0 && n > 0 && !(ok = pipe.wait_warp(kBarOfree + x, (n - 1) & 1))) break;
-                tc_fence_after();
-                const int k16 = (n_cur + 15) / 16;
-                const uint64_t vd = vd0 + s_cur * (L::kY / 16);
-                if (elect_one()) {
-#pragma unroll
-                    for (int s = 0; s < kKeys / 16; ++s)
-                        if (s < k16)
-                            mma_ts(tmem + 256 + x * 128, tmem + buf * 64 + s * 8, vd + s * (2048 / 16),
-                                   idesc_bf16(kM, D, true), i > 0 || s > 0);
-                    mma_commit(pipe.bar(kBarPV + buf));
-                    mma_commit(pipe.bar(kBarFree + ring0 + s_cur));
-                }
-                __syncwarp();
             }
-            if (!ok) break;
-            skip_to(e_end);
-            c += own.n;
-            if (own.n > 0) ++n;
+            // PV of the next tile: P is written, its values are there, O (for an item's first) is read
+            if (at_tile(V, kBarVfull, kBarVfree, L::kVst) && V.c < S.c) {
+                const int buf = 2 * x + (V.c & 1);
+                bool go = pipe.ready(kBarP + buf, (V.c >> 1) & 1);
+                if (go) go = pipe.ready(kBarVfull + v_ring + V.ring.st, V.ring.ph);
+                if (go && V.i == 0 && V.n > 0) go = pipe.ready(kBarOfree + x, (V.n - 1) & 1);
+                if (go) {
+                    tc_fence_after();
+                    const int k16 = (keys_of(V) + 15) / 16;
+                    const uint64_t vd = vd0 + V.ring.st * (L::kY / 16);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int s = 0; s < kKeys / 16; ++s)
+                            if (s < k16)
+                                mma_ts(tmem + 256 + x * 128, tmem + x * 128 + 64 + (V.c & 1) * 32 + s * 8, vd + s * (2048 / 16),
+                                       idesc_bf16(kM, D, true), V.i > 0 || s > 0);
+                        mma_commit(pipe.bar(kBarPV + buf));
+                        mma_commit(pipe.bar(kBarVfree + v_ring + V.ring.st));
+                    }
+                    __syncwarp();
+                    V.ring.next(L::kVst);
+                    ++V.i;
+                    ++V.e;
+                    ++V.c;
+                    progress = true;
+                }
+            }
+            if (S.done && V.done) break;
+            if (progress) {
+                spins = 0;
+                since = 0;
+            } else if (!(ok = pipe.idle(&spins, &since))) {
+                break;
+            }
         }
         if (elect_one()) {
             mma_commit(pipe.bar(kBarDrain + x));  // what was issued completes before TMEM is released
@@ -332,9 +384,9 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
         // ---------------------------------------------------------------- softmax rows of tile x
         const int x = warp >> 3, w = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane, pair = 4 * x + quad;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const uint32_t s_col = tmem + lanes + x * 128 + w * 64, o_col = tmem + lanes + 256 + x * 128;
+        const uint32_t s_col = tmem + lanes + x * 128, p_col = s_col + 64 + w * 32, o_col = tmem + lanes + 256 + x * 128;
         float *refs = reinterpret_cast<float *>(smem + L::kRef) + x * kM + row;
-        float2 *ends = reinterpret_cast<float2 *>(smem + L::kEnd) + x * 2 * kM + row;  // + item parity * 4 kM + warpgroup * kM
+        float2 *ends = reinterpret_cast<float2 *>(smem + L::kEnd) + x * 2 * kM + row;  // + warpgroup * kM
         const float scale2 = a.scale * kLog2e;
         const float2 scale22 = make_float2(scale2, scale2);
         bool ok = true;
@@ -379,6 +431,9 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                 tmem_ld32(s_col, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
                 if (n > 32) tmem_ld32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
                 tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) pipe.arrive(kBarSfree + x);
                 if (!full) {
                     const uint32_t mk0 = range_bits(lo, hi, 0) | range_bits(0, as, 0);
                     const uint32_t mk1 = range_bits(lo, hi, 32) | range_bits(0, as, 32);
@@ -433,15 +488,17 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
 #pragma unroll
                     for (int u = 0; u < 4; ++u) v[u] = fma2(as2(s + q + 2 * u), scale22, nb2);
 #pragma unroll
-                    for (int u = 0; u < 3; ++u) v[u] = make_float2(exp2_ftz(v[u].x), exp2_ftz(v[u].y));
-                    v[3] = exp2_fma2(v[3]);
+                    for (int u = 0; u < 4; ++u) v[u] = make_float2(exp2_ftz(v[u].x), exp2_ftz(v[u].y));
                     z0 = add2(z0, add2(v[0], v[1]));
                     z1 = add2(z1, add2(v[2], v[3]));
 #pragma unroll
                     for (int u = 0; u < 4; ++u) s[q / 2 + u] = pack_bf16(v[u].x, v[u].y);  // s[q / 2 ..] has been read
                 }
                 l += (z0.x + z0.y) + (z1.x + z1.y);
-                tmem_st32(s_col, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                // the PV of two tiles before has read this buffer
+                if (cc >= 2 && !(ok = pipe.wait_warp(kBarPV + 2 * x + w, ((cc >> 1) - 1) & 1))) break;
+                tc_fence_after();
+                tmem_st32(p_col, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -451,18 +508,18 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
             c += own.n;
             // ---- O / l and lse: each warpgroup half of the columns
             if (own.n > 0) {
-                float2 *e = ends + (n_items & 1) * 4 * kM;
-                e[w * kM] = make_float2(m, l);
+                if (!(ok = pipe.wait_warp(kBarPV + 2 * x + ((c - 1) & 1), ((c - 1) >> 1) & 1))) break;
+                tc_fence_after();
+                // (only now: a PV of this item has waited for the other's read of the last item's sums)
+                ends[w * kM] = make_float2(m, l);
                 __syncwarp();
                 if (lane == 0) pipe.arrive(kBarEnd + pair);
                 if (!(ok = pipe.wait_warp(kBarEnd + pair, n_items & 1))) break;
-                const float2 y = e[(w ^ 1) * kM];
+                const float2 y = ends[(w ^ 1) * kM];
                 const float mf = fmaxf(m, y.x);  // references only rise
                 if (mf != -INFINITY) l = l * exp2_ftz(m - mf) + y.y * exp2_ftz(y.x - mf);
                 m = mf;
                 ++n_items;
-                if (!(ok = pipe.wait_warp(kBarPV + 2 * x + ((c - 1) & 1), ((c - 1) >> 1) & 1))) break;
-                tc_fence_after();
             }
             const bool some = m != -INFINITY && l > 0.f;  // a split may hold nothing that the row sees
             const float inv = some ? 1.f / l : 0.f;
@@ -472,6 +529,13 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
             constexpr int kHalf = D / 2;
             bf16 *orow = static_cast<bf16 *>(a.O.ptr) + b * a.O.sb + h * a.O.sh + (int64_t)i * a.O.st + w * kHalf;
             float *prow = a.part_o ? a.part_o + (place * a.slots + slot) * D + w * kHalf : nullptr;
+            // the four rows of a lane's group of four (null: no row)
+            char *to[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint64_t p = have ? (prow ? (uint64_t)prow : (uint64_t)orow) : 0ull;
+                to[k] = reinterpret_cast<char *>(__shfl_sync(kFull, p, (lane & ~3) + k));
+            }
 #pragma unroll
             for (int part = 0; part < kHalf / 32; ++part) {
                 uint32_t o[32];
@@ -482,24 +546,34 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
 #pragma unroll
                     for (int q = 0; q < 32; ++q) o[q] = 0u;
                 }
-                if (!have) continue;
-                if (prow) {
-                    float4 *dst = reinterpret_cast<float4 *>(prow + part * 32);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        dst[q] = make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
-                                             __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
+                for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * inv);
+                if (prow) {  // (of every lane or of none)
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        uint4 u[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            u[q] = make_uint4(o[16 * g + 4 * q], o[16 * g + 4 * q + 1], o[16 * g + 4 * q + 2], o[16 * g + 4 * q + 3]);
+                        swap_units(u);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (to[k]) *reinterpret_cast<uint4 *>(to[k] + part * 128 + g * 64 + (lane & 3) * 16) = u[k];
+                    }
                 } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(orow + part * 32);
+                    uint4 u[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        uint4 v;
-                        v.x = pack_bf16(__uint_as_float(o[8 * q + 0]) * inv, __uint_as_float(o[8 * q + 1]) * inv);
-                        v.y = pack_bf16(__uint_as_float(o[8 * q + 2]) * inv, __uint_as_float(o[8 * q + 3]) * inv);
-                        v.z = pack_bf16(__uint_as_float(o[8 * q + 4]) * inv, __uint_as_float(o[8 * q + 5]) * inv);
-                        v.w = pack_bf16(__uint_as_float(o[8 * q + 6]) * inv, __uint_as_float(o[8 * q + 7]) * inv);
-                        dst[q] = v;
+                        uint32_t v[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            v[k] = pack_bf16(__uint_as_float(o[8 * q + 2 * k]), __uint_as_float(o[8 * q + 2 * k + 1]));
+                        u[q] = make_uint4(v[0], v[1], v[2], v[3]);
                     }
+                    swap_units(u);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (to[k]) *reinterpret_cast<uint4 *>(to[k] + part * 64 + (lane & 3) * 16) = u[k];
                 }
             }
             if (have && w == 0) {

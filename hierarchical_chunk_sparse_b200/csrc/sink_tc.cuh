@@ -7,6 +7,17 @@
 namespace hils {
 namespace tc {
 
+// Non-blocking test of an mbarrier phase.
+__device__ __forceinline__ bool mbar_test_phase(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // The CTA's waits. Each is bounded by the global timer; the first one that expires sets
 // the abort flag and bit 0 of the call's status word, after which every wait fails, the
 // roles stop issuing, and the CTA drains what it started and returns.
@@ -35,6 +46,29 @@ struct Pipe {
         *abort_flag = 1u;
         atomicOr(status, 1u);
         return false;
+    }
+    // a test that does not wait (a warp's lanes agree)
+    __device__ __forceinline__ bool ready(int i, uint32_t parity) const {
+        return __all_sync(kFull, mbar_test_phase(bar(i), parity));
+    }
+    // For a loop over several barriers: false once it has made no progress for the limit since
+    // *since (0: none yet) or the CTA stops. `spins` counts the idle rounds.
+    __device__ __forceinline__ bool idle(int *spins, uint64_t *since) const {
+        bool ok = true;
+        if (wait_ns == 0) {
+            ok = false;
+        } else if ((++*spins & 63) == 0) {
+            const uint64_t now = global_ns();
+            if (*since == 0) *since = now;
+            if (*abort_flag) return false;
+            ok = (long long)(now - *since) <= wait_ns;
+        }
+        ok = __all_sync(kFull, ok);
+        if (!ok) {
+            *abort_flag = 1u;
+            atomicOr(status, 1u);
+        }
+        return ok;
     }
     // every lane waits; true if all succeeded
     __device__ __forceinline__ bool wait_warp(int i, uint32_t parity) const {
@@ -117,6 +151,27 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     return r;
 }
 
+// Four lanes that hold 16-byte units 0..3 of their own rows (one row a lane) exchange them:
+// afterwards unit k of lane j (of each four) is unit j of the row of lane k, so that one store
+// of the warp writes 64 consecutive bytes of eight rows instead of 16 of 32.
+__device__ __forceinline__ void swap_units(uint4 (&u)[4]) {
+    const int lane = threadIdx.x % 32;
+    auto step = [&](uint4 &a, uint4 &b, int mask) {  // a: kept by lanes without the bit, b: by those with it
+        const bool up = lane & mask;
+        uint4 s = up ? a : b;
+        s.x = __shfl_xor_sync(kFull, s.x, mask);
+        s.y = __shfl_xor_sync(kFull, s.y, mask);
+        s.z = __shfl_xor_sync(kFull, s.z, mask);
+        s.w = __shfl_xor_sync(kFull, s.w, mask);
+        if (up) a = s;
+        else b = s;
+    };
+    step(u[0], u[2], 2);
+    step(u[1], u[3], 2);
+    step(u[0], u[1], 1);
+    step(u[2], u[3], 1);
+}
+
 // Bit q is set where lo <= c0 + q < hi.
 __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int c0) {
     const int l = max(lo - c0, 0), h = min(hi - c0, 32);
@@ -139,14 +194,19 @@ struct RowItem {
     int split;
     bool hasB;          // B has rows
 
+    RowItem() = default;
     __device__ __forceinline__ RowItem(int j, int B, int H, int G, int P, int qt, int nqb, int Lq, int N, int W, int A_,
                                        int splits) {
-        split = j % splits;
-        j /= splits;
-        const int hp = H / P, units = B * hp;
-        const int qb = nqb - 1 - j / units, u = j % units;  // latest queries (most keys) first
+        split = 0;
+        if (splits > 1) {
+            const int q = j / splits;
+            split = j - q * splits;
+            j = q;
+        }
+        const int hp = H / P, units = B * hp, q = j / units, u = j - q * units;
+        const int qb = nqb - 1 - q;  // latest queries (most keys) first
         b = u / hp;
-        h = (u % hp) * P;
+        h = (u - b * hp) * P;
         hk = h / G;
         i0 = qb * 2 * qt;
         A = A_;
@@ -155,8 +215,12 @@ struct RowItem {
         hasB = tB < N;
         sp = sink_span(tA, min(N - 1, tB + qt - 1), W, A, KT);
         const int nt = sp.ns + sp.nw;
-        e0 = (int)((int64_t)nt * split / splits);
-        e1 = (int)((int64_t)nt * (split + 1) / splits);
+        e0 = 0;
+        e1 = nt;
+        if (splits > 1) {
+            e0 = (int)((int64_t)nt * split / splits);
+            e1 = (int)((int64_t)nt * (split + 1) / splits);
+        }
         eA = sp.ns + (sp.nw > 0 ? (min(sp.hi, tB) - sp.lo + KT - 1) / KT : 0);
         const int gone = tB - W - sp.lo - (KT - 1);  // >= 0: B sees no key of the first window tile
         wB = sp.lo >= A && gone >= 0 ? gone / KT + 1 : 0;
