@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_dq_tc_kernel(const __grid_co
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) pipe.arrive(kBarP + x);
+                pipe.arrive_if(lane == 0, kBarP + x);
                 ++c;
             }
             if (!ok) break;
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_dq_tc_kernel(const __grid_co
             if (any_tile) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) pipe.arrive(kBarOfree + x);
+                pipe.arrive_if(lane == 0, kBarOfree + x);
             }
         }
     }
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_dkv_tc_kernel(const __grid_c
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) pipe.arrive(kBarP + w);
+                pipe.arrive_if(lane == 0, kBarP + w);
             }
             if (!ok) break;
             c += steps;
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_dkv_tc_kernel(const __grid_c
             if (steps > 0) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) pipe.arrive(kBarOfree);
+                pipe.arrive_if(lane == 0, kBarOfree);
             }
         }
     }

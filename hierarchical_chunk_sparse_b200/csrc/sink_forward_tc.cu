@@ -55,6 +55,10 @@ enum {
     kNumBars = 58
 };
 
+// An entry's note for a tile (B's in the upper half of the word): its keys, and whether it is the
+// item's first or last of the tile; 0 for an entry that is not the tile's.
+constexpr uint32_t kNoteFirst = 128u, kNoteLast = 256u, kNoteEnd = 0x80000000u;
+
 struct FwdTc {
     SinkArgs a;
     int P, qt, nqb;     // prefill: packed heads, queries of a tile, row items per (b, packed heads)
@@ -70,7 +74,8 @@ struct Smem {
     static constexpr int kQ = 0, kK = (PREFIX ? 1 : 2) * kX, kV = kK + kRings * kKst * kY;
     static constexpr int kRef = kV + kRings * kVst * kY;  // [2 tiles][128] references
     static constexpr int kEnd = kRef + 2 * kM * 4;        // [2 tiles][2 warpgroups][128] reference, sum
-    static constexpr int kBars = kEnd + 4 * kM * 8, kMisc = kBars + 8 * kNumBars;
+    static constexpr int kNote = kEnd + 4 * kM * 8;       // notes of the K stages [8], the V stages [8]
+    static constexpr int kBars = kNote + 64, kMisc = kBars + 8 * kNumBars;
     static constexpr int kBytes = kMisc + 16;
 };
 
@@ -156,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = smem_u32(smem);
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + L::kMisc);
+    volatile uint32_t *notes = reinterpret_cast<uint32_t *>(smem + L::kNote);
     const Pipe pipe{sbase + L::kBars, misc + 1, a.status, a.wait_ns};
     const int G = gridDim.x, cta = blockIdx.x;
     if (sbase & 1023u) {  // an alignment that the launch has to give
@@ -191,13 +197,19 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
         };
         Ring kr[2], vr[2];  // of each ring: the next stage
         int loads[2] = {0, 0};
-        auto load_kv = [&](int ring, int k0, bool sink, int hk, int b) {
+        // One entry: `note` tells the MMA warps which tiles take it (0: none), for K and V alike.
+        auto load_kv = [&](int ring, uint32_t note, int k0, bool sink, int hk, int b) {
             const int ks = ring * L::kKst + kr[ring].st, vs = ring * L::kVst + vr[ring].st;
             const uint32_t bytes = (uint32_t)(sink ? f.sink_box : kKeys) * D * 2;
             if (loads[ring] >= L::kKst && !(ok = pipe.wait_warp(kBarKfree + ks, kr[ring].ph ^ 1u))) return;
             if (elect_one()) {
-                mbar_expect_tx(pipe.bar(kBarKfull + ks), bytes);
-                tile(sbase + L::kK + ks * L::kY, kYBlk, sink ? &tmKs : &tmK, kBarKfull + ks, k0, hk, b);
+                notes[ks] = note;
+                if (note & kNoteEnd) {
+                    pipe.arrive(kBarKfull + ks);
+                } else {
+                    mbar_expect_tx(pipe.bar(kBarKfull + ks), bytes);
+                    tile(sbase + L::kK + ks * L::kY, kYBlk, sink ? &tmKs : &tmK, kBarKfull + ks, k0, hk, b);
+                }
             }
             __syncwarp();
             kr[ring].next(L::kKst);
@@ -206,12 +218,20 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                 return;
             }
             if (elect_one()) {
-                mbar_expect_tx(pipe.bar(kBarVfull + vs), bytes);
-                tile(sbase + L::kV + vs * L::kY, kYBlk, sink ? &tmVs : &tmV, kBarVfull + vs, k0, hk, b);
+                notes[8 + vs] = note;
+                if (note & kNoteEnd) {
+                    pipe.arrive(kBarVfull + vs);
+                } else {
+                    mbar_expect_tx(pipe.bar(kBarVfull + vs), bytes);
+                    tile(sbase + L::kV + vs * L::kY, kYBlk, sink ? &tmVs : &tmV, kBarVfull + vs, k0, hk, b);
+                }
             }
             __syncwarp();
             vr[ring].next(L::kVst);
             ++loads[ring];
+        };
+        auto note_of = [](int keys, bool first, bool last) -> uint32_t {
+            return keys > 0 ? (uint32_t)keys | (first ? kNoteFirst : 0u) | (last ? kNoteLast : 0u) : 0u;
         };
         for (int r = 0; ok; ++r) {
             const int j = item_of_round(r, cta, G);
@@ -219,21 +239,28 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
             const auto it = decode_item<PREFIX>(f, j);
             if constexpr (PREFIX) {
                 if (nq[0] > 0 && !(ok = pipe.wait_warp(kBarQfree, (nq[0] - 1) & 1))) break;
+                const int n0 = it.r1 - it.r0, n1 = it.r2 - it.r1;
                 if (elect_one()) {
                     mbar_expect_tx(pipe.bar(kBarQfull), (uint32_t)(f.nb * a.G) * D * 2);
                     tile(sbase + L::kQ, kXBlk, &tmQ, kBarQfull, it.h, it.i0, 0);
+                    // a range that is not there lets the queries go at once
+                    if (n0 == 0) pipe.arrive(kBarQfree);
+                    if (n1 == 0) pipe.arrive(kBarQfree);
                 }
                 __syncwarp();
                 ++nq[0];
-                const int n0 = it.r1 - it.r0, n1 = it.r2 - it.r1;
                 for (int i = 0; i < max(n0, n1) && ok; ++i) {
-                    if (i < n0) load_kv(0, (it.r0 + i) * kKeys, false, it.hk, 0);
-                    if (ok && i < n1) load_kv(1, (it.r1 + i) * kKeys, false, it.hk, 0);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int n = x ? n1 : n0, e = (x ? it.r1 : it.r0) + i;
+                        if (i < n && ok)
+                            load_kv(x, note_of(min(kKeys, a.N - e * kKeys), i == 0, i + 1 == n), e * kKeys, false, it.hk, 0);
+                    }
                 }
             } else {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    if (own_tiles<PREFIX>(it, x).n == 0) continue;
+                    if (it.last(x) < 0) continue;
                     if (nq[x] > 0 && !(ok = pipe.wait_warp(kBarQfree + x, (nq[x] - 1) & 1))) break;
                     if (elect_one()) {
                         mbar_expect_tx(pipe.bar(kBarQfull + x), L::kX);
@@ -242,9 +269,17 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                     __syncwarp();
                     ++nq[x];
                 }
-                for (int e = it.e0; e < it.e1 && ok; ++e) load_kv(0, it.first_key(e), e < it.sp.ns, it.hk, it.b);
+                const int l0 = it.last(0), l1 = it.last(1);
+                bool first0 = true, first1 = true;
+                for (int e = it.e0; e < it.e1 && ok; ++e) {
+                    const uint32_t n0 = note_of(it.keys(0, e), first0, e == l0), n1 = note_of(it.keys(1, e), first1, e == l1);
+                    first0 = first0 && n0 == 0u;
+                    first1 = first1 && n1 == 0u;
+                    load_kv(0, n0 | n1 << 16, it.first_key(e), e < it.sp.ns, it.hk, it.b);
+                }
             }
         }
+        for (int ring = 0; ring < L::kRings && ok; ++ring) load_kv(ring, kNoteEnd, 0, false, 0, 0);
         // what was started lands before the CTA's memory is released
         if (lane == 0) {
             for (int x = 0; x < 2; ++x) pipe.drain(kBarQfull + x, nq[x]);
@@ -262,66 +297,51 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
         const int k_ring = PREFIX ? x * L::kKst : 0, v_ring = PREFIX ? x * L::kVst : 0;
         const uint64_t qd = tile_desc(sbase + L::kQ + (PREFIX ? 0 : x * L::kX), 16);
         const uint64_t kd0 = tile_desc(sbase + L::kK + k_ring * L::kY, 16), vd0 = tile_desc(sbase + L::kV + v_ring * L::kY, kYBlk);
-        // Two cursors over the tiles of x, for S and for PV: c tiles and n items of x are done
-        struct Cursor {
-            decltype(decode_item<PREFIX>(f, 0)) it;
-            Own own{0, 0, 0, 0};
+        // S and PV go through the same entries, each in its own ring: c tiles and n items are done
+        struct Side {
             Ring ring;
-            int r = -1, i = 0, e = 0, e_end = 0, c = 0, n = 0;
+            int c = 0, n = 0;
             bool done = false;
         };
-        Cursor S, V;
-        bool ok = true;
-        // Brings a cursor to its next tile; false if there is none, or if entries of the ring that
-        // are not this tile's have to land first, to be released.
-        auto at_tile = [&](Cursor &u, int full, int free, int stages) -> bool {
-            while (!u.done) {
-                const bool more = u.i < u.own.n;
-                const int to = more ? u.own.entry(u.i) : u.e_end;
-                while (!PREFIX && u.e < to) {
-                    if (!pipe.ready(full + u.ring.st, u.ring.ph)) return false;
-                    if (lane == 0) pipe.arrive(free + u.ring.st);
-                    u.ring.next(stages);
-                    ++u.e;
-                }
-                if (more) return true;
-                if (PREFIX && u.own.n == 0 && &u == &S && u.r >= 0) {  // a range that is not there: its queries are let go
-                    if (!pipe.ready(kBarQfull, u.r & 1)) return false;
-                    if (lane == 0) pipe.arrive(kBarQfree);
-                }
-                if (u.own.n > 0) ++u.n;
-                const int j = item_of_round(++u.r, cta, G);
-                if (j >= f.items) {
-                    u.done = true;
-                    return false;
-                }
-                u.it = decode_item<PREFIX>(f, j);
-                u.own = own_tiles<PREFIX>(u.it, x);
-                u.i = 0;
-                if constexpr (!PREFIX) {
-                    u.e = u.it.e0;
-                    u.e_end = u.it.e1;
-                }
-            }
-            return false;
-        };
-        auto keys_of = [&](const Cursor &u) {
-            const int e = u.own.entry(u.i);
-            if constexpr (PREFIX) return min(kKeys, a.N - e * kKeys);
-            else return u.it.keys(x, e);
+        Side S, V;
+        // What the next S and the next PV need, one barrier a lane, so that one test serves all:
+        // 0-2 its keys, S before it read, an item's queries; 3-5 P, its values, O of the item before
+        // read. (Selects: a branch for each lane would cost more than the tests.)
+        uint32_t my_bar, my_par;
+        auto set_needs = [&] {
+            const int s_full = kBarKfull + k_ring + S.ring.st, v_full = kBarVfull + v_ring + V.ring.st;
+            const int p_full = kBarP + 2 * x + (V.c & 1);
+            int i = lane == 0 ? s_full : kBarSfree + x;
+            uint32_t par = lane == 0 ? S.ring.ph : (uint32_t)(S.c - 1);
+            i = lane == 2 ? kBarQfull + bq : i;
+            par = lane == 2 ? S.n : par;
+            i = lane == 3 ? p_full : i;
+            par = lane == 3 ? (uint32_t)V.c >> 1 : par;
+            i = lane == 4 ? v_full : i;
+            par = lane == 4 ? V.ring.ph : par;
+            i = lane == 5 ? kBarOfree + x : i;
+            par = lane == 5 ? (uint32_t)(V.n - 1) : par;
+            my_bar = pipe.bar(i);
+            my_par = par & 1u;
         };
         int spins = 0;
         uint64_t since = 0;
-        while (true) {
+        while (!S.done || !V.done) {
+            set_needs();
+            const unsigned got = __ballot_sync(kFull, mbar_test_phase(my_bar, my_par)) | (S.c == 0 ? 2u : 0u);
+            __syncwarp();
             bool progress = false;
-            // S of the next tile: its keys and (for an item's first) queries are there, the S before is read
-            if (at_tile(S, kBarKfull, kBarKfree, L::kKst)) {
-                bool go = pipe.ready(kBarKfull + k_ring + S.ring.st, S.ring.ph);
-                if (go && S.i == 0) go = pipe.ready(kBarQfull + bq, (PREFIX ? S.r : S.n) & 1);
-                if (go && S.c > 0) go = pipe.ready(kBarSfree + x, (S.c - 1) & 1);
-                if (go) {
+            if (!S.done && (got & 1u)) {
+                const uint32_t all = notes[k_ring + S.ring.st], note = PREFIX ? all : (all >> (16 * x)) & 0xffffu;
+                if (all & kNoteEnd) {
+                    S.done = progress = true;
+                } else if (note == 0u) {  // not this tile's
+                    pipe.arrive_if(lane == 0, kBarKfree + k_ring + S.ring.st);
+                    S.ring.next(L::kKst);
+                    progress = true;
+                } else if ((got & 2u) && (!(note & kNoteFirst) || (got & 4u))) {
                     tc_fence_after();
-                    const uint32_t id = idesc_bf16(kM, (keys_of(S) + 15) & ~15, false);
+                    const uint32_t id = idesc_bf16(kM, ((note & 127u) + 15) & ~15, false);
                     const uint64_t kd = kd0 + S.ring.st * (L::kY / 16);
                     if (elect_one()) {
 #pragma unroll
@@ -330,48 +350,48 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                                    kd + ((s >> 2) * kYBlk + (s & 3) * 32) / 16, id, s > 0);
                         mma_commit(pipe.bar(kBarS + 2 * x + (S.c & 1)));
                         mma_commit(pipe.bar(kBarKfree + k_ring + S.ring.st));
-                        if (S.i + 1 == S.own.n) mma_commit(pipe.bar(kBarQfree + bq));
+                        if (note & kNoteLast) mma_commit(pipe.bar(kBarQfree + bq));
                     }
                     __syncwarp();
                     S.ring.next(L::kKst);
-                    ++S.i;
-                    ++S.e;
                     ++S.c;
+                    if (note & kNoteLast) ++S.n;
                     progress = true;
                 }
             }
-            // PV of the next tile: P is written, its values are there, O (for an item's first) is read
-            if (at_tile(V, kBarVfull, kBarVfree, L::kVst) && V.c < S.c) {
-                const int buf = 2 * x + (V.c & 1);
-                bool go = pipe.ready(kBarP + buf, (V.c >> 1) & 1);
-                if (go) go = pipe.ready(kBarVfull + v_ring + V.ring.st, V.ring.ph);
-                if (go && V.i == 0 && V.n > 0) go = pipe.ready(kBarOfree + x, (V.n - 1) & 1);
-                if (go) {
+            if (!V.done && (got & 16u)) {
+                const uint32_t all = notes[8 + v_ring + V.ring.st], note = PREFIX ? all : (all >> (16 * x)) & 0xffffu;
+                if (all & kNoteEnd) {
+                    V.done = progress = true;
+                } else if (note == 0u) {
+                    pipe.arrive_if(lane == 0, kBarVfree + v_ring + V.ring.st);
+                    V.ring.next(L::kVst);
+                    progress = true;
+                } else if ((got & 8u) && V.c < S.c && (!(note & kNoteFirst) || V.n == 0 || (got & 32u))) {
                     tc_fence_after();
-                    const int k16 = (keys_of(V) + 15) / 16;
+                    const int k16 = ((note & 127u) + 15) / 16;
+                    const uint32_t acc = note & kNoteFirst ? 0u : 1u;
                     const uint64_t vd = vd0 + V.ring.st * (L::kY / 16);
                     if (elect_one()) {
 #pragma unroll
                         for (int s = 0; s < kKeys / 16; ++s)
                             if (s < k16)
                                 mma_ts(tmem + 256 + x * 128, tmem + x * 128 + 64 + (V.c & 1) * 32 + s * 8, vd + s * (2048 / 16),
-                                       idesc_bf16(kM, D, true), V.i > 0 || s > 0);
-                        mma_commit(pipe.bar(kBarPV + buf));
+                                       idesc_bf16(kM, D, true), s > 0 ? 1u : acc);
+                        mma_commit(pipe.bar(kBarPV + 2 * x + (V.c & 1)));
                         mma_commit(pipe.bar(kBarVfree + v_ring + V.ring.st));
                     }
                     __syncwarp();
                     V.ring.next(L::kVst);
-                    ++V.i;
-                    ++V.e;
                     ++V.c;
+                    if (note & kNoteLast) ++V.n;
                     progress = true;
                 }
             }
-            if (S.done && V.done) break;
             if (progress) {
                 spins = 0;
                 since = 0;
-            } else if (!(ok = pipe.idle(&spins, &since))) {
+            } else if (!pipe.idle(&spins, &since)) {
                 break;
             }
         }
@@ -433,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) pipe.arrive(kBarSfree + x);
+                pipe.arrive_if(lane == 0, kBarSfree + x);
                 if (!full) {
                     const uint32_t mk0 = range_bits(lo, hi, 0) | range_bits(0, as, 0);
                     const uint32_t mk1 = range_bits(lo, hi, 32) | range_bits(0, as, 32);
@@ -459,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                 const float m_new = raise ? mt : ref;
                 *refs = m_new;
                 __syncwarp();
-                if (lane == 0) pipe.arrive(kBarRef + pair);
+                pipe.arrive_if(lane == 0, kBarRef + pair);
                 if (__any_sync(kFull, raise && ref != -INFINITY)) {
                     // O holds the tiles before this one
                     if (!(ok = pipe.wait_warp(kBarPV + 2 * x + (w ^ 1), ((cc - 1) >> 1) & 1))) break;
@@ -475,10 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                         tmem_st8(o_col + part * 8, o);
                     }
                 }
-                if (m_new != m) {
-                    l = l > 0.f ? l * exp2_ftz(m - m_new) : 0.f;
-                    m = m_new;
-                }
+                l *= m_new == m ? 1.f : exp2_ftz(m - m_new);  // 0 when m is -inf
+                m = m_new;
                 const float nb = m == -INFINITY ? 0.f : -m;
                 const float2 nb2 = make_float2(nb, nb);
                 float2 z0 = make_float2(0.f, 0.f), z1 = z0;
@@ -502,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) pipe.arrive(kBarP + 2 * x + w);
+                pipe.arrive_if(lane == 0, kBarP + 2 * x + w);
             }
             if (!ok) break;
             c += own.n;
@@ -513,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                 // (only now: a PV of this item has waited for the other's read of the last item's sums)
                 ends[w * kM] = make_float2(m, l);
                 __syncwarp();
-                if (lane == 0) pipe.arrive(kBarEnd + pair);
+                pipe.arrive_if(lane == 0, kBarEnd + pair);
                 if (!(ok = pipe.wait_warp(kBarEnd + pair, n_items & 1))) break;
                 const float2 y = ends[(w ^ 1) * kM];
                 const float mf = fmaxf(m, y.x);  // references only rise
@@ -522,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                 ++n_items;
             }
             const bool some = m != -INFINITY && l > 0.f;  // a split may hold nothing that the row sees
-            const float inv = some ? 1.f / l : 0.f;
+            const float inv = some ? __fdividef(1.f, l) : 0.f;
             const float lse = some ? (m + log2f(l)) * kLn2 : -INFINITY;
             const int64_t place = ((int64_t)b * a.H + h) * a.Lq + i;
             const int slot = PREFIX ? 2 * it.split + x : it.split;
@@ -583,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
             if (own.n > 0) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) pipe.arrive(kBarOfree + x);
+                pipe.arrive_if(lane == 0, kBarOfree + x);
             }
         }
     }

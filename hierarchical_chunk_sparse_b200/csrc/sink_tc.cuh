@@ -70,15 +70,26 @@ struct Pipe {
         }
         return ok;
     }
-    // every lane waits; true if all succeeded
+    // A converged warp waits; true if the phase completed. The loop's condition is a vote, so that
+    // no branch diverges (one that does costs about 100 cycles, as does a branch around one lane's
+    // arrival).
     __device__ __forceinline__ bool wait_warp(int i, uint32_t parity) const {
+        const uint32_t b = bar(i);
+        if (wait_ns > 0) {
+            for (int it = 0; it < 64; ++it)
+                if (__all_sync(kFull, mbar_try_wait(b, parity))) return true;
+        }
         return __all_sync(kFull, wait(i, parity));
     }
     __device__ __forceinline__ void arrive(int i) const {
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar(i)) : "memory");
     }
-    __device__ __forceinline__ void arrive(int i, uint32_t count) const {
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar(i)), "r"(count) : "memory");
+    // one lane's arrival (count times), without a branch
+    __device__ __forceinline__ void arrive_if(bool on, int i, uint32_t count = 1) const {
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(bar(i)),
+            "r"(count), "r"((uint32_t)on)
+            : "memory");
     }
     // bounded wait for this CTA's own copies or MMAs while it stops: `uses` phases of barrier i
     __device__ __forceinline__ void drain(int i, int uses) const {

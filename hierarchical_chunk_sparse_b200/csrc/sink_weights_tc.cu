@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
                 if (++tile == it.tiles) tile = 0;
                 if (!(ok = pipe.wait_warp(kBarYfull + st, (g / kStages) & 1))) break;
                 if (!it.valid(x, q0, f.qn)) {
-                    if (lane == 0) pipe.arrive(kBarYfree + st);
+                    pipe.arrive_if(lane == 0, kBarYfree + st);
                     continue;
                 }
                 const int sb = 2 * x + (c & 1);
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
                 if (++tile == it.tiles) tile = 0;
                 if (!(ok = pipe.wait_warp(kBarYfull + st, (g / kStages) & 1))) break;
                 if (!it.valid(x, q0, f.qn)) {
-                    if (lane == 0) pipe.arrive(kBarYfree + st);
+                    pipe.arrive_if(lane == 0, kBarYfree + st);
                     continue;
                 }
                 // queries of each head that see this key
@@ -295,14 +295,14 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
                 if (n > 0 && !(ok = pipe.wait_warp(kBarHalfFree + pair, (n - 1) & 1))) break;
                 hsum[x * kM + row] = w;
                 __syncwarp();
-                if (lane == 0) pipe.arrive(kBarHalf + pair);
+                pipe.arrive_if(lane == 0, kBarHalf + pair);
                 ++n;
                 continue;
             }
             if (!(ok = pipe.wait_warp(kBarHalf + pair, n & 1))) break;
             w += hsum[x * kM + row];
             __syncwarp();
-            if (lane == 0) pipe.arrive(kBarHalfFree + pair);
+            pipe.arrive_if(lane == 0, kBarHalfFree + pair);
             ++n;
             if (key >= a.N) continue;
             if (it.nseg > 1) {
