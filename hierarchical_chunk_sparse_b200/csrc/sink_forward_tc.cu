@@ -19,7 +19,8 @@
 //                row's reference goes from one to the other through shared memory, before the
 //                exponentials, so that they overlap. It is raised, and O rescaled, only when a
 //                tile's maximum passes it by more than 8 in log2 units (P <= 2^8: exact in the
-//                float32 sums, rounded in bf16 as well as below 1).
+//                float32 sums, rounded in bf16 as well as below 1). The warpgroup of an item's
+//                last tile writes its output, while the other begins the next item.
 //   warps 16, 17 tcgen05.mma of A, B;   warp 18  TMA.
 // A softmax warp takes its 64 scores into registers and hands S back before anything else, and
 // P has two buffers of its own, so that neither S of the next tile nor the next softmax waits
@@ -48,11 +49,11 @@ enum {
     kBarSfree = 28,   // + tile: S read (4 warps)
     kBarP = 30,       // + 2 tile + buffer: P written (4 warps)
     kBarPV = 34,      // + 2 tile + buffer: its PV, and every MMA before that, completed
-    kBarOfree = 38,   // + tile: O read (8 warps)
+    kBarOfree = 38,   // + tile: O read (4 warps)
     kBarRef = 40,     // + 4 tile + quadrant: the rows' reference after a tile (1 warp)
-    kBarEnd = 48,     // + 4 tile + quadrant: both warpgroups' sums of an item (2 warps)
-    kBarDrain = 56,   // + tile
-    kNumBars = 58
+    kBarEnd = 48,     // + 8 item parity + 4 tile + quadrant: one warpgroup's sums, for the other (1 warp)
+    kBarDrain = 64,   // + tile
+    kNumBars = 66
 };
 
 // An entry's note for a tile (B's in the upper half of the word): its keys, and whether it is the
@@ -73,7 +74,7 @@ struct Smem {
     static constexpr int kKst = PREFIX ? 3 : 4, kVst = PREFIX ? 2 : 4, kRings = PREFIX ? 2 : 1;
     static constexpr int kQ = 0, kK = (PREFIX ? 1 : 2) * kX, kV = kK + kRings * kKst * kY;
     static constexpr int kRef = kV + kRings * kVst * kY;  // [2 tiles][128] references
-    static constexpr int kEnd = kRef + 2 * kM * 4;        // [2 tiles][2 warpgroups][128] reference, sum
+    static constexpr int kEnd = kRef + 2 * kM * 4;        // [2 item parities][2 tiles][128] reference, sum
     static constexpr int kNote = kEnd + 4 * kM * 8;       // notes of the K stages [8], the V stages [8]
     static constexpr int kBars = kNote + 64, kMisc = kBars + 8 * kNumBars;
     static constexpr int kBytes = kMisc + 16;
@@ -171,9 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i) {
             uint32_t cnt = 1;
-            if ((i >= kBarP && i < kBarP + 4) || (i >= kBarSfree && i < kBarSfree + 2)) cnt = 4;
-            if (i >= kBarOfree && i < kBarOfree + 2) cnt = 8;
-            if (i >= kBarEnd && i < kBarEnd + 8) cnt = 2;
+            if ((i >= kBarP && i < kBarP + 4) || (i >= kBarSfree && i < kBarSfree + 2) || (i >= kBarOfree && i < kBarOfree + 2)) cnt = 4;
             // both tiles release what they share
             if (PREFIX ? i == kBarQfree : (i >= kBarKfree && i < kBarKfree + 6) || (i >= kBarVfree && i < kBarVfree + 4)) cnt = 2;
             mbar_init(pipe.bar(i), cnt);
@@ -406,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t s_col = tmem + lanes + x * 128, p_col = s_col + 64 + w * 32, o_col = tmem + lanes + 256 + x * 128;
         float *refs = reinterpret_cast<float *>(smem + L::kRef) + x * kM + row;
-        float2 *ends = reinterpret_cast<float2 *>(smem + L::kEnd) + x * 2 * kM + row;  // + warpgroup * kM
+        float2 *ends = reinterpret_cast<float2 *>(smem + L::kEnd) + x * kM + row;  // + item parity * 2 kM
         const float scale2 = a.scale * kLog2e;
         const float2 scale22 = make_float2(scale2, scale2);
         bool ok = true;
@@ -524,41 +523,50 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
             }
             if (!ok) break;
             c += own.n;
-            // ---- O / l and lse: each warpgroup half of the columns
+            // ---- O / l and lse: by the warpgroup of the last tile
             if (own.n > 0) {
-                if (!(ok = pipe.wait_warp(kBarPV + 2 * x + ((c - 1) & 1), ((c - 1) >> 1) & 1))) break;
-                tc_fence_after();
-                // (only now: a PV of this item has waited for the other's read of the last item's sums)
-                ends[w * kM] = make_float2(m, l);
-                __syncwarp();
-                pipe.arrive_if(lane == 0, kBarEnd + pair);
-                if (!(ok = pipe.wait_warp(kBarEnd + pair, n_items & 1))) break;
-                const float2 y = ends[(w ^ 1) * kM];
+                const int end = kBarEnd + 8 * (n_items & 1) + pair;
+                float2 *e = ends + (n_items & 1) * 2 * kM;
+                if (((c - 1) & 1) != w) {
+                    *e = make_float2(m, l);
+                    __syncwarp();
+                    pipe.arrive_if(lane == 0, end);
+                    ++n_items;
+                    continue;
+                }
+                if (!(ok = pipe.wait_warp(end, (n_items >> 1) & 1))) break;
+                ++n_items;
+                const float2 y = *e;
                 const float mf = fmaxf(m, y.x);  // references only rise
                 if (mf != -INFINITY) l = l * exp2_ftz(m - mf) + y.y * exp2_ftz(y.x - mf);
                 m = mf;
-                ++n_items;
+                if (!(ok = pipe.wait_warp(kBarPV + 2 * x + w, ((c - 1) >> 1) & 1))) break;
+                tc_fence_after();
+            } else if (w == 1) {
+                continue;
             }
             const bool some = m != -INFINITY && l > 0.f;  // a split may hold nothing that the row sees
             const float inv = some ? __fdividef(1.f, l) : 0.f;
-            const float lse = some ? (m + log2f(l)) * kLn2 : -INFINITY;
             const int64_t place = ((int64_t)b * a.H + h) * a.Lq + i;
             const int slot = PREFIX ? 2 * it.split + x : it.split;
-            constexpr int kHalf = D / 2;
-            bf16 *orow = static_cast<bf16 *>(a.O.ptr) + b * a.O.sb + h * a.O.sh + (int64_t)i * a.O.st + w * kHalf;
-            float *prow = a.part_o ? a.part_o + (place * a.slots + slot) * D + w * kHalf : nullptr;
+            const bool part = a.part_o != nullptr;  // float32 partial rows, else bf16 outputs
+            if (have && (part || a.lse))
+                (part ? a.part_lse[place * a.slots + slot] : a.lse[place]) = some ? (m + log2f(l)) * kLn2 : -INFINITY;
             // the four rows of a lane's group of four (null: no row)
             char *to[4];
+            {
+                const uint64_t p = !have ? 0ull
+                                   : part ? (uint64_t)(a.part_o + (place * a.slots + slot) * D)
+                                          : (uint64_t)(static_cast<bf16 *>(a.O.ptr) + b * a.O.sb + h * a.O.sh + (int64_t)i * a.O.st);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint64_t p = have ? (prow ? (uint64_t)prow : (uint64_t)orow) : 0ull;
-                to[k] = reinterpret_cast<char *>(__shfl_sync(kFull, p, (lane & ~3) + k));
+                for (int k = 0; k < 4; ++k) to[k] = reinterpret_cast<char *>(__shfl_sync(kFull, p, (lane & ~3) + k)) + (lane & 3) * 16;
             }
-#pragma unroll
-            for (int part = 0; part < kHalf / 32; ++part) {
+            const bool live[4] = {(uint64_t)to[0] >= 64, (uint64_t)to[1] >= 64, (uint64_t)to[2] >= 64, (uint64_t)to[3] >= 64};
+#pragma unroll 1
+            for (int col = 0; col < D; col += 32) {
                 uint32_t o[32];
                 if (own.n > 0) {  // every lane loads
-                    tmem_ld32(o_col + w * kHalf + part * 32, o);
+                    tmem_ld32(o_col + col, o);
                     tmem_wait_ld();
                 } else {
 #pragma unroll
@@ -566,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                 }
 #pragma unroll
                 for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * inv);
-                if (prow) {  // (of every lane or of none)
+                if (part) {
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         uint4 u[4];
@@ -576,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                         swap_units(u);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            if (to[k]) *reinterpret_cast<uint4 *>(to[k] + part * 128 + g * 64 + (lane & 3) * 16) = u[k];
+                            if (live[k]) *reinterpret_cast<uint4 *>(to[k] + col * 4 + g * 64) = u[k];
                     }
                 } else {
                     uint4 u[4];
@@ -591,12 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                     swap_units(u);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        if (to[k]) *reinterpret_cast<uint4 *>(to[k] + part * 64 + (lane & 3) * 16) = u[k];
+                        if (live[k]) *reinterpret_cast<uint4 *>(to[k] + col * 2) = u[k];
                 }
-            }
-            if (have && w == 0) {
-                if (prow) a.part_lse[place * a.slots + slot] = lse;
-                else if (a.lse) a.lse[place] = lse;
             }
             if (own.n > 0) {
                 tc_fence_before();
