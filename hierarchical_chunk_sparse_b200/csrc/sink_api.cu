@@ -77,7 +77,7 @@ DecodePlan decode_plan(const hils_params *p, int64_t T, int64_t A, int64_t P, bo
     d.prefix_splits = prefix ? sink_prefix_splits(p->B, Hk, groups(p), (int)P, sms) : 0;
     d.ctas = sink_decode_ctas(p->dtype, p->B, Hk, d.keys, sms);
     d.segs = d.ctas + (int64_t)p->B * Hk;
-    d.bytes = kSinkStatusBytes + sink_align((size_t)p->B * Hk * 4) + sink_part_bytes(rows, d.prefix_splits, p->d) +
+    d.bytes = kSinkStatusBytes + sink_part_bytes(rows, d.prefix_splits, p->d) +
               sink_part_bytes(d.segs * groups(p), 1, p->d) + sink_align(rows * 4) +
               (acc ? sink_align((size_t)rows * d.keys * 4) : 0);
     return d;
@@ -87,7 +87,6 @@ DecodePlan decode_plan(const hils_params *p, int64_t T, int64_t A, int64_t P, bo
 void decode_space(const hils_params *p, const DecodePlan &plan, Carve &ws, float *lse, SinkDecodeArgs *a) {
     const size_t rows = (size_t)p->B * p->H, segs = (size_t)plan.segs * a->G;
     ws.take<uint32_t>(kSinkStatusBytes / 4);
-    a->counters = ws.take<int>(rows / a->G);
     a->slots = plan.prefix_splits;
     a->part_o = ws.take<float>(rows * a->slots * p->d);
     a->part_lse = ws.take<float>(rows * a->slots);

@@ -200,7 +200,6 @@ struct SinkDecodeArgs {
     // this kernel's own: of CTA c's share of row r = (b, hk), head g, at (c + r) * G + g (a
     // staircase: no two pairs (c, r) that meet have the same sum)
     float *seg_o, *seg_lse;
-    int *counters;             // [B * Hk] arrivals, zero before and after the call
     float *logits;             // with acc: [B, H, logit_stride] scaled logits in log2 units, by visible order
     int64_t logit_stride;
 };

@@ -8,12 +8,14 @@ constexpr int kThr = 128, kWarps = kThr / 32, kStages = 3;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <typename T>
-constexpr int tile_keys() { return sizeof(T) == 2 ? 32 : 16; }
+constexpr int tile_keys() { return sizeof(T) == 2 ? 16 : 8; }
 template <typename T, int D>
 constexpr int tile_bytes() { return tile_keys<T>() * D * (int)sizeof(T); }  // of K, and of V
+// the warps' rings, their results of a row, and (float32) its queries
 template <typename T, int D>
-constexpr int decode_smem() {
-    return kWarps * kStages * 2 * tile_bytes<T, D>() + kWarps * kMaxGroupHeads * (D + 2) * 4 + kMaxGroupHeads * (D + 16) * 4;
+int decode_smem(int G) {
+    return kWarps * kStages * 2 * tile_bytes<T, D>() + kWarps * kMaxGroupHeads * 8 + kWarps * G * D * 4 +
+           (sizeof(T) == 4 ? G * D * 4 : 0);
 }
 
 // What a sequence sees, in order: the shared prefix, the sinks, the window.
@@ -90,13 +92,32 @@ __device__ Place<KT> find_tile(const SinkDecodeArgs &a, int Hk, int64_t at) {
 // u ^ (r % 8); zeros for rows behind the last visible one.
 template <typename T, int D, int KT>
 __device__ __forceinline__ void load_kv(const SinkDecodeArgs &a, const Place<KT> &p, uint8_t *dst) {
-    constexpr int kU = D * (int)sizeof(T) / 16, kPer = 32 / kU == 0 ? 1 : 32 / kU, kRounds = KT / kPer;
-    static_assert(kU <= 32, "a row is one round of the warp at most");
+    constexpr int kU = D * (int)sizeof(T) / 16, kPer = 32 / kU, kRounds = KT / kPer;
+    static_assert(kU <= 32 && KT % kPer == 0, "a round of the warp is whole rows");
     const int lane = threadIdx.x % 32, u = lane % kU, r0 = lane / kU;
-    const int v0 = p.k * KT;
+    const int v0 = p.k * KT, v1 = v0 + KT, own = v0 - p.v.prefix;
     const T *kc = static_cast<const T *>(a.K.ptr) + p.b * a.K.sb + p.hk * a.K.sh;
     const T *vc = static_cast<const T *>(a.V.ptr) + p.b * a.V.sb + p.hk * a.V.sh;
-#pragma unroll 4
+    uint8_t *to = dst + r0 * (kU * 16);
+    if (v1 <= p.v.n && (own >= p.v.sinks || (own >= 0 && own + KT <= p.v.sinks) || v1 <= p.v.prefix)) {
+        // all of one run of slots: the prefix, the sinks or the window
+        const bool pre = own < 0;
+        const int64_t j = (pre ? v0 : own < p.v.sinks ? own : p.v.lo + (own - p.v.sinks)) + r0;
+        const int64_t ks = (pre ? a.Kp.st : a.K.st), vs = (pre ? a.Vp.st : a.V.st);
+        const uint8_t *k = reinterpret_cast<const uint8_t *>((pre ? static_cast<const T *>(a.Kp.ptr) + p.hk * a.Kp.sh : kc) + j * ks) + u * 16;
+        const uint8_t *w = reinterpret_cast<const uint8_t *>((pre ? static_cast<const T *>(a.Vp.ptr) + p.hk * a.Vp.sh : vc) + j * vs) + u * 16;
+        const int64_t kstep = ks * kPer * (int)sizeof(T), vstep = vs * kPer * (int)sizeof(T);
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) {
+            const int at = i * 512 + ((u ^ ((i * kPer + r0) & 7)) * 16);
+            cp_async16(to + at, k);
+            cp_async16(to + tile_bytes<T, D>() + at, w);
+            k += kstep;
+            w += vstep;
+        }
+        return;
+    }
+#pragma unroll 1
     for (int i = 0; i < kRounds; ++i) {
         const int r = i * kPer + r0;
         int v = v0 + r;
@@ -111,9 +132,9 @@ __device__ __forceinline__ void load_kv(const SinkDecodeArgs &a, const Place<KT>
             k = kc + j * a.K.st;
             w = vc + j * a.V.st;
         }
-        const int at = r * (kU * 16) + ((u ^ (r & 7)) * 16);
-        cp_async16_zfill(dst + at, reinterpret_cast<const uint8_t *>(k) + u * 16, in);
-        cp_async16_zfill(dst + tile_bytes<T, D>() + at, reinterpret_cast<const uint8_t *>(w) + u * 16, in);
+        const int at = i * 512 + ((u ^ (r & 7)) * 16);
+        cp_async16_zfill(to + at, reinterpret_cast<const uint8_t *>(k) + u * 16, in);
+        cp_async16_zfill(to + tile_bytes<T, D>() + at, reinterpret_cast<const uint8_t *>(w) + u * 16, in);
     }
 }
 
@@ -178,56 +199,38 @@ struct Rows<bf16, D> {
         m[0] = m[1] = -INFINITY;
         l[0] = l[1] = 0.f;
     }
-    __device__ __forceinline__ void tile(const SinkDecodeArgs &a, const Place<32> &p, const uint8_t *stage, float scale2,
+    __device__ __forceinline__ void tile(const SinkDecodeArgs &a, const Place<16> &p, const uint8_t *stage, float scale2,
                                          float *) {
-        const int lane = threadIdx.x % 32, id = lane / 8;
+        const int lane = threadIdx.x % 32, id = lane / 8, r7 = lane & 7;
         const uint32_t kb = (uint32_t)__cvta_generic_to_shared(stage), vb = kb + tile_bytes<bf16, D>();
-        float s[2][4];
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};  // two chains of products
+        const uint32_t kr = kb + (r7 + (id & 1) * 8) * (D * 2);
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-            s[mt][0] = s[mt][1] = s[mt][2] = s[mt][3] = 0.f;
-            const int r = mt * 16 + (lane & 7) + (id & 1) * 8;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                uint32_t f[4];
-                ldsm4(f, kb + r * (D * 2) + (((2 * k + (id >> 1)) ^ (r & 7)) * 16));
-                mma16816(s[mt], f, q[k][0], q[k][1]);
-            }
+        for (int k = 0; k < D / 16; ++k) {
+            uint32_t f[4];
+            ldsm4(f, kr + (((2 * k + (id >> 1)) ^ r7) * 16));
+            mma16816(k & 1 ? s1 : s, f, q[k][0], q[k][1]);
         }
-        const int left = p.v.n - p.k * 32;  // visible slots from this tile's first
-        float mt2[2] = {-INFINITY, -INFINITY};
+        const int left = p.v.n - p.k * 16;  // visible slots from this tile's first
+        const int r = lane / 4;             // keys r (elements 0, 1) and r + 8 (2, 3) of heads g, g + 1
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = mt * 16 + lane / 4 + (e >> 1) * 8;
-                s[mt][e] = r < left ? s[mt][e] * scale2 : -INFINITY;
-                mt2[e & 1] = fmaxf(mt2[e & 1], s[mt][e]);
-            }
+        for (int e = 0; e < 4; ++e) s[e] = r + (e >> 1) * 8 < left ? (s[e] + s1[e]) * scale2 : -INFINITY;
         if (a.logits) {
+            const int g = 2 * (lane % 4);
+            float *out = a.logits + ((int64_t)p.b * a.H + p.hk * a.G + g) * a.logit_stride + p.k * 16 + r;
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = mt * 16 + lane / 4 + (e >> 1) * 8, g = 2 * (lane % 4) + (e & 1);
-                    if (r < left && g < a.G)
-                        a.logits[((int64_t)p.b * a.H + p.hk * a.G + g) * a.logit_stride + p.k * 32 + r] = s[mt][e];
-                }
+            for (int e = 0; e < 4; ++e)
+                if (r + (e >> 1) * 8 < left && g + (e & 1) < a.G) out[(e & 1) * a.logit_stride + (e >> 1) * 8] = s[e];
         }
         float f[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float mx = fmaxf(m[i], max8(mt2[i])), ref = mx == -INFINITY ? 0.f : mx;
+            const float mx = fmaxf(m[i], max8(fmaxf(s[i], s[i + 2]))), ref = mx == -INFINITY ? 0.f : mx;
             f[i] = exp2f(m[i] - ref);
             m[i] = mx;
-            l[i] *= f[i];
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                for (int e = i; e < 4; e += 2) {
-                    s[mt][e] = exp2f(s[mt][e] - ref);
-                    l[i] += s[mt][e];
-                }
+            s[i] = exp2f(s[i] - ref);
+            s[i + 2] = exp2f(s[i + 2] - ref);
+            l[i] = fmaf(l[i], f[i], s[i] + s[i + 2]);
         }
         if (__any_sync(kFull, f[0] != 1.f || f[1] != 1.f)) {
 #pragma unroll
@@ -239,20 +242,17 @@ struct Rows<bf16, D> {
             }
         }
         // the probabilities rounded to bf16 as operands
+        const uint32_t b0 = transpose8(pack2(s[0], s[1])), b1 = transpose8(pack2(s[2], s[3]));
+        const uint32_t vr = vb + (r7 + (id >> 1) * 8) * (D * 2);
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-            const uint32_t b0 = transpose8(pack2(s[mt][0], s[mt][1])), b1 = transpose8(pack2(s[mt][2], s[mt][3]));
-            const int r = mt * 16 + (lane & 7) + (id >> 1) * 8;
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-                uint32_t v[4];
-                ldsm4_t(v, vb + r * (D * 2) + (((2 * c + (id & 1)) ^ (r & 7)) * 16));
-                mma16816(o[c], v, b0, b1);
-            }
+        for (int c = 0; c < D / 16; ++c) {
+            uint32_t v[4];
+            ldsm4_t(v, vr + (((2 * c + (id & 1)) ^ r7) * 16));
+            mma16816(o[c], v, b0, b1);
         }
     }
-    // this warp's results: row g of so [8][D], sm, sl [8]
-    __device__ __forceinline__ void finish(float *sm, float *sl, float *so) {
+    // this warp's results: row g of so [G][D], sm, sl [8]
+    __device__ __forceinline__ void finish(float *sm, float *sl, float *so, int G) {
         const int lane = threadIdx.x % 32, g = 2 * (lane % 4);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -261,6 +261,7 @@ struct Rows<bf16, D> {
                 sm[g + i] = m[i];
                 sl[g + i] = z;
             }
+            if (g + i >= G) continue;
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
                 so[(g + i) * D + c * 16 + lane / 4] = o[c][i];
@@ -270,7 +271,7 @@ struct Rows<bf16, D> {
     }
 };
 
-// float32 on the CUDA cores: a key's logits are two lanes' halves of the dimensions; then a
+// float32 on the CUDA cores: a key's logits are four lanes' quarters of the dimensions; then a
 // lane owns D / 32 dimensions of the output and runs over the keys.
 template <int D>
 struct Rows<float, D> {
@@ -286,17 +287,17 @@ struct Rows<float, D> {
             for (int e = 0; e < kE; ++e) o[g][e] = 0.f;
         }
     }
-    __device__ __forceinline__ void tile(const SinkDecodeArgs &a, const Place<16> &p, const uint8_t *stage, float scale2,
+    __device__ __forceinline__ void tile(const SinkDecodeArgs &a, const Place<8> &p, const uint8_t *stage, float scale2,
                                          float *qs) {
-        const int lane = threadIdx.x % 32, key = lane % 16, half = lane / 16;
-        const float *kt = reinterpret_cast<const float *>(stage), *vt = kt + 16 * D;
+        const int lane = threadIdx.x % 32, key = lane % 8, part = lane / 8;
+        const float *kt = reinterpret_cast<const float *>(stage), *vt = kt + 8 * D;
         float s[kMaxGroupHeads];
 #pragma unroll
         for (int g = 0; g < kMaxGroupHeads; ++g) s[g] = 0.f;
 #pragma unroll 4
-        for (int u = 0; u < D / 8; ++u) {
-            const int uu = half * (D / 8) + u;
-            const float4 k = *reinterpret_cast<const float4 *>(kt + key * D + ((uu ^ (key & 7)) * 4));
+        for (int u = 0; u < D / 16; ++u) {
+            const int uu = u * 4 + part;
+            const float4 k = *reinterpret_cast<const float4 *>(kt + key * D + ((uu ^ key) * 4));
 #pragma unroll
             for (int g = 0; g < kMaxGroupHeads; ++g) {
                 if (g >= a.G) break;
@@ -304,30 +305,31 @@ struct Rows<float, D> {
                 s[g] = fmaf(k.x, x.x, fmaf(k.y, x.y, fmaf(k.z, x.z, fmaf(k.w, x.w, s[g]))));
             }
         }
-        const bool in = key < p.v.n - p.k * 16;
+        const bool in = key < p.v.n - p.k * 8;
 #pragma unroll
         for (int g = 0; g < kMaxGroupHeads; ++g) {
             if (g >= a.G) break;
+            s[g] += __shfl_xor_sync(kFull, s[g], 8);
             s[g] += __shfl_xor_sync(kFull, s[g], 16);
             s[g] = in ? s[g] * scale2 : -INFINITY;
-            if (a.logits && in && half == 0)
-                a.logits[((int64_t)p.b * a.H + p.hk * a.G + g) * a.logit_stride + p.k * 16 + key] = s[g];
+            if (a.logits && in && part == 0)
+                a.logits[((int64_t)p.b * a.H + p.hk * a.G + g) * a.logit_stride + p.k * 8 + key] = s[g];
             float mx = s[g];
 #pragma unroll
-            for (int o_ = 8; o_ > 0; o_ >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o_));
+            for (int o_ = 4; o_ > 0; o_ >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o_));
             mx = fmaxf(mx, m[g]);
             const float ref = mx == -INFINITY ? 0.f : mx, f = exp2f(m[g] - ref);
             s[g] = exp2f(s[g] - ref);
             float z = s[g];
 #pragma unroll
-            for (int o_ = 8; o_ > 0; o_ >>= 1) z += __shfl_xor_sync(kFull, z, o_);
+            for (int o_ = 4; o_ > 0; o_ >>= 1) z += __shfl_xor_sync(kFull, z, o_);
             m[g] = mx;
             l[g] = fmaf(l[g], f, z);
 #pragma unroll
             for (int e = 0; e < kE; ++e) o[g][e] *= f;
         }
 #pragma unroll 4
-        for (int k = 0; k < 16; ++k) {
+        for (int k = 0; k < 8; ++k) {
             float v[kE];
             const int unit = lane * kE / 4, at = k * D + ((unit ^ (k & 7)) * 4) + (lane * kE) % 4;
             if (kE == 4) {
@@ -350,10 +352,11 @@ struct Rows<float, D> {
             }
         }
     }
-    __device__ __forceinline__ void finish(float *sm, float *sl, float *so) {
+    __device__ __forceinline__ void finish(float *sm, float *sl, float *so, int G) {
         const int lane = threadIdx.x % 32;
 #pragma unroll
         for (int g = 0; g < kMaxGroupHeads; ++g) {
+            if (g >= G) break;
             if (lane == 0) {
                 sm[g] = m[g];
                 sl[g] = l[g];
@@ -365,151 +368,158 @@ struct Rows<float, D> {
 };
 
 // The tiles of all rows are cut into one even share for each CTA, whatever the sequences'
-// lengths. A row that several CTAs share, or that has partial results of the prefix kernel,
-// is joined, in order, by the last of its CTAs to arrive.
+// lengths. A row that is one CTA's alone gets its output here; of any other, each CTA leaves
+// its share's result as a segment for the combine.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThr) sink_decode_kernel(SinkDecodeArgs a) {
+__global__ void __launch_bounds__(kThr, 2) sink_decode_kernel(SinkDecodeArgs a) {
     constexpr int KT = tile_keys<T>(), kE = D / 32;
     constexpr int kStage = 2 * tile_bytes<T, D>();
     extern __shared__ __align__(128) uint8_t smem[];
     const int Hk = a.H / a.G, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     uint8_t *ring = smem + warp * kStages * kStage;
-    float *merge = reinterpret_cast<float *>(smem + kWarps * kStages * kStage);
-    float *sm = merge, *sl = sm + kWarps * kMaxGroupHeads, *so = sl + kWarps * kMaxGroupHeads;
-    float *qs = so + kWarps * kMaxGroupHeads * D;  // float32: the row's queries
-    int *flag = reinterpret_cast<int *>(qs + kMaxGroupHeads * D);
+    float *sm = reinterpret_cast<float *>(smem + kWarps * kStages * kStage), *sl = sm + kWarps * kMaxGroupHeads;
+    float *so = sl + kWarps * kMaxGroupHeads, *qs = so + kWarps * a.G * D;
     const float scale2 = a.scale * kLog2e;
     const int64_t total = all_tiles<KT>(a, Hk), n_cta = min((int64_t)gridDim.x, total), c = blockIdx.x;
-    if (c >= n_cta) return;  // every other CTA has a tile: each of a row's CTAs arrives
-    const int64_t t0 = total * c / n_cta, t1 = total * (c + 1) / n_cta;
-    auto cta_of = [&](int64_t tile) { return ((tile + 1) * n_cta - 1) / total; };
-    Place<KT> cur = find_tile<KT>(a, Hk, t0);  // the CTA's current row, at its first tile here
-    Place<KT> ld = cur;
-    ld.advance(a, Hk, warp);
-    int64_t at = t0 + warp;
-    int put = 0, got = 0;  // stages written, read
-    auto next_load = [&] {
-        if (at < t1) {
-            load_kv<T, D, KT>(a, ld, ring + put % kStages * kStage);
-            ld.advance(a, Hk, kWarps);
-            at += kWarps;
-        }
-        ++put;
-        cp_async_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) next_load();
-    for (int64_t t = t0; t < t1;) {  // a row, or what of it is this CTA's
-        const int64_t row0 = t - cur.k;  // the row's first tile
-        const int64_t end = min(t1, row0 + cur.v.tiles);
-        if (sizeof(T) == 4) {
-            __syncthreads();  // the row before is joined
-            for (int e = threadIdx.x; e < a.G * D; e += kThr) {
-                const int g = e / D;
-                qs[e] = static_cast<const float *>(a.Q.ptr)[cur.b * a.Q.sb + (int64_t)(cur.hk * a.G + g) * a.Q.sh + e % D];
+    if (c < n_cta) {  // every CTA below n_cta has a tile
+        const int64_t t0 = total * c / n_cta, t1 = total * (c + 1) / n_cta;
+        Place<KT> cur = find_tile<KT>(a, Hk, t0);  // the CTA's current row, at its first tile here
+        Place<KT> ld = cur;
+        ld.advance(a, Hk, warp);
+        int64_t at = t0 + warp;
+        int put = 0, got = 0;  // stages written, read
+        auto next_load = [&] {
+            if (at < t1) {
+                load_kv<T, D, KT>(a, ld, ring + put * kStage);
+                ld.advance(a, Hk, kWarps);
+                at += kWarps;
             }
+            if (++put == kStages) put = 0;
+            cp_async_commit();
+        };
+#pragma unroll 1
+        for (int i = 0; i < kStages - 1; ++i) next_load();
+        for (int64_t t = t0; t < t1;) {  // a row, or what of it is this CTA's
+            const int64_t row0 = t - cur.k;  // the row's first tile
+            const int64_t end = min(t1, row0 + cur.v.tiles);
+            if (sizeof(T) == 4) {  // (the row before has been joined)
+                for (int e = threadIdx.x; e < a.G * D; e += kThr) {
+                    const int g = e / D;
+                    qs[e] = static_cast<const float *>(a.Q.ptr)[cur.b * a.Q.sb + (int64_t)(cur.hk * a.G + g) * a.Q.sh + e % D];
+                }
+                __syncthreads();
+            }
+            Rows<T, D> rows;
+            rows.start(a, cur.b, cur.hk, qs);
+            Place<KT> p = cur;
+            const int skip = (int)((warp - (t - t0)) & (kWarps - 1));  // this warp's first tile at or after t
+            p.k += skip;
+            const int n = (int)(end - t);
+#pragma unroll 1
+            for (int x = skip; x < n; x += kWarps, p.k += kWarps) {
+                next_load();
+                cp_async_wait<kStages - 1>();
+                __syncwarp();
+                rows.tile(a, p, ring + got * kStage, scale2, qs);
+                if (++got == kStages) got = 0;
+                __syncwarp();
+            }
+            rows.finish(sm + warp * kMaxGroupHeads, sl + warp * kMaxGroupHeads, so + warp * a.G * D, a.G);
             __syncthreads();
-        }
-        Rows<T, D> rows;
-        rows.start(a, cur.b, cur.hk, qs);
-        Place<KT> p = cur;
-        // this warp's first tile at or after t
-        const int skip = (int)((warp - (t - t0)) % kWarps + kWarps) % kWarps;
-        p.k += skip;
-        for (int64_t x = t + skip; x < end; x += kWarps, p.k += kWarps) {
-            next_load();
-            cp_async_wait<kStages - 1>();
-            __syncwarp();
-            rows.tile(a, p, ring + got % kStages * kStage, scale2, qs);
-            ++got;
-            __syncwarp();
-        }
-        rows.finish(sm + warp * kMaxGroupHeads, sl + warp * kMaxGroupHeads, so + warp * kMaxGroupHeads * D);
-        __syncthreads();
-        const int64_t rowidx = (int64_t)cur.b * Hk + cur.hk;
-        const int64_t c0 = cta_of(row0), c1 = cta_of(row0 + cur.v.tiles - 1);
-        const bool alone = c0 == c1 && a.slots == 0;
-        for (int g = warp; g < a.G; g += kWarps) {
-            float mx = -INFINITY, z = 0.f, r[kE] = {};
+            const int64_t rowidx = (int64_t)cur.b * Hk + cur.hk;
+            const bool alone = a.slots == 0 && row0 >= t0 && row0 + cur.v.tiles <= t1;
+            for (int g = warp; g < a.G; g += kWarps) {
+                float mx = -INFINITY, z = 0.f, r[kE] = {};
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm[w * kMaxGroupHeads + g]);
+                for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm[w * kMaxGroupHeads + g]);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float lw = sl[w * kMaxGroupHeads + g], f = lw > 0.f ? exp2f(sm[w * kMaxGroupHeads + g] - mx) : 0.f;
-                z = fmaf(f, lw, z);
+                for (int w = 0; w < kWarps; ++w) {
+                    const float lw = sl[w * kMaxGroupHeads + g], f = lw > 0.f ? exp2f(sm[w * kMaxGroupHeads + g] - mx) : 0.f;
+                    z = fmaf(f, lw, z);
 #pragma unroll
-                for (int e = 0; e < kE; ++e) r[e] = fmaf(f, so[(w * kMaxGroupHeads + g) * D + lane * kE + e], r[e]);
-            }
-            const float inv = z > 0.f ? 1.f / z : 0.f, lse = z > 0.f ? (mx + log2f(z)) * kLn2 : -INFINITY;
-            const int h = cur.hk * a.G + g;
-            if (alone) {
-                T *dst = static_cast<T *>(a.O.ptr) + cur.b * a.O.sb + h * a.O.sh + lane * kE;
-#pragma unroll
-                for (int e = 0; e < kE; e += 2) store2(dst + e, r[e] * inv, r[e + 1] * inv);
-                if (lane == 0) a.lse[(int64_t)cur.b * a.H + h] = lse;
-            } else {
-                const int64_t seg = (c + rowidx) * a.G + g;
-#pragma unroll
-                for (int e = 0; e < kE; e += 2) store2(a.seg_o + seg * D + lane * kE + e, r[e] * inv, r[e + 1] * inv);
-                if (lane == 0) a.seg_lse[seg] = lse;
-            }
-        }
-        if (!alone) {
-            __threadfence();
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                const int before = atomicAdd(a.counters + rowidx, 1);
-                *flag = before == (int)(c1 - c0);
-                if (*flag) a.counters[rowidx] = 0;  // as the next call finds it
-            }
-            __syncthreads();
-            if (*flag) {
-                __threadfence();
-                for (int g = warp; g < a.G; g += kWarps) {
-                    const int h = cur.hk * a.G + g, ns = (int)(c1 - c0) + 1, all = ns + a.slots;
-                    const int64_t row = (int64_t)cur.b * a.H + h;
-                    // partial s: the prefix kernel's slots, then the CTAs' segments in order
-                    auto lse_of = [&](int s) {
-                        return s < a.slots ? __ldcg(a.part_lse + row * a.slots + s)
-                                           : __ldcg(a.seg_lse + (c0 + (s - a.slots) + rowidx) * a.G + g);
-                    };
-                    float mx = -INFINITY, z = 0.f;
-                    for (int s = lane; s < all; s += 32) mx = fmaxf(mx, lse_of(s));
-                    mx = warp_max(mx);
-                    const float ref = mx == -INFINITY ? 0.f : mx;
-                    float r[kE] = {};
-                    for (int s0 = 0; s0 < all; s0 += 32) {
-                        const float wl = s0 + lane < all ? expf(lse_of(s0 + lane) - ref) : 0.f;
-                        z += wl;
-                        const int m = min(32, all - s0);
-#pragma unroll 4
-                        for (int i = 0; i < m; ++i) {
-                            const int s = s0 + i;
-                            const float w = __shfl_sync(kFull, wl, i);
-                            const float *src = s < a.slots ? a.part_o + (row * a.slots + s) * D
-                                                           : a.seg_o + ((c0 + (s - a.slots) + rowidx) * a.G + g) * D;
-#pragma unroll
-                            for (int e = 0; e < kE; e += 2) {
-                                const float2 x = __ldcg(reinterpret_cast<const float2 *>(src + lane * kE + e));
-                                r[e] = fmaf(w, x.x, r[e]);
-                                r[e + 1] = fmaf(w, x.y, r[e + 1]);
-                            }
-                        }
-                    }
-                    z = warp_sum(z);
-                    const float inv = z > 0.f ? 1.f / z : 0.f;
+                    for (int e = 0; e < kE; ++e) r[e] = fmaf(f, so[(w * a.G + g) * D + lane * kE + e], r[e]);
+                }
+                const float inv = z > 0.f ? 1.f / z : 0.f, lse = z > 0.f ? (mx + log2f(z)) * kLn2 : -INFINITY;
+                const int h = cur.hk * a.G + g;
+                if (alone) {
                     T *dst = static_cast<T *>(a.O.ptr) + cur.b * a.O.sb + h * a.O.sh + lane * kE;
 #pragma unroll
                     for (int e = 0; e < kE; e += 2) store2(dst + e, r[e] * inv, r[e + 1] * inv);
-                    if (lane == 0) a.lse[row] = z > 0.f ? mx + logf(z) : -INFINITY;
+                    if (lane == 0) a.lse[(int64_t)cur.b * a.H + h] = lse;
+                } else {
+                    const int64_t seg = (c + rowidx) * a.G + g;
+#pragma unroll
+                    for (int e = 0; e < kE; e += 2) store2(a.seg_o + seg * D + lane * kE + e, r[e] * inv, r[e + 1] * inv);
+                    if (lane == 0) a.seg_lse[seg] = lse;
                 }
             }
+            __syncthreads();  // sm, sl, so, qs are free again
+            cur.advance(a, Hk, n);
+            t = end;
         }
-        __syncthreads();  // sm, sl, so are free again
-        cur.advance(a, Hk, (int)(end - t));
-        t = end;
+        cp_async_wait<0>();
     }
-    cp_async_wait<0>();
+    pdl_wait();  // the prefix kernel's partial results are complete when this grid is
+}
+
+// One warp per row (b, h): the partial results of the prefix kernel's slots and of the decode
+// CTAs' segments, in that order; weights exp(lse_s - max). Rows that one CTA has finished are left.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) sink_decode_combine_kernel(SinkDecodeArgs a, int ctas) {
+    constexpr int KT = tile_keys<T>(), kE = D / 32;
+    const int Hk = a.H / a.G, lane = threadIdx.x % 32;
+    const int64_t rows = (int64_t)a.B * a.H, row = min((int64_t)blockIdx.x * 4 + threadIdx.x / 32, rows - 1);
+    const int b = (int)(row / a.H), h = (int)(row % a.H), hk = h / a.G, g = h % a.G;
+    int64_t before = 0, total = 0;
+    for (int i = lane; i < a.B; i += 32) {
+        const int64_t n = (int64_t)visible<KT>(a, i).tiles * Hk;
+        total += n;
+        before += i < b ? n : 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(kFull, total, o);
+        before += __shfl_xor_sync(kFull, before, o);
+    }
+    const int tiles = visible<KT>(a, b).tiles;
+    const int64_t first = before + (int64_t)hk * tiles, n_cta = min((int64_t)ctas, total);
+    auto cta_of = [&](int64_t tile) { return ((tile + 1) * n_cta - 1) / total; };
+    const int64_t c0 = cta_of(first), seg0 = c0 + (int64_t)b * Hk + hk;
+    const int ns = (int)(cta_of(first + tiles - 1) - c0) + 1, all = a.slots + ns;
+    pdl_wait();  // every thread: this grid must not be over before the one that it follows
+    if (all == 1 || (int64_t)blockIdx.x * 4 + threadIdx.x / 32 >= rows) return;
+    auto lse_of = [&](int s) {
+        return s < a.slots ? a.part_lse[row * a.slots + s] : a.seg_lse[(seg0 + (s - a.slots)) * a.G + g];
+    };
+    auto row_of = [&](int s) {
+        return (s < a.slots ? a.part_o + (row * a.slots + s) * D : a.seg_o + ((seg0 + (s - a.slots)) * a.G + g) * D) + lane * kE;
+    };
+    float mx = -INFINITY, z = 0.f, r[kE] = {};
+    for (int s = lane; s < all; s += 32) mx = fmaxf(mx, lse_of(s));
+    mx = warp_max(mx);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    for (int s0 = 0; s0 < all; s0 += 32) {
+        const float wl = s0 + lane < all ? expf(lse_of(s0 + lane) - ref) : 0.f;
+        z += wl;
+        const int m = min(32, all - s0);
+#pragma unroll 8
+        for (int i = 0; i < m; ++i) {
+            const float w = __shfl_sync(kFull, wl, i);
+            const float *src = row_of(s0 + i);
+#pragma unroll
+            for (int e = 0; e < kE; e += 2) {
+                const float2 x = load2(src + e);
+                r[e] = fmaf(w, x.x, r[e]);
+                r[e + 1] = fmaf(w, x.y, r[e + 1]);
+            }
+        }
+    }
+    z = warp_sum(z);
+    const float inv = z > 0.f ? 1.f / z : 0.f;
+    T *dst = static_cast<T *>(a.O.ptr) + b * a.O.sb + h * a.O.sh + lane * kE;
+#pragma unroll
+    for (int e = 0; e < kE; e += 2) store2(dst + e, r[e] * inv, r[e + 1] * inv);
+    if (lane == 0) a.lse[row] = z > 0.f ? mx + logf(z) : -INFINITY;
 }
 
 // One warp per row: weights exp(lse_s - max) over the row's slots, in slot order.
@@ -549,31 +559,45 @@ __global__ void __launch_bounds__(256) sink_combine_kernel(SinkCombineArgs a) {
     if (lane == 0 && a.lse) a.lse[row] = z > 0.f ? mx + logf(z) : -INFINITY;
 }
 
+// acc_out = acc + the weights of the group's heads, kAcc slots 256 apart for each thread (their
+// loads in flight together).
+constexpr int kAcc = 4;
 __global__ void __launch_bounds__(256) sink_acc_kernel(SinkDecodeArgs a, const float *lse, const float *acc, float *acc_out,
                                                        int chunks) {
     const int Hk = a.H / a.G;
-    const int bk = blockIdx.x / chunks, b = bk / Hk, hk = bk % Hk;
-    const int v = (blockIdx.x % chunks) * 256 + threadIdx.x;
+    const int bk = blockIdx.x / chunks, b = bk / Hk, hk = bk - b * Hk;
+    const int v0 = (blockIdx.x - bk * chunks) * (256 * kAcc) + threadIdx.x;
     const int n = min(max(__ldg(a.cache_len + b), 0), a.T);
     int sinks, lo;
     sink_visible(n, a.W, a.A, &sinks, &lo);
-    if (v >= sinks + n - lo) return;
-    const int64_t j = v < sinks ? v : lo + (v - sinks);
-    const int64_t row = (int64_t)b * a.H + hk * a.G;
-    float w = 0.f;
-    for (int g = 0; g < a.G; ++g)
-        w += exp2f(a.logits[(row + g) * a.logit_stride + v] - __ldg(lse + row + g) * 1.4426950408889634f);
-    const int64_t at = ((int64_t)b * Hk + hk) * a.T + j;
-    acc_out[at] = acc[at] + w;
+    const int nvis = sinks + n - lo;
+    const int64_t row = (int64_t)b * a.H + hk * a.G, out = ((int64_t)b * Hk + hk) * a.T;
+    pdl_wait();
+    if (v0 >= nvis) return;
+    float w[kAcc] = {};
+    for (int g = 0; g < a.G; ++g) {
+        const float L = lse[row + g] * kLog2e;
+        const float *s = a.logits + (row + g) * a.logit_stride + v0;
+#pragma unroll
+        for (int k = 0; k < kAcc; ++k)
+            if (v0 + 256 * k < nvis) w[k] += exp2f(s[256 * k] - L);
+    }
+#pragma unroll
+    for (int k = 0; k < kAcc; ++k) {
+        const int v = v0 + 256 * k;
+        if (v >= nvis) continue;
+        const int64_t at = out + (v < sinks ? v : lo + (v - sinks));
+        acc_out[at] = acc[at] + w[k];
+    }
 }
 
 }  // namespace
 
-// CTAs of a decode: one per SM, no more than there are tiles.
+// CTAs of a decode: two per SM, no more than there are tiles.
 int sink_decode_ctas(hils_dtype dt, int B, int Hk, int64_t keys, int sms) {
     const int kt = dt == HILS_BF16 ? tile_keys<bf16>() : tile_keys<float>();
     const int64_t tiles = (int64_t)B * Hk * (keys > kt ? (keys + kt - 1) / kt : 1);
-    return (int)(tiles < sms ? tiles : sms);
+    return (int)(tiles < 2 * sms ? tiles : 2 * sms);
 }
 
 namespace {
@@ -581,10 +605,25 @@ template <typename T, int D>
 hils_status decode(const SinkDecodeArgs &a, int ctas, cudaStream_t s) {
     static KernelSetup setup;
     const auto k = sink_decode_kernel<T, D>;
-    const hils_status st = kernel_setup(setup, (const void *)k, kThr, decode_smem<T, D>(), nullptr);
+    hils_status st = kernel_setup(setup, (const void *)k, kThr, decode_smem<T, D>(kMaxGroupHeads), nullptr);
     if (st != HILS_OK) return st;
-    k<<<ctas, kThr, decode_smem<T, D>(), s>>>(a);
-    return record_cuda_error(cudaGetLastError());
+    if (a.slots) {  // it may begin while the prefix kernel ends
+        st = launch_dependent((const void *)k, dim3(ctas), dim3(kThr), decode_smem<T, D>(a.G), s, a);
+    } else {
+        k<<<ctas, kThr, decode_smem<T, D>(a.G), s>>>(a);
+        st = record_cuda_error(cudaGetLastError());
+    }
+    if (st != HILS_OK) return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(((int64_t)a.B * a.H + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return record_cuda_error(cudaLaunchKernelEx(&cfg, sink_decode_combine_kernel<T, D>, a, ctas));
 }
 }  // namespace
 
@@ -609,12 +648,20 @@ hils_status launch_sink_combine(hils_dtype dt, int d, const SinkCombineArgs &a, 
 
 hils_status launch_sink_decode_acc(const SinkDecodeArgs &a, const float *lse, const float *acc, float *acc_out,
                                    cudaStream_t s) {
-    const int chunks = (int)((a.logit_stride + 255) / 256);
+    const int chunks = (int)((a.logit_stride + 256 * kAcc - 1) / (256 * kAcc));
     const int64_t grid = (int64_t)a.B * (a.H / a.G) * chunks;
     if (grid == 0) return HILS_OK;
     if (grid > 0x7fffffffll) return HILS_ERR_UNSUPPORTED;
-    sink_acc_kernel<<<(unsigned)grid, 256, 0, s>>>(a, lse, acc, acc_out, chunks);
-    return record_cuda_error(cudaGetLastError());
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return record_cuda_error(cudaLaunchKernelEx(&cfg, sink_acc_kernel, a, lse, acc, acc_out, chunks));
 }
 
 }  // namespace hils
