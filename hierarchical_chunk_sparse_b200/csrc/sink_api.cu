@@ -74,7 +74,10 @@ DecodePlan decode_plan(const hils_params *p, int64_t T, int64_t A, int64_t P, bo
     const int Hk = p->H / groups(p), sms = device_sm_count();
     const int64_t rows = (int64_t)p->B * p->H;
     d.keys = prefix ? T : (T < A + p->W ? T : A + p->W);
-    d.prefix_splits = prefix ? sink_prefix_splits(p->B, Hk, groups(p), (int)P, sms) : 0;
+    // a prefix that is cheaper read by each sequence than in a pass of its own
+    const bool direct = prefix && sink_prefix_direct(p->dtype, p->d, p->B, Hk, P);
+    if (direct) d.keys = P + T;
+    d.prefix_splits = prefix && !direct ? sink_prefix_splits(p->B, Hk, groups(p), (int)P, sms) : 0;
     d.ctas = sink_decode_ctas(p->dtype, p->B, Hk, d.keys, sms);
     d.segs = d.ctas + (int64_t)p->B * Hk;
     d.bytes = kSinkStatusBytes + sink_part_bytes(rows, d.prefix_splits, p->d) +
@@ -286,6 +289,8 @@ int hils_sink_decode(const hils_params *p, int A, hils_ctensor Q, hils_ctensor K
         a.logits = ws.take<float>((size_t)rows * plan.keys);
         a.logit_stride = plan.keys;
     }
+    // few slots a row: a second launch would cost more than sharing the rows saves
+    a.whole = plan.keys <= kSinkWholeRow;
     HILS_TRY(launch_sink_decode(p->dtype, p->d, a, plan.ctas, stream));
     return acc ? launch_sink_decode_acc(a, a.lse, acc, acc_out, stream) : HILS_OK;
 }
@@ -341,7 +346,14 @@ int hils_prefix_decode(const hils_params *p, hils_ctensor Q, hils_ctensor Kp, hi
     a.part_o = const_cast<float *>(s.part_o);
     a.part_lse = const_cast<float *>(s.part_lse);
     a.wait_ns = work_wait_ns(p->flags);
-    HILS_TRY(forward(p, a, stream));
+    if (plan.prefix_splits == 0) {  // each sequence reads the prefix before its own cache
+        s.Kp = a.K;
+        s.Vp = a.V;
+        s.P = P;
+        s.whole = (int64_t)P + T <= kSinkWholeRow;
+    } else {
+        HILS_TRY(forward(p, a, stream));
+    }
     return launch_sink_decode(p->dtype, p->d, s, plan.ctas, stream);
 }
 

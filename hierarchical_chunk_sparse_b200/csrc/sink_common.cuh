@@ -78,6 +78,11 @@ inline int sink_prefix_splits(int B, int Hk, int G, int P, int sms) {
     const int64_t s = fill < most ? fill : most;
     return (int)(s < 1 ? 1 : s > 128 ? 128 : s);
 }
+// Whether each sequence reads a shared prefix by itself (from L2, after the first): its bytes.
+inline bool sink_prefix_direct(hils_dtype dt, int d, int B, int Hk, int64_t P) {
+    if (dt == HILS_F32) return B <= 5;
+    return B == 1 || (int64_t)B * Hk * P * d * 4 <= (64ll << 20);
+}
 inline size_t sink_part_bytes(int64_t rows, int slots, int d) {
     return sink_align((size_t)rows * slots * d * 4) + sink_align((size_t)rows * slots * 4);
 }
@@ -185,6 +190,7 @@ hils_status launch_sink_reduce(hils_dtype dt, int d, const SinkBwdArgs &a, bool 
 
 // ------------------------------------------------------------------ decode
 
+constexpr int kSinkWholeRow = 1024;  // longest row that one CTA takes by itself
 struct SinkDecodeArgs {
     View Q, K, V;
     MutView O;
@@ -194,6 +200,7 @@ struct SinkDecodeArgs {
     float scale;
     View Kp, Vp;               // P shared tokens before each sequence's own, read per sequence
     int P = 0;
+    bool whole = false;        // no row is shared between CTAs: one launch, nothing to join
     // partial results of rows (b, h) from another kernel: part_o [rows][slots][d], part_lse [rows][slots]
     const float *part_o, *part_lse;
     int slots = 0;

@@ -4,17 +4,19 @@
 namespace hils {
 namespace {
 
-constexpr int kThr = 128, kWarps = kThr / 32, kStages = 3;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <typename T>
 constexpr int tile_keys() { return sizeof(T) == 2 ? 16 : 8; }
 template <typename T, int D>
 constexpr int tile_bytes() { return tile_keys<T>() * D * (int)sizeof(T); }  // of K, and of V
+// stages of a warp's ring (what fits beside the results of eight warps and heads)
+template <typename T, int kWarps>
+constexpr int ring_stages() { return kWarps == 8 && sizeof(T) == 4 ? 2 : 3; }
 // the warps' rings, their results of a row, and (float32) its queries
-template <typename T, int D>
+template <typename T, int D, int kWarps>
 int decode_smem(int G) {
-    return kWarps * kStages * 2 * tile_bytes<T, D>() + kWarps * kMaxGroupHeads * 8 + kWarps * G * D * 4 +
+    return kWarps * ring_stages<T, kWarps>() * 2 * tile_bytes<T, D>() + kWarps * kMaxGroupHeads * 8 + kWarps * G * D * 4 +
            (sizeof(T) == 4 ? G * D * 4 : 0);
 }
 
@@ -32,6 +34,11 @@ __device__ __forceinline__ Visible visible(const SinkDecodeArgs &a, int b) {
     v.n = a.P + v.sinks + len - v.lo;
     v.tiles = max(1, (v.n + KT - 1) / KT);  // an empty row still gets its outputs
     return v;
+}
+
+// a / b of numbers that mostly fit 32 bits (a 64-bit division takes some 100 instructions).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    return (uint64_t)a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
 // A place in the flattened tiles of all (b, key-value head) rows.
@@ -82,8 +89,8 @@ __device__ Place<KT> find_tile(const SinkDecodeArgs &a, int Hk, int64_t at) {
         p.b = min(b0 + l, a.B - 1);
         p.v = visible<KT>(a, p.b);
         const int64_t in = at - before;
-        p.hk = (int)(in / p.v.tiles);
-        p.k = (int)(in % p.v.tiles);
+        p.hk = (int)divide(in, p.v.tiles);
+        p.k = (int)(in - (int64_t)p.hk * p.v.tiles);
         return p;
     }
 }
@@ -369,10 +376,10 @@ struct Rows<float, D> {
 
 // The tiles of all rows are cut into one even share for each CTA, whatever the sequences'
 // lengths. A row that is one CTA's alone gets its output here; of any other, each CTA leaves
-// its share's result as a segment for the combine.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThr, 2) sink_decode_kernel(SinkDecodeArgs a) {
-    constexpr int KT = tile_keys<T>(), kE = D / 32;
+// its share's result as a segment for the combine. With `whole`, the shares end at rows.
+template <typename T, int D, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, 8 / kWarps) sink_decode_kernel(SinkDecodeArgs a) {
+    constexpr int KT = tile_keys<T>(), kE = D / 32, kThr = kWarps * 32, kStages = ring_stages<T, kWarps>();
     constexpr int kStage = 2 * tile_bytes<T, D>();
     extern __shared__ __align__(128) uint8_t smem[];
     const int Hk = a.H / a.G, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -380,10 +387,23 @@ __global__ void __launch_bounds__(kThr, 2) sink_decode_kernel(SinkDecodeArgs a) 
     float *sm = reinterpret_cast<float *>(smem + kWarps * kStages * kStage), *sl = sm + kWarps * kMaxGroupHeads;
     float *so = sl + kWarps * kMaxGroupHeads, *qs = so + kWarps * a.G * D;
     const float scale2 = a.scale * kLog2e;
-    const int64_t total = all_tiles<KT>(a, Hk), n_cta = min((int64_t)gridDim.x, total), c = blockIdx.x;
+    const int64_t total = a.whole ? (int64_t)a.B * Hk : all_tiles<KT>(a, Hk), c = blockIdx.x;
+    const int64_t n_cta = min((int64_t)gridDim.x, total);
     if (c < n_cta) {  // every CTA below n_cta has a tile
-        const int64_t t0 = total * c / n_cta, t1 = total * (c + 1) / n_cta;
-        Place<KT> cur = find_tile<KT>(a, Hk, t0);  // the CTA's current row, at its first tile here
+        int64_t t0 = divide(total * c, n_cta), t1 = divide(total * (c + 1), n_cta);
+        Place<KT> cur;  // the CTA's current row, at its first tile here
+        if (a.whole) {  // rows [t0, t1): their tiles, counted from 0
+            cur.b = (int)(t0 / Hk);
+            cur.hk = (int)(t0 % Hk);
+            cur.k = 0;
+            cur.v = visible<KT>(a, cur.b);
+            int64_t n = 0;
+            for (int64_t r = t0; r < t1; ++r) n += visible<KT>(a, (int)(r / Hk)).tiles;
+            t0 = 0;
+            t1 = n;
+        } else {
+            cur = find_tile<KT>(a, Hk, t0);
+        }
         Place<KT> ld = cur;
         ld.advance(a, Hk, warp);
         int64_t at = t0 + warp;
@@ -469,7 +489,7 @@ __global__ void __launch_bounds__(128) sink_decode_combine_kernel(SinkDecodeArgs
     constexpr int KT = tile_keys<T>(), kE = D / 32;
     const int Hk = a.H / a.G, lane = threadIdx.x % 32;
     const int64_t rows = (int64_t)a.B * a.H, row = min((int64_t)blockIdx.x * 4 + threadIdx.x / 32, rows - 1);
-    const int b = (int)(row / a.H), h = (int)(row % a.H), hk = h / a.G, g = h % a.G;
+    const int b = (int)divide(row, a.H), h = (int)(row - (int64_t)b * a.H), hk = h / a.G, g = h % a.G;
     int64_t before = 0, total = 0;
     for (int i = lane; i < a.B; i += 32) {
         const int64_t n = (int64_t)visible<KT>(a, i).tiles * Hk;
@@ -483,7 +503,7 @@ __global__ void __launch_bounds__(128) sink_decode_combine_kernel(SinkDecodeArgs
     }
     const int tiles = visible<KT>(a, b).tiles;
     const int64_t first = before + (int64_t)hk * tiles, n_cta = min((int64_t)ctas, total);
-    auto cta_of = [&](int64_t tile) { return ((tile + 1) * n_cta - 1) / total; };
+    auto cta_of = [&](int64_t tile) { return divide((tile + 1) * n_cta - 1, total); };
     const int64_t c0 = cta_of(first), seg0 = c0 + (int64_t)b * Hk + hk;
     const int ns = (int)(cta_of(first + tiles - 1) - c0) + 1, all = a.slots + ns;
     pdl_wait();  // every thread: this grid must not be over before the one that it follows
@@ -603,14 +623,24 @@ int sink_decode_ctas(hils_dtype dt, int B, int Hk, int64_t keys, int sms) {
 namespace {
 template <typename T, int D>
 hils_status decode(const SinkDecodeArgs &a, int ctas, cudaStream_t s) {
-    static KernelSetup setup;
-    const auto k = sink_decode_kernel<T, D>;
-    hils_status st = kernel_setup(setup, (const void *)k, kThr, decode_smem<T, D>(kMaxGroupHeads), nullptr);
+    static KernelSetup setup, whole;
+    hils_status st;
+    if (a.whole) {
+        const auto k = sink_decode_kernel<T, D, 8>;
+        st = kernel_setup(whole, (const void *)k, 256, decode_smem<T, D, 8>(kMaxGroupHeads), nullptr);
+        if (st != HILS_OK) return st;
+        const int64_t rows = (int64_t)a.B * (a.H / a.G), sms = device_sm_count();
+        k<<<(unsigned)(rows < sms ? rows : sms), 256, decode_smem<T, D, 8>(a.G), s>>>(a);
+        return record_cuda_error(cudaGetLastError());
+    }
+    const auto k = sink_decode_kernel<T, D, 4>;
+    const int smem = decode_smem<T, D, 4>(a.G);
+    st = kernel_setup(setup, (const void *)k, 128, decode_smem<T, D, 4>(kMaxGroupHeads), nullptr);
     if (st != HILS_OK) return st;
     if (a.slots) {  // it may begin while the prefix kernel ends
-        st = launch_dependent((const void *)k, dim3(ctas), dim3(kThr), decode_smem<T, D>(a.G), s, a);
+        st = launch_dependent((const void *)k, dim3(ctas), dim3(128), smem, s, a);
     } else {
-        k<<<ctas, kThr, decode_smem<T, D>(a.G), s>>>(a);
+        k<<<ctas, 128, smem, s>>>(a);
         st = record_cuda_error(cudaGetLastError());
     }
     if (st != HILS_OK) return st;
