@@ -404,37 +404,65 @@ def hils_summarize_backward(p: Params, K, LQ, dKsum, dBsum, dK, dLQ, N: int | No
         _stream(stream)))
 
 
-def _sink_call(call: str, p: Params, views, arrays, workspace, stream, make_args) -> None:
-    """Checks and makes one of the calls below: `views` (name, tensor, shape) are strided in
-    params.dtype, `arrays` (name, tensor, shape, dtype) dense; None is left to the C call.
-    Every tensor has to be on one device, whose current stream is used if `stream` is None."""
-    dev = None
-    for name, t, shape, dt in [(n, t, sh, p.dtype) for n, t, sh in views] + arrays:
+def _sink_call(call: str, p: Params, views, arrays, workspace, stream):
+    """Checks the tensors of one of the calls below, before the C call reads their pointers:
+    `views` (name, tensor, shape) are strided in params.dtype, `arrays` (name, tensor, shape,
+    dtype) dense; None is left to the C call. All have to be on one device. Gives the C
+    views and pointers in order, then a function that makes the call with that device
+    current, on `stream` or else the device's current stream."""
+    dev, dt, out = -1, p.dtype, []
+    for name, t, shape in views:
         if t is None:
+            out.append(_CTensor(None, 0, 0, 0))
             continue
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{call}: {name} has shape {tuple(t.shape)}, expected {shape}")
-        if t.dtype != dt:
-            raise ValueError(f"{call}: {name} has dtype {t.dtype}, expected {dt}")
-        if not t.is_cuda:
-            raise ValueError(f"{call}: {name} must be a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{call}: {name} is on {t.device}, other tensors on {dev}")
-    for name, t, _, _ in arrays:
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{call}: {name} must be dense (contiguous)")
-    if workspace is not None and dev is not None and workspace.device != dev:
-        raise ValueError(f"{call}: workspace is on {workspace.device}, other tensors on {dev}")
-    wp, wn = _ws(workspace)
-    fn = getattr(load_library(), call)
-    args = make_args()
-    if dev is not None and dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            _check(call, fn(ctypes.byref(p.c()), *args, wp, wn, _stream(stream)))
-    else:
-        _check(call, fn(ctypes.byref(p.c()), *args, wp, wn, _stream(stream)))
+        at = t.get_device()
+        if t.shape != shape or t.dtype != dt or at < 0 or (at != dev and dev >= 0):
+            _refuse(call, name, t, shape, dt, dev)
+        dev = at
+        st = t.stride()
+        if st[3] != 1 and shape[3] > 1:
+            raise ValueError(f"{call}: {name}: the head dimension must be contiguous")
+        out.append(_CTensor(t.data_ptr(), st[0], st[1], st[2]))
+    for name, t, shape, adt in arrays:
+        if t is None:
+            out.append(None)
+            continue
+        at = t.get_device()
+        if t.shape != shape or t.dtype != adt or at < 0 or (at != dev and dev >= 0) or not t.is_contiguous():
+            _refuse(call, name, t, shape, adt, dev)
+        dev = at
+        out.append(t.data_ptr())
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        if workspace.get_device() != dev and dev >= 0:
+            raise ValueError(f"{call}: workspace is on {workspace.device}, other tensors on cuda:{dev}")
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    fn = getattr(_lib or load_library(), call)
+
+    def run(*args) -> None:
+        if dev >= 0 and dev != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                rc = fn(p.c(), *args, ws, ws_bytes, _stream(stream))
+        else:
+            rc = fn(p.c(), *args, ws, ws_bytes, torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream))
+        if rc != 0:
+            _check(call, rc)
+
+    out.append(run)
+    return out
+
+
+def _refuse(call: str, name: str, t, shape, dtype, dev: int) -> None:
+    """Raises what is wrong with a tensor that _sink_call does not take."""
+    if t.shape != shape:
+        raise ValueError(f"{call}: {name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.dtype != dtype:
+        raise ValueError(f"{call}: {name} has dtype {t.dtype}, expected {dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{call}: {name} must be a CUDA tensor")
+    if dev >= 0 and t.get_device() != dev:
+        raise ValueError(f"{call}: {name} is on {t.device}, other tensors on cuda:{dev}")
+    raise ValueError(f"{call}: {name} must be dense (contiguous)")
 
 
 def _bhtd(call: str, name: str, t) -> int:
@@ -452,9 +480,9 @@ def hils_sink_prefill(p: Params, A: int, Q, K, V, O, lse=None, workspace=None, s
     call = "hils_sink_prefill"
     lq, n = _bhtd(call, "Q", Q), _bhtd(call, "K", K)
     q, kv = (p.B, p.H, lq, p.d), (p.B, p.Hk, n, p.d)
-    _sink_call(call, p, [("Q", Q, q), ("K", K, kv), ("V", V, kv), ("O", O, q)], [("lse", lse, q[:3], torch.float32)],
-               workspace, stream,
-               lambda: (A, _view(Q), lq, _view(K), _view(V), n, _view(O), _ptr(lse)))
+    cq, ck, cv, co, cl, run = _sink_call(call, p, (("Q", Q, q), ("K", K, kv), ("V", V, kv), ("O", O, q)),
+                                         (("lse", lse, q[:3], torch.float32),), workspace, stream)
+    run(A, cq, lq, ck, cv, n, co, cl)
 
 
 def hils_sink_prefill_backward(p: Params, A: int, Q, K, V, O, lse, dO, dQ, dK, dV, workspace=None, stream=None) -> None:
@@ -464,10 +492,10 @@ def hils_sink_prefill_backward(p: Params, A: int, Q, K, V, O, lse, dO, dQ, dK, d
     call = "hils_sink_prefill_backward"
     n = _bhtd(call, "Q", Q)
     q, kv = (p.B, p.H, n, p.d), (p.B, p.Hk, n, p.d)
-    _sink_call(call, p, [("Q", Q, q), ("K", K, kv), ("V", V, kv), ("O", O, q), ("dO", dO, q), ("dQ", dQ, q),
-                         ("dK", dK, kv), ("dV", dV, kv)], [("lse", lse, q[:3], torch.float32)], workspace, stream,
-               lambda: (A, _view(Q), _view(K), _view(V), n, _view(O), _ptr(lse), _view(dO), _view(dQ), _view(dK),
-                        _view(dV)))
+    cq, ck, cv, co, cdo, cdq, cdk, cdv, cl, run = _sink_call(
+        call, p, (("Q", Q, q), ("K", K, kv), ("V", V, kv), ("O", O, q), ("dO", dO, q), ("dQ", dQ, q), ("dK", dK, kv),
+                  ("dV", dV, kv)), (("lse", lse, q[:3], torch.float32),), workspace, stream)
+    run(A, cq, ck, cv, n, co, cl, cdo, cdq, cdk, cdv)
 
 
 def hils_sink_weights(p: Params, A: int, Q, K, lse, acc, acc_out=None, workspace=None, stream=None) -> None:
@@ -480,10 +508,11 @@ def hils_sink_weights(p: Params, A: int, Q, K, lse, acc, acc_out=None, workspace
     out = acc if acc_out is None else acc_out
     t = acc.shape[-1] if acc is not None else 0
     w = (p.B, p.Hk, t)
-    _sink_call(call, p, [("Q", Q, (p.B, p.H, lq, p.d)), ("K", K, (p.B, p.Hk, n, p.d))],
-               [("lse", lse, (p.B, p.H, lq), torch.float32), ("acc", acc, w, torch.float32),
-                ("acc_out", out, w, torch.float32)], workspace, stream,
-               lambda: (A, _view(Q), lq, _view(K), n, _ptr(lse), _ptr(acc), _ptr(out), t))
+    cq, ck, cl, ca, cw, run = _sink_call(
+        call, p, (("Q", Q, (p.B, p.H, lq, p.d)), ("K", K, (p.B, p.Hk, n, p.d))),
+        (("lse", lse, (p.B, p.H, lq), torch.float32), ("acc", acc, w, torch.float32), ("acc_out", out, w, torch.float32)),
+        workspace, stream)
+    run(A, cq, lq, ck, n, cl, ca, cw, t)
 
 
 def hils_sink_decode(p: Params, A: int, Q, Kc, Vc, cache_len, O, lse=None, acc=None, acc_out=None, workspace=None,
@@ -497,11 +526,11 @@ def hils_sink_decode(p: Params, A: int, Q, Kc, Vc, cache_len, O, lse=None, acc=N
     t = _bhtd(call, "Kc", Kc)
     out = acc if acc_out is None else acc_out
     q, kv, w = (p.B, p.H, 1, p.d), (p.B, p.Hk, t, p.d), (p.B, p.Hk, t)
-    _sink_call(call, p, [("Q", Q, q), ("Kc", Kc, kv), ("Vc", Vc, kv), ("O", O, q)],
-               [("cache_len", cache_len, (p.B,), torch.int32), ("lse", lse, (p.B, p.H), torch.float32),
-                ("acc", acc, w, torch.float32), ("acc_out", out, w, torch.float32)], workspace, stream,
-               lambda: (A, _view(Q), _view(Kc), _view(Vc), t, _ptr(cache_len), _view(O), _ptr(lse), _ptr(acc),
-                        _ptr(out)))
+    cq, ck, cv, co, cn, cl, ca, cw, run = _sink_call(
+        call, p, (("Q", Q, q), ("Kc", Kc, kv), ("Vc", Vc, kv), ("O", O, q)),
+        (("cache_len", cache_len, (p.B,), torch.int32), ("lse", lse, (p.B, p.H), torch.float32),
+         ("acc", acc, w, torch.float32), ("acc_out", out, w, torch.float32)), workspace, stream)
+    run(A, cq, ck, cv, t, cn, co, cl, ca, cw)
 
 
 def hils_prefix_decode(p: Params, Q, Kp, Vp, Kc, Vc, cache_len, O, lse=None, workspace=None, stream=None) -> None:
@@ -512,11 +541,10 @@ def hils_prefix_decode(p: Params, Q, Kp, Vp, Kc, Vc, cache_len, O, lse=None, wor
     call = "hils_prefix_decode"
     t, n = _bhtd(call, "Kc", Kc), _bhtd(call, "Kp", Kp)
     q, kv, pre = (p.B, p.H, 1, p.d), (p.B, p.Hk, t, p.d), (1, p.Hk, n, p.d)
-    _sink_call(call, p, [("Q", Q, q), ("Kp", Kp, pre), ("Vp", Vp, pre), ("Kc", Kc, kv), ("Vc", Vc, kv), ("O", O, q)],
-               [("cache_len", cache_len, (p.B,), torch.int32), ("lse", lse, (p.B, p.H), torch.float32)], workspace,
-               stream,
-               lambda: (_view(Q), _view(Kp), _view(Vp), n, _view(Kc), _view(Vc), t, _ptr(cache_len), _view(O),
-                        _ptr(lse)))
+    cq, ckp, cvp, ck, cv, co, cn, cl, run = _sink_call(
+        call, p, (("Q", Q, q), ("Kp", Kp, pre), ("Vp", Vp, pre), ("Kc", Kc, kv), ("Vc", Vc, kv), ("O", O, q)),
+        (("cache_len", cache_len, (p.B,), torch.int32), ("lse", lse, (p.B, p.H), torch.float32)), workspace, stream)
+    run(cq, ckp, cvp, n, ck, cv, t, cn, co, cl)
 
 
 def hils_cache_evict(p: Params, A: int, budget: int, K, V, acc, cache_len, Kout, Vout, acc_out, idx, len_out,
@@ -529,12 +557,12 @@ def hils_cache_evict(p: Params, A: int, budget: int, K, V, acc, cache_len, Kout,
     call = "hils_cache_evict"
     t = _bhtd(call, "K", K)
     kv, out = (p.B, p.Hk, t, p.d), (p.B, p.Hk, budget, p.d)
-    _sink_call(call, p, [("K", K, kv), ("V", V, kv), ("Kout", Kout, out), ("Vout", Vout, out)],
-               [("acc", acc, kv[:3], torch.float32), ("cache_len", cache_len, (p.B,), torch.int32),
-                ("acc_out", acc_out, out[:3], torch.float32), ("idx", idx, out[:3], torch.int32),
-                ("len_out", len_out, (p.B,), torch.int32)], workspace, stream,
-               lambda: (A, budget, _view(K), _view(V), t, _ptr(acc), _ptr(cache_len), _view(Kout), _view(Vout),
-                        _ptr(acc_out), _ptr(idx), _ptr(len_out)))
+    ck, cv, cko, cvo, ca, cn, cao, ci, clo, run = _sink_call(
+        call, p, (("K", K, kv), ("V", V, kv), ("Kout", Kout, out), ("Vout", Vout, out)),
+        (("acc", acc, kv[:3], torch.float32), ("cache_len", cache_len, (p.B,), torch.int32),
+         ("acc_out", acc_out, out[:3], torch.float32), ("idx", idx, out[:3], torch.int32),
+         ("len_out", len_out, (p.B,), torch.int32)), workspace, stream)
+    run(A, budget, ck, cv, t, ca, cn, cko, cvo, cao, ci, clo)
 
 
 def alloc_workspace(p: Params, call: int, Lq: int, C: int, device="cuda") -> torch.Tensor | None:

@@ -1,143 +1,195 @@
 // Eviction from a KV cache by accumulated attention weight. Per (b, key-value head) with
 // n = cache_len[b] tokens, n > budget: keep the slots [0, A), the W newest and, of the
-// slots between, the budget - A - W with the largest acc (equal ones: the lower slot; NaN
-// counts as the smallest). The kept rows are written in slot order.
+// slots between, the m = budget - A - W with the largest acc (equal ones: the lower slot;
+// NaN counts as the smallest). The kept rows are written in slot order.
 #include "sink_common.cuh"
 
 namespace hils {
 namespace {
 
-constexpr int kThr = 1024;
-
 // Order of the accumulated weights: larger float, larger key; -0 equals +0, NaN is lowest.
 __device__ __forceinline__ unsigned weight_key(float f) { return f != f ? 0u : ordered_key(f + 0.f); }
 
-// Exclusive sum over the block of (x, y); the totals in *tx, *ty.
-__device__ __forceinline__ void block_scan(int &x, int &y, int *total_x, int *total_y, int2 *sh) {
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    int ix = x, iy = y;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int ax = __shfl_up_sync(kFull, ix, o), ay = __shfl_up_sync(kFull, iy, o);
-        if (lane >= o) {
-            ix += ax;
-            iy += ay;
-        }
-    }
-    __syncthreads();
-    if (lane == 31) sh[warp] = make_int2(ix, iy);
-    __syncthreads();
-    int bx = 0, by = 0, tx = 0, ty = 0;
-    for (int w = 0; w < kThr / 32; ++w) {
-        if (w == warp) {
-            bx = tx;
-            by = ty;
-        }
-        tx += sh[w].x;
-        ty += sh[w].y;
-    }
-    x = bx + ix - x;
-    y = by + iy - y;
-    *total_x = tx;
-    *total_y = ty;
-}
-
-// One CTA per (b, head): the threshold by a radix select of 8 bits a pass, then the kept
-// slots in order.
-__global__ void __launch_bounds__(kThr) evict_select_kernel(EvictArgs a) {
-    __shared__ unsigned hist[256];
-    __shared__ unsigned s_digit;
-    __shared__ int s_need;
-    __shared__ int2 sh[kThr / 32];
-    const int tid = threadIdx.x;
+// One CTA per (b, head): the m-th largest key bit by bit, each bit a count over keys held in
+// registers (32 counts of up to 32 keys a thread; a histogram's shared atomics collide on the
+// few exponents that the weights have, and took 70 us of this kernel's 77 at 64 x 32K). It
+// ends early once exactly m keys reach the trial. Warp w holds the keys of R * 32 consecutive
+// slots; those behind THR * R slots are read again for each bit.
+template <int THR, int R>
+__global__ void __launch_bounds__(THR) evict_select_kernel(EvictArgs a) {
+    constexpr int kW = THR / 32;
+    __shared__ int sh[2][kW];
+    __shared__ int2 base[kW];
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int64_t bk = blockIdx.x;
     const int b = (int)(bk / a.Hk);
     const int n = min(max(__ldg(a.cache_len + b), 0), a.T);
     const float *acc = a.acc + bk * a.T;
     int32_t *idx = a.idx + bk * a.budget;
     if (n <= a.budget) {
-        for (int i = tid; i < a.budget; i += kThr) idx[i] = i < n ? i : -1;
+        for (int i = tid; i < a.budget; i += THR) idx[i] = i < n ? i : -1;
         return;
     }
     const int m0 = a.A, m1 = n - a.W, m = a.budget - a.A - a.W;  // m of [m0, m1), fewer than there are
-    unsigned prefix = 0u, mask = 0u;
-    int need = m;  // of the slots whose key has the prefix
-    for (int shift = 24; shift >= 0 && m > 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kThr) hist[i] = 0u;
-        __syncthreads();
-        for (int i = m0 + tid; i < m1; i += kThr) {
-            const unsigned k = weight_key(acc[i]);
-            if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
-        }
-        __syncthreads();
-        if (tid == 0) {
-            int left = need, dgt = 255;
-            while (dgt > 0 && (int)hist[dgt] < left) left -= (int)hist[dgt--];
-            s_digit = (unsigned)dgt;
-            s_need = left;
-        }
-        __syncthreads();
-        prefix |= s_digit << shift;
-        mask |= 255u << shift;
-        need = s_need;
-        __syncthreads();
-    }
-    for (int i = tid; i < a.A; i += kThr) idx[i] = i;
-    for (int i = tid; i < a.W; i += kThr) idx[a.budget - a.W + i] = n - a.W + i;
+    for (int i = tid; i < a.A; i += THR) idx[i] = i;
+    for (int i = tid; i < a.W; i += THR) idx[a.budget - a.W + i] = n - a.W + i;
     if (m == 0) return;
-    int kept = 0, equal = 0;  // before this round: above the threshold, at it
-    for (int i0 = m0; i0 < m1; i0 += kThr) {
-        const int i = i0 + tid;
-        const unsigned k = i < m1 ? weight_key(acc[i]) : 0u;
-        int gt = i < m1 && k > prefix, eq = i < m1 && k == prefix, tg, te;
-        const bool is_gt = gt != 0, is_eq = eq != 0;
-        block_scan(gt, eq, &tg, &te, sh);
-        const int before_eq = equal + eq;
-        if (is_gt || (is_eq && before_eq < need)) idx[a.A + kept + gt + min(before_eq, need)] = i;
-        kept += tg;
-        equal += te;
+    const int mid = m1 - m0, far = THR * R;  // slots [far, mid) of the middle stay in memory
+    unsigned key[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int i = (warp * R + r) * 32 + lane;
+        key[r] = i < mid ? weight_key(__ldg(acc + m0 + i)) : 0u;
+    }
+    unsigned thr = 0u;  // the largest trial that at least m keys reach
+    bool exact = false; // exactly m do
+    for (int bit = 31; bit >= 0 && !exact; --bit) {
+        const unsigned trial = thr | (1u << bit);
+        int c = 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) c += key[r] >= trial;
+        for (int i = far + tid; i < mid; i += THR) c += weight_key(__ldg(acc + m0 + i)) >= trial;
+        c = __reduce_add_sync(kFull, c);
+        if (lane == 0) sh[bit & 1][warp] = c;
         __syncthreads();
+        c = __reduce_add_sync(kFull, lane < kW ? sh[bit & 1][lane] : 0);
+        if (c >= m) {
+            thr = trial;
+            exact = c == m;
+        }
+    }
+    // keys above thr are kept, and of those equal to it the first need (all of them if exact)
+    auto kind = [&](int i, unsigned k) { return i >= mid ? 0 : k > thr || (exact && k == thr) ? 2 : k == thr ? 1 : 0; };
+    int2 mine = make_int2(0, 0);  // of this warp's register slots: above, equal
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int t = kind((warp * R + r) * 32 + lane, key[r]);
+        mine.x += __popc(__ballot_sync(kFull, t == 2));
+        mine.y += __popc(__ballot_sync(kFull, t == 1));
+    }
+    if (lane == 0) base[warp] = mine;
+    int c = 0;  // above, in all
+    for (int i = far + tid; i < mid; i += THR) c += kind(i, weight_key(__ldg(acc + m0 + i))) == 2;
+    c = __reduce_add_sync(kFull, c);
+    __syncthreads();  // (sh: every warp is behind its last read)
+    if (lane == 0) sh[0][warp] = c + mine.x;
+    __syncthreads();
+    const int above = __reduce_add_sync(kFull, lane < kW ? sh[0][lane] : 0), need = m - above;
+    int2 at = make_int2(0, 0), all = make_int2(0, 0);
+    for (int w = 0; w < kW; ++w) {
+        const int2 x = base[w];
+        if (w < warp) at = make_int2(at.x + x.x, at.y + x.y);
+        all = make_int2(all.x + x.x, all.y + x.y);
+    }
+    auto keep = [&](int i, int t, int2 &p) {
+        const unsigned up = __ballot_sync(kFull, t == 2), eq = __ballot_sync(kFull, t == 1), lower = (1u << lane) - 1u;
+        const int gt = p.x + __popc(up & lower), eb = p.y + __popc(eq & lower);
+        if (t == 2 || (t == 1 && eb < need)) idx[a.A + gt + min(eb, need)] = m0 + i;
+        p.x += __popc(up);
+        p.y += __popc(eq);
+    };
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int i = (warp * R + r) * 32 + lane;
+        keep(i, kind(i, key[r]), at);
+    }
+    // the slots that stayed in memory: THR at a time, in order
+    for (int i0 = far; i0 < mid; i0 += THR) {
+        const int i = i0 + tid, t = i < mid ? kind(i, weight_key(__ldg(acc + m0 + i))) : 0;
+        const int2 x = make_int2(__popc(__ballot_sync(kFull, t == 2)), __popc(__ballot_sync(kFull, t == 1)));
+        __syncthreads();
+        if (lane == 0) base[warp] = x;
+        __syncthreads();
+        int2 p = all;
+        for (int w = 0; w < kW; ++w) {
+            const int2 y = base[w];
+            if (w < warp) p = make_int2(p.x + y.x, p.y + y.y);
+            all = make_int2(all.x + y.x, all.y + y.y);
+        }
+        keep(i, t, p);
     }
 }
 
-// One warp per kept row; row 0 of head 0 also writes the sequence's new length.
-__global__ void __launch_bounds__(256) evict_gather_kernel(EvictArgs a, int units, int esize) {
-    const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+// Copies the kept rows: a warp takes 256 / U rows of U 16-byte units (K's, then V's), so that
+// each lane has eight loads in flight; bound by HBM. Block 0 also writes the new lengths.
+template <int U>
+__global__ void __launch_bounds__(256) evict_gather_kernel(EvictArgs a, int esize) {
+    constexpr int kRows = 256 / U;
     const int lane = threadIdx.x % 32;
-    if (row >= (int64_t)a.B * a.Hk * a.budget) return;
-    const int r = (int)(row % a.budget);
-    const int64_t bk = row / a.budget;
-    const int b = (int)(bk / a.Hk), h = (int)(bk % a.Hk);
-    const int j = a.idx[row];
-    if (j < 0) return;
-    if (lane == 0) a.acc_out[row] = a.acc[bk * a.T + j];
-    const char *ks = static_cast<const char *>(a.K.ptr) + (b * a.K.sb + h * a.K.sh + (int64_t)j * a.K.st) * esize;
-    const char *vs = static_cast<const char *>(a.V.ptr) + (b * a.V.sb + h * a.V.sh + (int64_t)j * a.V.st) * esize;
-    char *kd = static_cast<char *>(a.Kout.ptr) + (b * a.Kout.sb + h * a.Kout.sh + (int64_t)r * a.Kout.st) * esize;
-    char *vd = static_cast<char *>(a.Vout.ptr) + (b * a.Vout.sb + h * a.Vout.sh + (int64_t)r * a.Vout.st) * esize;
-    for (int u = lane; u < 2 * units; u += 32) {
-        const bool v = u >= units;
-        const int x = (v ? u - units : u) * 16;
-        *reinterpret_cast<uint4 *>((v ? vd : kd) + x) = __ldg(reinterpret_cast<const uint4 *>((v ? vs : ks) + x));
+    const int64_t rows = (int64_t)a.B * a.Hk * a.budget, r0 = ((int64_t)blockIdx.x * 8 + threadIdx.x / 32) * kRows;
+    pdl_wait();
+    if (blockIdx.x == 0)
+        for (int b = threadIdx.x; b < a.B; b += 256) a.len_out[b] = min(min(max(a.cache_len[b], 0), a.T), a.budget);
+    if (r0 >= rows) return;
+    const int my = lane < kRows && r0 + lane < rows ? a.idx[r0 + lane] : -1;
+    if (my >= 0) {
+        const int64_t bk = (r0 + lane) / a.budget;
+        a.acc_out[r0 + lane] = __ldg(a.acc + bk * a.T + my);
     }
+    uint4 v[8];
+    char *to[8];
+    // a row's (b, head) and place, kept while the rows go on within one head
+    int64_t bk = r0 / a.budget;
+    int r = (int)(r0 - bk * a.budget);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int e = i * 32 + lane, row = e / U, u = e % U;
+        const int j = __shfl_sync(kFull, my, row);
+        int64_t k = bk;
+        int rr = r + row;
+        while (rr >= a.budget) {
+            rr -= a.budget;
+            ++k;
+        }
+        const int b = (int)(k / a.Hk), h = (int)(k - (int64_t)b * a.Hk);
+        const bool val = u >= U / 2;
+        const View &s = val ? a.V : a.K;
+        const MutView &d = val ? a.Vout : a.Kout;
+        to[i] = nullptr;
+        if (j >= 0) {
+            const int x = (val ? u - U / 2 : u) * 16;
+            v[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const char *>(s.ptr) +
+                                                         (b * s.sb + h * s.sh + (int64_t)j * s.st) * esize + x));
+            to[i] = static_cast<char *>(d.ptr) + (b * d.sb + h * d.sh + (int64_t)rr * d.st) * esize + x;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (to[i]) *reinterpret_cast<uint4 *>(to[i]) = v[i];
 }
 
-__global__ void evict_len_kernel(EvictArgs a) {
-    const int b = blockIdx.x * blockDim.x + threadIdx.x;
-    if (b < a.B) a.len_out[b] = min(min(max(a.cache_len[b], 0), a.T), a.budget);
+template <int THR, int R>
+hils_status select(const EvictArgs &a, cudaStream_t s) {
+    evict_select_kernel<THR, R><<<(unsigned)(a.B * a.Hk), THR, 0, s>>>(a);
+    return record_cuda_error(cudaGetLastError());
+}
+
+template <int U>
+hils_status gather(const EvictArgs &a, int esize, cudaStream_t s) {
+    const int64_t rows = (int64_t)a.B * a.Hk * a.budget, per = 8 * (256 / U), grid = rows > 0 ? (rows + per - 1) / per : 1;
+    if (grid > 0x7fffffffll) return HILS_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = rows > 0 ? 1 : 0;
+    return record_cuda_error(cudaLaunchKernelEx(&cfg, evict_gather_kernel<U>, a, esize));
 }
 
 }  // namespace
 
 hils_status launch_cache_evict(hils_dtype dt, int d, const EvictArgs &a, cudaStream_t s) {
-    const int64_t heads = (int64_t)a.B * a.Hk, rows = heads * a.budget;
-    if (rows > 0) {
-        evict_select_kernel<<<(unsigned)heads, kThr, 0, s>>>(a);
-        const int esize = dt == HILS_BF16 ? 2 : 4;
-        evict_gather_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a, d * esize / 16, esize);
+    if ((int64_t)a.B * a.Hk * a.budget > 0) {
+        const hils_status st = a.T <= 2048 ? select<256, 8>(a, s) : a.T <= 16384 ? select<512, 32>(a, s) : select<1024, 32>(a, s);
+        if (st != HILS_OK) return st;
     }
-    if (a.B > 0) evict_len_kernel<<<(a.B + 255) / 256, 256, 0, s>>>(a);
-    return record_cuda_error(cudaGetLastError());
+    if (a.B == 0) return HILS_OK;
+    const int esize = dt == HILS_BF16 ? 2 : 4, units = 2 * d * esize / 16;
+    return units == 16 ? gather<16>(a, esize, s) : units == 32 ? gather<32>(a, esize, s) : gather<64>(a, esize, s);
 }
 
 }  // namespace hils
