@@ -1,20 +1,25 @@
 // Backward of the window-and-sink attention on the 5th-generation tensor cores (bf16;
-// formulas in sink_common.cuh): two persistent kernels, so that no sum is an atomic.
+// formulas in sink_common.cuh): one persistent kernel in two forms, so that no sum is an atomic.
 //
-// dQ, query-major: items of two 128-row query tiles A and B as in the prefill, 64-key tiles.
-//   S = Q K^T, T = dO V^T (M = 128 rows, N = 64 keys), dS = p (T - D) in bf16 over S,
-//   dQ += dS K with dS from TMEM; scale is applied once to the float32 sum.
-//   TMEM: S_A [0,64), S_B [64,128), T_A [128,192), T_B [192,256), dQ_A [256,384), dQ_B [384,512).
-// dK and dV, key-major: items of one 128-key block of a (b, key-value head) and a segment of
-//   its steps, a step being 64 queries of one head of the group.
-//   S^T = K Q^T, T^T = V dO^T (M = 128 keys, N = 64 queries), P^T and dS^T in bf16 over them,
-//   dV += P^T dO, dK += dS^T Q with P^T, dS^T from TMEM. S^T and T^T are double-buffered: even
-//   steps belong to softmax warps 0-3, odd ones to warps 4-7. lse and D of a step's queries
-//   are staged in shared memory, since a thread owns a key and runs over the queries.
-//   TMEM: S^T [0,64), [64,128), T^T [128,192), [192,256), dV [256,384), dK [384,512).
+// An item holds a tile X of 128 rows (TMEM lanes) and walks steps of 64 rows Y:
+//   dQ      X = Q, dO of 128 query rows (P packed heads x 128 / P queries, as in the prefill),
+//           Y = K, V of 64 keys;       acc: dQ += dS K
+//   dK, dV  X = K, V of 128 keys (a block and a segment of its steps),
+//           Y = Q, dO of 64 queries of one head of the group;   acc: dV += P^T dO, dK += dS^T Q
+//   S = X1 Y1^T, T = X2 Y2^T (M = 128, N = 64, K = d), p = exp2(S scale2 - lse2),
+//   dS = p (T - D); P and dS in bf16 from TMEM; scale once on the float32 sums.
 // Both recompute S and T: 7 products instead of the 5 of one kernel that would have to add
 // dQ (or dK and dV) across CTAs with atomics, whose order changes the result.
-// Warp roles and waits as in the prefill: 8 softmax warps, MMA, TMA.
+// Warps (640 threads), hand-offs through mbarriers:
+//   0-15   a thread owns a row of X; steps alternate between warps 0-7 and 8-15, each step's
+//          64 columns in two halves. S and T go into registers and are handed back before the
+//          arithmetic; P and dS have two buffers of their own. The warps of an item's last step
+//          write its sums while the others begin the next item.
+//   16, 17 tcgen05.mma of S and T; of the sums;  18  TMA;  19  lse and D of a step's queries
+//          (dK, dV: a thread owns a key and runs over the queries), fetched two steps ahead.
+// TMEM: S [0,64), T [64,128), P [128,160), [160,192), dS [192,224), [224,256), dV or dQ
+// [256,384), dK [384,512). Bound by the products: S, T take 48 cycles an MMA with N = 64 (their
+// operands come from shared memory), 1024 cycles a step for dQ and 1280 for dK, dV.
 #include "sink_tc.cuh"
 
 namespace hils {
@@ -22,347 +27,126 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384, kMmaWarp = 8, kLoadWarp = 10;
+constexpr int kM = 128, kRows = 64, kStages = 3;
+constexpr int kThreads = 640, kStWarp = 16, kSumWarp = 17, kLoadWarp = 18, kScalarWarp = 19;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
+static_assert(kM == kSinkKeys, "a key block is a tile");
 
-// lse in log2 units; +inf for a row that sees nothing, so that exp2(s - L) = 0
-__device__ __forceinline__ float log2_lse(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
-
-// 32 columns of p = exp2(s scale2 - L), 0 where masked, and ds = p (t - D).
-template <typename LF, typename DF>
-__device__ __forceinline__ void grad_columns(const uint32_t (&s)[32], const uint32_t (&t)[32], uint32_t mk, bool full,
-                                             float scale2, LF L, DF Dv, uint32_t (&p)[16], uint32_t (&ds)[16]) {
-#pragma unroll
-    for (int q = 0; q < 32; q += 2) {
-        float v0 = fmaf(__uint_as_float(s[q]), scale2, -L(q)), v1 = fmaf(__uint_as_float(s[q + 1]), scale2, -L(q + 1));
-        if (!full) {
-            v0 = (mk >> q) & 1u ? v0 : -INFINITY;
-            v1 = (mk >> (q + 1)) & 1u ? v1 : -INFINITY;
-        }
-        v0 = exp2_ftz(v0);
-        v1 = exp2_ftz(v1);
-        float d0 = v0 * (__uint_as_float(t[q]) - Dv(q)), d1 = v1 * (__uint_as_float(t[q + 1]) - Dv(q + 1));
-        if (!full) {  // t may be anything there
-            d0 = (mk >> q) & 1u ? d0 : 0.f;
-            d1 = (mk >> (q + 1)) & 1u ? d1 : 0.f;
-        }
-        p[q / 2] = pack_bf16(v0, v1);
-        ds[q / 2] = pack_bf16(d0, d1);
-    }
-}
-
-// ---------------------------------------------------------------------------- dQ
-
-namespace dq {
-constexpr int kM = 128, kKeys = 64, kStages = 3;
 enum {
-    kBarXfull = 0,   // + tile: Q, dO
-    kBarXfree = 2,   // + tile
-    kBarKfull = 4,   // + stage: K and V
-    kBarKfree = 7,   // + stage (both tiles)
-    kBarST = 10,     // + tile: S, T written
-    kBarP = 12,      // + tile: dS written (4 warps)
-    kBarPV = 14,     // + tile: dS K completed
-    kBarOfree = 16,  // + tile: dQ read (4 warps)
-    kBarDrain = 18,  // + tile
+    kBarXfull = 0,   // + buffer
+    kBarXfree = 2,   // + buffer: its last S, T completed
+    kBarYfull = 4,   // + stage: rows (bytes); dK, dV: lse and D (32 arrivals)
+    kBarYfree = 7,   // + stage: the sums that read it completed
+    kBarST = 10,     // + step parity: S, T written
+    kBarSTfree = 12, // S, T read (8 warps)
+    kBarP = 13,      // + step parity: P, dS written (8 warps)
+    kBarSum = 15,    // + step parity: the sums that read them, and every one before, completed
+    kBarOfree = 17,  // an item's sums read (8 warps)
+    kBarDrain = 18,  // + MMA warp
     kNumBars = 20
 };
-template <int D>
-struct Smem {
-    static constexpr int kX = kM * D * 2, kY = kKeys * D * 2;
-    static constexpr int kQ = 0, kDO = 2 * kX, kK = 4 * kX, kV = kK + kStages * kY;
-    static constexpr int kBars = kV + kStages * kY, kMisc = kBars + 8 * kNumBars;
-    static constexpr int kBytes = kMisc + 16 + 1024;  // + alignment slack
-};
-struct Args {
-    SinkBwdArgs a;
-    int P, qt, nqb, items, sink_box;
-};
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) sink_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
-                                                                 const __grid_constant__ CUtensorMap tmDO,
-                                                                 const __grid_constant__ CUtensorMap tmK,
-                                                                 const __grid_constant__ CUtensorMap tmV,
-                                                                 const __grid_constant__ CUtensorMap tmKs,
-                                                                 const __grid_constant__ CUtensorMap tmVs, Args f) {
-    extern __shared__ uint8_t smem_raw[];
-    using L = Smem<D>;
-    constexpr int kBlocks = D / 64, kXBlk = kM * 128, kYBlk = kKeys * 128;
-    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    const SinkBwdArgs &a = f.a;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t sbase = smem_u32(smem);
-    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + L::kMisc);
-    const Pipe pipe{sbase + L::kBars, misc + 1, a.status, a.wait_ns};
-    const int G = gridDim.x, cta = blockIdx.x;
-    auto item = [&](int j) { return RowItem<kKeys>(j, a.B, a.H, a.G, f.P, f.qt, f.nqb, a.Lq, a.N, a.W, a.A, 1); };
-
-    if (tid == 0) {
-        for (int i = 0; i < kNumBars; ++i) {
-            uint32_t cnt = 1;
-            if (i >= kBarKfree && i < kBarKfree + kStages) cnt = 2;
-            if ((i >= kBarP && i < kBarP + 2) || (i >= kBarOfree && i < kBarOfree + 2)) cnt = 4;
-            mbar_init(pipe.bar(i), cnt);
-        }
-        misc[1] = 0u;
-        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-    }
-    if (warp == kMmaWarp) tmem_alloc(sbase + L::kMisc, kTmemCols);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = misc[0];
-
-    if (warp == kLoadWarp) {
-        if (lane == 0) {
-            int nx[2] = {0, 0}, g = 0;
-            bool ok = true;
-            for (int r = 0; ok; ++r) {
-                const int j = item_of_round(r, cta, G);
-                if (j >= f.items) break;
-                const RowItem<kKeys> it = item(j);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (it.last(x) < 0) continue;
-                    if (nx[x] > 0 && !(ok = pipe.wait(kBarXfree + x, (nx[x] - 1) & 1))) break;
-                    mbar_expect_tx(pipe.bar(kBarXfull + x), 2 * L::kX);
-                    ++nx[x];
-#pragma unroll
-                    for (int c = 0; c < kBlocks; ++c) {
-                        const uint32_t o = sbase + x * L::kX + c * kXBlk;
-                        tma_load_4d(o + L::kQ, &tmQ, pipe.bar(kBarXfull + x), c * 64, it.i0 + x * f.qt, it.h, it.b);
-                        tma_load_4d(o + L::kDO, &tmDO, pipe.bar(kBarXfull + x), c * 64, it.i0 + x * f.qt, it.h, it.b);
-                    }
-                }
-                for (int e = it.e0; e < it.e1 && ok; ++e, ++g) {
-                    const int s = g % kStages, k0 = it.first_key(e);
-                    if (g >= kStages && !(ok = pipe.wait(kBarKfree + s, (g / kStages - 1) & 1))) break;
-                    const bool sink = e < it.sp.ns;
-                    mbar_expect_tx(pipe.bar(kBarKfull + s), 2u * (sink ? f.sink_box : kKeys) * D * 2);
-#pragma unroll
-                    for (int c = 0; c < kBlocks; ++c) {
-                        const uint32_t o = sbase + s * L::kY + c * kYBlk;
-                        tma_load_4d(o + L::kK, sink ? &tmKs : &tmK, pipe.bar(kBarKfull + s), c * 64, k0, it.hk, it.b);
-                        tma_load_4d(o + L::kV, sink ? &tmVs : &tmV, pipe.bar(kBarKfull + s), c * 64, k0, it.hk, it.b);
-                    }
-                }
-            }
-            for (int x = 0; x < 2; ++x) pipe.drain(kBarXfull + x, nx[x]);
-            for (int s = 0; s < kStages; ++s) pipe.drain(kBarKfull + s, g > s ? (g - s + kStages - 1) / kStages : 0);
-        }
-        __syncwarp();
-    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-        const int x = warp - kMmaWarp;
-        if (lane == 0) {
-            int g = 0, c = 0, n = 0;
-            bool ok = true;
-            const uint32_t q = sbase + L::kQ + x * L::kX, go = sbase + L::kDO + x * L::kX;
-            for (int r = 0; ok; ++r) {
-                const int j = item_of_round(r, cta, G);
-                if (j >= f.items) break;
-                const RowItem<kKeys> it = item(j);
-                const int last = it.last(x);
-                if (last >= 0 && !(ok = pipe.wait(kBarXfull + x, n & 1))) break;
-                tc_fence_after();
-                bool first = true;
-                for (int e = it.e0; e < it.e1; ++e, ++g) {
-                    const int nk = it.keys(x, e), s = g % kStages;
-                    if (!(ok = pipe.wait(kBarKfull + s, (g / kStages) & 1))) break;
-                    if (nk <= 0) {
-                        pipe.arrive(kBarKfree + s);
-                        continue;
-                    }
-                    if (c > 0 && !(ok = pipe.wait(kBarPV + x, (c - 1) & 1))) break;
-                    tc_fence_after();
-                    const int n16 = (nk + 15) & ~15;
-                    const uint32_t kb = sbase + L::kK + s * L::kY, vb = sbase + L::kV + s * L::kY;
-                    const uint32_t id = idesc_bf16(kM, n16, false);
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t xo = (k >> 2) * kXBlk + (k & 3) * 32, yo = (k >> 2) * kYBlk + (k & 3) * 32;
-                        mma_ss(tmem + x * 64, smem_desc(q + xo, 16, 1024), smem_desc(kb + yo, 16, 1024), id, k > 0);
-                    }
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t xo = (k >> 2) * kXBlk + (k & 3) * 32, yo = (k >> 2) * kYBlk + (k & 3) * 32;
-                        mma_ss(tmem + 128 + x * 64, smem_desc(go + xo, 16, 1024), smem_desc(vb + yo, 16, 1024), id, k > 0);
-                    }
-                    mma_commit(pipe.bar(kBarST + x));
-                    if (e == last) mma_commit(pipe.bar(kBarXfree + x));
-                    if (!(ok = pipe.wait(kBarP + x, c & 1))) break;
-                    if (first && n > 0 && !(ok = pipe.wait(kBarOfree + x, (n - 1) & 1))) break;
-                    tc_fence_after();
-                    for (int k = 0; k < n16 / 16; ++k)
-                        mma_ts(tmem + 256 + x * 128, tmem + x * 64 + k * 8, smem_desc(kb + k * 2048, kYBlk, 1024),
-                               idesc_bf16(kM, D, true), !first || k > 0);
-                    mma_commit(pipe.bar(kBarKfree + s));
-                    mma_commit(pipe.bar(kBarPV + x));
-                    first = false;
-                    ++c;
-                }
-                if (last >= 0) ++n;
-            }
-            mma_commit(pipe.bar(kBarDrain + x));
-            pipe.drain(kBarDrain + x, 1);
-        }
-        __syncwarp();
-    } else if (warp < 8) {
-        const int x = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const uint32_t s_col = tmem + lanes + x * 64, t_col = s_col + 128, o_col = tmem + lanes + 256 + x * 128;
-        const float scale2 = a.scale * kLog2e;
-        bool ok = true;
-        int c = 0;
-        for (int r = 0; ok; ++r) {
-            const int j = item_of_round(r, cta, G);
-            if (j >= f.items) break;
-            const RowItem<kKeys> it = item(j);
-            const int h = it.h + row / f.qt, i = it.i0 + x * f.qt + row % f.qt, t = a.N - a.Lq + i;
-            const bool have = i < a.Lq;
-            const int64_t place = ((int64_t)it.b * a.H + h) * a.Lq + i;
-            const float Lr = have ? log2_lse(__ldg(a.lse + place)) : INFINITY;
-            const float Dr = have ? __ldg(a.Dv + place) : 0.f;
-            bool any_tile = false;
-            for (int e = it.e0; e < it.e1; ++e) {
-                const int n = it.keys(x, e);
-                if (n <= 0) continue;
-                any_tile = true;
-                int lo, hi, as;
-                it.columns(e, n, t, a.W, &lo, &hi, &as);
-                if (!have) hi = as = 0;
-                const bool full = __all_sync(kFull, lo <= 0 && hi == kKeys);
-                if (!(ok = pipe.wait_warp(kBarST + x, c & 1))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int ch = 0; ch < 2; ++ch) {
-                    if (ch * 32 >= n) continue;
-                    const uint32_t mk = full ? kFull : range_bits(lo, hi, ch * 32) | range_bits(0, as, ch * 32);
-                    uint32_t ds[16];
-                    if (__any_sync(kFull, mk != 0)) {
-                        uint32_t s[32], u[32], p[16];
-                        tmem_ld32(s_col + ch * 32, s);
-                        tmem_ld32(t_col + ch * 32, u);
-                        tmem_wait_ld();
-                        grad_columns(s, u, mk, full, scale2, [&](int) { return Lr; }, [&](int) { return Dr; }, p, ds);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) ds[q] = 0u;
-                    }
-                    tmem_st16(s_col + ch * 16, ds);  // columns whose S has been read
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                pipe.arrive_if(lane == 0, kBarP + x);
-                ++c;
-            }
-            if (!ok) break;
-            if (any_tile) {
-                if (!(ok = pipe.wait_warp(kBarPV + x, (c - 1) & 1))) break;
-                tc_fence_after();
-            }
-            bf16 *orow = static_cast<bf16 *>(a.dQ.ptr) + it.b * a.dQ.sb + h * a.dQ.sh + (int64_t)i * a.dQ.st;
-#pragma unroll
-            for (int part = 0; part < D / 32; ++part) {
-                uint32_t o[32];
-                if (any_tile) {
-                    tmem_ld32(o_col + part * 32, o);
-                    tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 32; ++q) o[q] = 0u;
-                }
-                if (!have) continue;
-                uint4 *dst = reinterpret_cast<uint4 *>(orow + part * 32);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        w[k] = pack_bf16(__uint_as_float(o[8 * q + 2 * k]) * a.scale, __uint_as_float(o[8 * q + 2 * k + 1]) * a.scale);
-                    dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            }
-            if (any_tile) {
-                tc_fence_before();
-                __syncwarp();
-                pipe.arrive_if(lane == 0, kBarOfree + x);
-            }
-        }
-    }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == kMmaWarp) {
-        tc_fence_after();
-        tmem_free(tmem, kTmemCols);
-    }
-}
-}  // namespace dq
-
-// ---------------------------------------------------------------------------- dK, dV
-
-namespace dkv {
-constexpr int kM = kSinkKeys, kRows = 64, kStages = 3;
-enum {
-    kBarXfull = 0,    // + buffer: K, V of an item
-    kBarXfree = 2,    // + buffer: its last S, T completed
-    kBarYfull = 4,    // + stage: Q, dO (bytes), lse and D (32 arrivals)
-    kBarYfree = 7,    // + stage: the products that read it completed
-    kBarST = 10,      // + buffer: S^T, T^T written
-    kBarP = 12,       // + buffer: P^T, dS^T written (4 warps)
-    kBarPV = 14,      // + buffer: the products that read them completed
-    kBarDone = 16,    // dK, dV of an item final
-    kBarOfree = 17,   // dK, dV read (8 warps)
-    kBarDrain = 18,
-    kNumBars = 19
-};
 template <int D>
 struct Smem {
     static constexpr int kX = kM * D * 2, kY = kRows * D * 2;
-    static constexpr int kK = 0, kV = 2 * kX, kQ = 4 * kX, kDO = kQ + kStages * kY;
-    static constexpr int kSc = kDO + kStages * kY;  // per stage: lse (log2 units) [64], D [64]
+    static constexpr int kX1 = 0, kX2 = 2 * kX, kY1 = 4 * kX, kY2 = kY1 + kStages * kY;
+    static constexpr int kSc = kY2 + kStages * kY;  // per stage: -lse (log2 units) [64], -D [64]
     static constexpr int kBars = kSc + kStages * kRows * 8, kMisc = kBars + 8 * kNumBars;
-    static constexpr int kBytes = kMisc + 24 + 1024;  // + alignment slack
+    static constexpr int kBytes = kMisc + 16;
 };
+
 struct Args {
     SinkBwdArgs a;
-    int items;  // of one (b, key-value head)
+    int P, qt, tiles, sink_box;  // dQ: packed heads, queries of a tile, tiles of (b, packed heads)
+    int items;                   // dK, dV: items of one (b, key-value head)
+    int total;
 };
+
 struct Item {
-    int xb, b, hk, j0, i0, i1, tiles, s0, s1, nseg, index;
+    int b, h, hk;     // batch, first head (dQ), key-value head
+    int row0;         // first query of the tile (dQ), first key of the block
+    int steps;
+    SinkSpan sp;      // dQ: the keys
+    int i0, i1, tiles, s0, nseg, index;  // dK, dV: queries, their tiles, first step, segment
 };
+
+template <bool DQ>
 __device__ __forceinline__ Item decode(const Args &f, int j) {
     const SinkBwdArgs &a = f.a;
-    const int Hk = a.H / a.G, heads = a.B * Hk;
     Item it;
-    it.xb = j % heads;  // the blocks with most steps (the first ones of a causal range) come first
-    const int x = j / heads;
-    it.b = it.xb / Hk;
-    it.hk = it.xb % Hk;
-    const SinkItem k = sink_item(a, x);
-    it.j0 = k.blk * kM;
-    it.nseg = k.nseg;
-    it.index = it.xb * f.items + x;
-    sink_rows_of_block(a, it.j0, min(kM, a.N - it.j0), &it.i0, &it.i1);
-    it.tiles = (it.i1 - it.i0 + kRows - 1) / kRows;
-    const int64_t steps = (int64_t)a.G * it.tiles;
-    it.s0 = (int)(steps * k.seg / k.nseg);
-    it.s1 = (int)(steps * (k.seg + 1) / k.nseg);
+    if (DQ) {
+        const int hp = a.H / f.P, units = a.B * hp, q = j / units, u = j - q * units;
+        it.b = u / hp;
+        it.h = (u - it.b * hp) * f.P;
+        it.hk = it.h / a.G;
+        it.row0 = (f.tiles - 1 - q) * f.qt;  // latest queries (most keys) first
+        const int t0 = a.N - a.Lq + it.row0;
+        it.sp = sink_span(t0, min(a.N - 1, t0 + f.qt - 1), a.W, a.A, kRows);
+        it.steps = it.sp.ns + it.sp.nw;
+        it.i0 = it.i1 = it.tiles = it.s0 = it.index = 0;
+        it.nseg = 1;
+    } else {
+        const int Hk = a.H / a.G, heads = a.B * Hk;
+        const int x = j / heads, xb = j - x * heads;  // the blocks with most steps come first
+        it.b = xb / Hk;
+        it.hk = xb - it.b * Hk;
+        it.h = it.hk * a.G;
+        const SinkItem k = sink_item(a, x);
+        it.row0 = k.blk * kM;
+        it.nseg = k.nseg;
+        it.index = xb * f.items + x;
+        sink_rows_of_block(a, it.row0, min(kM, a.N - it.row0), &it.i0, &it.i1);
+        it.tiles = (it.i1 - it.i0 + kRows - 1) / kRows;
+        const int steps = a.G * it.tiles;
+        it.s0 = 0;
+        it.steps = steps;
+        if (k.nseg > 1) {
+            it.s0 = (int)((int64_t)steps * k.seg / k.nseg);
+            it.steps = (int)((int64_t)steps * (k.seg + 1) / k.nseg) - it.s0;
+        }
+        it.sp = SinkSpan{};
+    }
     return it;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) sink_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
-                                                                  const __grid_constant__ CUtensorMap tmDO,
-                                                                  const __grid_constant__ CUtensorMap tmK,
-                                                                  const __grid_constant__ CUtensorMap tmV, Args f,
-                                                                  int total) {
-    extern __shared__ uint8_t smem_raw[];
+// A walk over an item's steps: their stage and its phase (kept over the items), and
+// (dK, dV) the step's query tile and head.
+struct Walk {
+    int st = 0;
+    uint32_t ph = 0;
+    int tile = 0, h = 0;
+    __device__ __forceinline__ void start(const Item &it) {
+        h = it.s0 > 0 ? it.s0 / it.tiles : 0;
+        tile = it.s0 - h * it.tiles;
+    }
+    __device__ __forceinline__ void next(const Item &it) {
+        if (++st == kStages) {
+            st = 0;
+            ph ^= 1u;
+        }
+        if (++tile == it.tiles) {
+            tile = 0;
+            ++h;
+        }
+    }
+};
+// dQ: first key of step i, and its keys
+__device__ __forceinline__ int step_key(const Item &it, int i) { return i < it.sp.ns ? i * kRows : it.sp.lo + (i - it.sp.ns) * kRows; }
+__device__ __forceinline__ int step_keys(const Item &it, int i) {
+    return min(kRows, (i < it.sp.ns ? it.sp.sinks : it.sp.hi) - step_key(it, i));
+}
+
+template <int D, bool DQ>
+__global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmX1,
+                                                                  const __grid_constant__ CUtensorMap tmX2,
+                                                                  const __grid_constant__ CUtensorMap tmY1,
+                                                                  const __grid_constant__ CUtensorMap tmY2,
+                                                                  const __grid_constant__ CUtensorMap tmS1,
+                                                                  const __grid_constant__ CUtensorMap tmS2, Args f) {
+    extern __shared__ __align__(1024) uint8_t smem[];
     using L = Smem<D>;
     constexpr int kBlocks = D / 64, kXBlk = kM * 128, kYBlk = kRows * 128;
-    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const SinkBwdArgs &a = f.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = smem_u32(smem);
@@ -370,238 +154,369 @@ __global__ void __launch_bounds__(kThreads, 1) sink_dkv_tc_kernel(const __grid_c
     float *scal = reinterpret_cast<float *>(smem + L::kSc);
     const Pipe pipe{sbase + L::kBars, misc + 1, a.status, a.wait_ns};
     const int G = gridDim.x, cta = blockIdx.x;
-
+    if (sbase & 1023u) {  // an alignment that the launch has to give
+        if (tid == 0) atomicOr(a.status, 1u);
+        return;
+    }
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i) {
             uint32_t cnt = 1;
-            if (i >= kBarYfull && i < kBarYfull + kStages) cnt = 33;
-            if (i >= kBarP && i < kBarP + 2) cnt = 4;
-            if (i == kBarOfree) cnt = 8;
+            if (!DQ && i >= kBarYfull && i < kBarYfull + kStages) cnt = 33;
+            if (i == kBarSTfree || i == kBarP || i == kBarP + 1 || i == kBarOfree) cnt = 8;
             mbar_init(pipe.bar(i), cnt);
         }
         misc[1] = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
-    if (warp == kMmaWarp) tmem_alloc(sbase + L::kMisc, kTmemCols);
+    if (warp == kStWarp) tmem_alloc(sbase + L::kMisc, kTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc[0];
 
     if (warp == kLoadWarp) {
+        // ---------------------------------------------------------------- TMA
         int n = 0, g = 0;  // items with steps, steps
         bool ok = true;
+        Walk w;
         for (int r = 0; ok; ++r) {
             const int j = item_of_round(r, cta, G);
-            if (j >= total) break;
-            const Item it = decode(f, j);
-            if (it.s0 >= it.s1) continue;
+            if (j >= f.total) break;
+            const Item it = decode<DQ>(f, j);
+            if (it.steps <= 0) continue;
             const int xb = n & 1;
             if (n >= 2 && !(ok = pipe.wait_warp(kBarXfree + xb, ((n >> 1) - 1) & 1))) break;
-            if (lane == 0) {
+            if (elect_one()) {
                 mbar_expect_tx(pipe.bar(kBarXfull + xb), 2 * L::kX);
 #pragma unroll
                 for (int c = 0; c < kBlocks; ++c) {
                     const uint32_t o = sbase + xb * L::kX + c * kXBlk;
-                    tma_load_4d(o + L::kK, &tmK, pipe.bar(kBarXfull + xb), c * 64, it.j0, it.hk, it.b);
-                    tma_load_4d(o + L::kV, &tmV, pipe.bar(kBarXfull + xb), c * 64, it.j0, it.hk, it.b);
+                    tma_load_4d(o + L::kX1, &tmX1, pipe.bar(kBarXfull + xb), c * 64, it.row0, DQ ? it.h : it.hk, it.b);
+                    tma_load_4d(o + L::kX2, &tmX2, pipe.bar(kBarXfull + xb), c * 64, it.row0, DQ ? it.h : it.hk, it.b);
                 }
             }
+            __syncwarp();
             ++n;
-            float sc[4];  // lse and D of rows lane, lane + 32 of the next step
-            auto scalars = [&](int s) {
-                const int64_t row0 = ((int64_t)it.b * a.H + it.hk * a.G + s / it.tiles) * a.Lq;
-                const int q0 = it.i0 + (s % it.tiles) * kRows;
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const int i = q0 + lane + 32 * m;
-                    sc[m] = i < it.i1 ? log2_lse(__ldg(a.lse + row0 + i)) : INFINITY;
-                    sc[2 + m] = i < it.i1 ? __ldg(a.Dv + row0 + i) : 0.f;
-                }
-            };
-            scalars(it.s0);
-            for (int s = it.s0; s < it.s1; ++s, ++g) {
-                const int st = g % kStages;
-                if (g >= kStages && !(ok = pipe.wait_warp(kBarYfree + st, (g / kStages - 1) & 1))) break;
-                if (lane == 0) {
-                    mbar_expect_tx(pipe.bar(kBarYfull + st), 2 * L::kY);
-                    const int h = it.hk * a.G + s / it.tiles, q0 = it.i0 + (s % it.tiles) * kRows;
+            w.start(it);
+            for (int i = 0; i < it.steps; ++i, ++g) {
+                if (g >= kStages && !(ok = pipe.wait_warp(kBarYfree + w.st, w.ph ^ 1u))) break;
+                const bool sink = DQ && i < it.sp.ns;
+                const int y = DQ ? step_key(it, i) : it.i0 + w.tile * kRows, h = DQ ? it.hk : it.h + w.h;
+                if (elect_one()) {
+                    mbar_expect_tx(pipe.bar(kBarYfull + w.st), 2u * (sink ? f.sink_box : kRows) * D * 2);
 #pragma unroll
                     for (int c = 0; c < kBlocks; ++c) {
-                        const uint32_t o = sbase + st * L::kY + c * kYBlk;
-                        tma_load_4d(o + L::kQ, &tmQ, pipe.bar(kBarYfull + st), c * 64, q0, h, it.b);
-                        tma_load_4d(o + L::kDO, &tmDO, pipe.bar(kBarYfull + st), c * 64, q0, h, it.b);
+                        const uint32_t o = sbase + w.st * L::kY + c * kYBlk;
+                        tma_load_4d(o + L::kY1, sink ? &tmS1 : &tmY1, pipe.bar(kBarYfull + w.st), c * 64, y, h, it.b);
+                        tma_load_4d(o + L::kY2, sink ? &tmS2 : &tmY2, pipe.bar(kBarYfull + w.st), c * 64, y, h, it.b);
                     }
                 }
-                float *d = scal + st * 2 * kRows + lane;
-                d[0] = sc[0];
-                d[32] = sc[1];
-                d[64] = sc[2];
-                d[96] = sc[3];
-                pipe.arrive(kBarYfull + st);
-                if (s + 1 < it.s1) scalars(s + 1);
+                __syncwarp();
+                w.next(it);
             }
         }
-        if (lane == 0) {
+        if (lane == 0) {  // what was started lands before the CTA's memory is released
             for (int x = 0; x < 2; ++x) pipe.drain(kBarXfull + x, n > x ? (n - x + 1) / 2 : 0);
-            // on a stop, a stage's phase may lack this warp's own arrivals only if its copy was not started
             for (int s = 0; s < kStages; ++s) pipe.drain(kBarYfull + s, g > s ? (g - s + kStages - 1) / kStages : 0);
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
-        if (lane == 0) {
-            int n = 0, c = 0;  // items with steps, steps
+    } else if (warp == kScalarWarp) {
+        // ---------------------------------------------------------------- lse and D of the queries
+        if (!DQ) {
+            int g = 0;
             bool ok = true;
+            Walk w;
             for (int r = 0; ok; ++r) {
                 const int j = item_of_round(r, cta, G);
-                if (j >= total) break;
-                const Item it = decode(f, j);
-                if (it.s0 >= it.s1) continue;
-                const int xb = n & 1, steps = it.s1 - it.s0;
-                const uint32_t kb = sbase + L::kK + xb * L::kX, vb = sbase + L::kV + xb * L::kX;
-                if (!(ok = pipe.wait(kBarXfull + xb, (n >> 1) & 1))) break;
-                // step i: S^T, T^T of step i, then the sums of step i - 1
-                for (int i = 0; i <= steps && ok; ++i) {
-                    if (i < steps) {
-                        const int cc = c + i, st = cc % kStages, p = cc & 1;
-                        if (!(ok = pipe.wait(kBarYfull + st, (cc / kStages) & 1))) break;
-                        if (cc >= 2 && !(ok = pipe.wait(kBarPV + p, ((cc >> 1) - 1) & 1))) break;
-                        tc_fence_after();
-                        const uint32_t qb = sbase + L::kQ + st * L::kY, gb = sbase + L::kDO + st * L::kY;
-                        const uint32_t id = idesc_bf16(kM, kRows, false);
+                if (j >= f.total) break;
+                const Item it = decode<DQ>(f, j);
+                if (it.steps <= 0) continue;
+                w.start(it);
+                int tile = w.tile, h = w.h, next = 0;
+                float sc[2][4];
+                auto fetch = [&](float(&d)[4]) {
+                    if (next >= it.steps) return;
+                    ++next;
+                    const int64_t row0 = ((int64_t)it.b * a.H + it.h + h) * a.Lq;
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t xo = (k >> 2) * kXBlk + (k & 3) * 32, yo = (k >> 2) * kYBlk + (k & 3) * 32;
-                            mma_ss(tmem + p * 64, smem_desc(kb + xo, 16, 1024), smem_desc(qb + yo, 16, 1024), id, k > 0);
-                        }
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t xo = (k >> 2) * kXBlk + (k & 3) * 32, yo = (k >> 2) * kYBlk + (k & 3) * 32;
-                            mma_ss(tmem + 128 + p * 64, smem_desc(vb + xo, 16, 1024), smem_desc(gb + yo, 16, 1024), id, k > 0);
-                        }
-                        mma_commit(pipe.bar(kBarST + p));
-                        if (i + 1 == steps) mma_commit(pipe.bar(kBarXfree + xb));
+                    for (int m = 0; m < 2; ++m) {
+                        const int i = it.i0 + tile * kRows + lane + 32 * m;
+                        d[m] = i < it.i1 ? __ldg(a.lse + row0 + i) : -INFINITY;
+                        d[2 + m] = i < it.i1 ? __ldg(a.Dv + row0 + i) : 0.f;
                     }
-                    if (i > 0) {
-                        const int cc = c + i - 1, st = cc % kStages, p = cc & 1;
-                        if (!(ok = pipe.wait(kBarP + p, (cc >> 1) & 1))) break;
-                        if (i == 1 && n > 0 && !(ok = pipe.wait(kBarOfree, (n - 1) & 1))) break;
-                        tc_fence_after();
-                        const uint32_t qb = sbase + L::kQ + st * L::kY, gb = sbase + L::kDO + st * L::kY;
-                        const uint32_t id = idesc_bf16(kM, D, true);
-#pragma unroll
-                        for (int k = 0; k < kRows / 16; ++k)
-                            mma_ts(tmem + 256, tmem + p * 64 + k * 8, smem_desc(gb + k * 2048, kYBlk, 1024), id, i > 1 || k > 0);
-#pragma unroll
-                        for (int k = 0; k < kRows / 16; ++k)
-                            mma_ts(tmem + 384, tmem + 128 + p * 64 + k * 8, smem_desc(qb + k * 2048, kYBlk, 1024), id,
-                                   i > 1 || k > 0);
-                        mma_commit(pipe.bar(kBarPV + p));
-                        mma_commit(pipe.bar(kBarYfree + st));
-                        if (i == steps) mma_commit(pipe.bar(kBarDone));
+                    if (++tile == it.tiles) {
+                        tile = 0;
+                        ++h;
                     }
+                };
+                auto put = [&](float(&d)[4]) {
+                    if (g >= kStages && !(ok = pipe.wait_warp(kBarYfree + w.st, w.ph ^ 1u))) return;
+                    float *to = scal + w.st * 2 * kRows + lane;
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {  // a query that sees nothing: exp2(s - inf) = 0
+                        to[32 * m] = d[m] == -INFINITY ? d[m] : -d[m] * kLog2e;
+                        to[64 + 32 * m] = -d[2 + m];
+                    }
+                    pipe.arrive(kBarYfull + w.st);
+                    ++g;
+                    w.next(it);
+                    fetch(d);
+                };
+                fetch(sc[0]);
+                fetch(sc[1]);
+                for (int i = 0; i < it.steps && ok; i += 2) {
+                    put(sc[0]);
+                    if (ok && i + 1 < it.steps) put(sc[1]);
                 }
-                c += steps;
-                ++n;
             }
-            mma_commit(pipe.bar(kBarDrain));
+        }
+        __syncwarp();
+    } else if (warp == kStWarp) {
+        // ---------------------------------------------------------------- S and T
+        int n = 0, c = 0;
+        bool ok = true;
+        Walk w;
+        const uint64_t x1 = tile_desc(sbase + L::kX1, 16), x2 = tile_desc(sbase + L::kX2, 16);
+        const uint64_t y1 = tile_desc(sbase + L::kY1, 16), y2 = tile_desc(sbase + L::kY2, 16);
+        for (int r = 0; ok; ++r) {
+            const int j = item_of_round(r, cta, G);
+            if (j >= f.total) break;
+            const Item it = decode<DQ>(f, j);
+            if (it.steps <= 0) continue;
+            const uint64_t xo = (n & 1) * (L::kX / 16);
+            if (!(ok = pipe.wait_warp(kBarXfull + (n & 1), (n >> 1) & 1))) break;
+            for (int i = 0; i < it.steps; ++i, ++c) {
+                const uint64_t yo = w.st * (L::kY / 16);
+                const uint32_t id = idesc_bf16(kM, DQ ? (step_keys(it, i) + 15) & ~15 : kRows, false);
+                if (!(ok = pipe.wait_warp(kBarYfull + w.st, w.ph))) break;
+                if (c > 0 && !(ok = pipe.wait_warp(kBarSTfree, (c - 1) & 1))) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_ss(tmem, x1 + xo + ((k >> 2) * kXBlk + (k & 3) * 32) / 16, y1 + yo + ((k >> 2) * kYBlk + (k & 3) * 32) / 16,
+                               id, k > 0);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_ss(tmem + 64, x2 + xo + ((k >> 2) * kXBlk + (k & 3) * 32) / 16,
+                               y2 + yo + ((k >> 2) * kYBlk + (k & 3) * 32) / 16, id, k > 0);
+                    mma_commit(pipe.bar(kBarST + (c & 1)));
+                    if (i + 1 == it.steps) mma_commit(pipe.bar(kBarXfree + (n & 1)));
+                }
+                __syncwarp();
+                w.next(it);
+            }
+            ++n;
+        }
+        if (elect_one()) {
+            mma_commit(pipe.bar(kBarDrain));  // what was issued completes before TMEM is released
             pipe.drain(kBarDrain, 1);
         }
         __syncwarp();
-    } else if (warp < 8) {
-        const int w = warp >> 2, quad = warp & 3, row = quad * 32 + lane;  // w: steps of its parity; then dV or dK
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const uint32_t s_col = tmem + lanes + w * 64, t_col = s_col + 128, o_col = tmem + lanes + 256 + w * 128;
-        const float scale2 = a.scale * kLog2e;
-        const int off = a.N - a.Lq;
+    } else if (warp == kSumWarp) {
+        // ---------------------------------------------------------------- the sums
+        int n = 0, c = 0;
         bool ok = true;
-        int c = 0, n = 0;
+        Walk w;
+        const uint64_t y1 = tile_desc(sbase + L::kY1, kYBlk), y2 = tile_desc(sbase + L::kY2, kYBlk);
+        const uint32_t id = idesc_bf16(kM, D, true);
         for (int r = 0; ok; ++r) {
             const int j = item_of_round(r, cta, G);
-            if (j >= total) break;
-            const Item it = decode(f, j);
-            const int key = it.j0 + row;
-            const int steps = max(0, it.s1 - it.s0);
-            for (int i = 0; i < steps; ++i) {
-                const int cc = c + i;
-                if ((cc & 1) != w) continue;
-                const int st = cc % kStages, q0 = it.i0 + ((it.s0 + i) % it.tiles) * kRows;
-                // columns (queries) that see this key
-                const int lo = key - off - q0, end = min(kRows, it.i1 - q0);
-                const int hi = key < a.A ? end : min(end, (int)min((int64_t)key + a.W - off - q0, (int64_t)kRows));
-                const bool full = __all_sync(kFull, lo <= 0 && hi == kRows);
-                if (!(ok = pipe.wait_warp(kBarYfull + st, (cc / kStages) & 1))) break;
-                if (!(ok = pipe.wait_warp(kBarST + w, (cc >> 1) & 1))) break;
+            if (j >= f.total) break;
+            const Item it = decode<DQ>(f, j);
+            if (it.steps <= 0) continue;
+            for (int i = 0; i < it.steps; ++i, ++c) {
+                const uint64_t yo = w.st * (L::kY / 16);
+                const int k16 = DQ ? (step_keys(it, i) + 15) / 16 : kRows / 16;
+                const uint32_t p = tmem + 128 + (c & 1) * 32, ds = tmem + 192 + (c & 1) * 32;
+                if (!(ok = pipe.wait_warp(kBarP + (c & 1), (c >> 1) & 1))) break;
+                if (!(ok = pipe.wait_warp(kBarYfull + w.st, w.ph))) break;  // (P came of it)
+                if (i == 0 && n > 0 && !(ok = pipe.wait_warp(kBarOfree, (n - 1) & 1))) break;
                 tc_fence_after();
-                const float *sc = scal + st * 2 * kRows;
+                if (elect_one()) {
+                    if (DQ) {
 #pragma unroll
-                for (int ch = 0; ch < 2; ++ch) {
-                    const uint32_t mk = full ? kFull : range_bits(lo, hi, ch * 32);
-                    uint32_t p[16], ds[16];
-                    if (__any_sync(kFull, mk != 0)) {
-                        uint32_t s[32], u[32];
-                        float Lc[32], Dc[32];
-                        tmem_ld32(s_col + ch * 32, s);
-                        tmem_ld32(t_col + ch * 32, u);
-#pragma unroll
-                        for (int q = 0; q < 32; q += 4) {
-                            *reinterpret_cast<float4 *>(&Lc[q]) = *reinterpret_cast<const float4 *>(sc + ch * 32 + q);
-                            *reinterpret_cast<float4 *>(&Dc[q]) = *reinterpret_cast<const float4 *>(sc + kRows + ch * 32 + q);
-                        }
-                        tmem_wait_ld();
-                        grad_columns(s, u, mk, full, scale2, [&](int q) { return Lc[q]; }, [&](int q) { return Dc[q]; }, p, ds);
+                        for (int k = 0; k < kRows / 16; ++k)
+                            if (k < k16) mma_ts(tmem + 256, ds + k * 8, y1 + yo + k * (2048 / 16), id, i > 0 || k > 0);
                     } else {
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) p[q] = ds[q] = 0u;
+                        for (int k = 0; k < kRows / 16; ++k) mma_ts(tmem + 256, p + k * 8, y2 + yo + k * (2048 / 16), id, i > 0 || k > 0);
+#pragma unroll
+                        for (int k = 0; k < kRows / 16; ++k) mma_ts(tmem + 384, ds + k * 8, y1 + yo + k * (2048 / 16), id, i > 0 || k > 0);
                     }
-                    tmem_st16(s_col + ch * 16, p);  // columns whose S, T have been read
-                    tmem_st16(t_col + ch * 16, ds);
+                    mma_commit(pipe.bar(kBarSum + (c & 1)));
+                    mma_commit(pipe.bar(kBarYfree + w.st));
                 }
+                __syncwarp();
+                w.next(it);
+            }
+            ++n;
+        }
+        if (elect_one()) {
+            mma_commit(pipe.bar(kBarDrain + 1));
+            pipe.drain(kBarDrain + 1, 1);
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------------- rows of X
+        const int w = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t s_col = lanes + half * 32, t_col = s_col + 64;
+        const uint32_t p_col = lanes + 128 + w * 32 + half * 16, d_col = p_col + 64;
+        const float scale2 = a.scale * kLog2e, lowest = scale2 > 0.f ? -INFINITY : INFINITY;  // its logit is -inf
+        const float2 scale22 = make_float2(scale2, scale2);
+        const int off = a.N - a.Lq;
+        bool ok = true;
+        int c = 0;
+        Walk walk;
+        for (int r = 0; ok; ++r) {
+            const int j = item_of_round(r, cta, G);
+            if (j >= f.total) break;
+            const Item it = decode<DQ>(f, j);
+            // dQ: this row's query; dK, dV: its key
+            const int hrow = DQ ? row / f.qt : 0, i_q = it.row0 + (DQ ? row - hrow * f.qt : 0), t = off + i_q, key = it.row0 + row;
+            const bool have = DQ ? i_q < a.Lq : key < a.N;
+            float2 nl = make_float2(0.f, 0.f), nd = nl;
+            int see0 = 0, see1 = 0;  // dK, dV: the queries that see the key, from the item's first on
+            if (DQ) {
+                const int64_t place = ((int64_t)it.b * a.H + it.h + hrow) * a.Lq + i_q;
+                const float lse = have ? __ldg(a.lse + place) : -INFINITY, Dr = have ? __ldg(a.Dv + place) : 0.f;
+                nl.x = nl.y = lse == -INFINITY ? lse : -lse * kLog2e;
+                nd.x = nd.y = -Dr;
+            } else {
+                see0 = key - off - it.i0;
+                see1 = (int)min(key < a.A ? (int64_t)it.i1 : (int64_t)key + a.W - off, (int64_t)it.i1) - it.i0;
+            }
+            walk.start(it);
+            for (int i = 0; i < it.steps; ++i, walk.next(it)) {
+                const int cc = c + i;
+                if ((cc & 1) != w) continue;
+                uint32_t mk;  // visible columns of this half
+                if (DQ) {
+                    const int k0 = step_key(it, i) + half * 32, n = step_keys(it, i) - half * 32;
+                    int hi = min(n, t + 1 - k0);
+                    hi = have ? hi : 0;
+                    mk = i < it.sp.ns ? range_bits(0, hi, 0) : range_bits(t - a.W + 1 - k0, hi, 0) | range_bits(0, min(a.A - k0, hi), 0);
+                } else {
+                    const int q = walk.tile * kRows + half * 32;
+                    mk = range_bits(see0 - q, see1 - q, 0);
+                }
+                const bool full = __all_sync(kFull, mk == kFull);
+                if (!(ok = pipe.wait_warp(kBarST + w, (cc >> 1) & 1))) break;
+                tc_fence_after();
+                uint32_t s[32], u[32];
+                tmem_ld32(s_col, s);
+                tmem_ld32(t_col, u);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                pipe.arrive_if(lane == 0, kBarSTfree);
+                if (!full) {
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) {
+                        s[q] = (mk >> q) & 1u ? s[q] : __float_as_uint(lowest);
+                        u[q] = (mk >> q) & 1u ? u[q] : 0u;  // it may be anything there
+                    }
+                }
+                const float *sc = scal + walk.st * 2 * kRows + half * 32;
+                if (!DQ && !(ok = pipe.wait_warp(kBarYfull + walk.st, walk.ph))) break;  // complete: S came of it
+                uint32_t p[16], ds[16];
+#pragma unroll
+                for (int q = 0; q < 32; q += 4) {
+                    float2 l0 = nl, l1 = nl, d0 = nd, d1 = nd;
+                    if (!DQ) {
+                        const float4 x = *reinterpret_cast<const float4 *>(sc + q), y = *reinterpret_cast<const float4 *>(sc + kRows + q);
+                        l0 = make_float2(x.x, x.y);
+                        l1 = make_float2(x.z, x.w);
+                        d0 = make_float2(y.x, y.y);
+                        d1 = make_float2(y.z, y.w);
+                    }
+                    float2 e0 = fma2(as2(s + q), scale22, l0), e1 = fma2(as2(s + q + 2), scale22, l1);
+                    e0 = make_float2(exp2_ftz(e0.x), exp2_ftz(e0.y));
+                    e1 = make_float2(exp2_ftz(e1.x), exp2_ftz(e1.y));
+                    const float2 g0 = mul2(e0, add2(as2(u + q), d0)), g1 = mul2(e1, add2(as2(u + q + 2), d1));
+                    p[q / 2] = pack_bf16(e0.x, e0.y);
+                    p[q / 2 + 1] = pack_bf16(e1.x, e1.y);
+                    ds[q / 2] = pack_bf16(g0.x, g0.y);
+                    ds[q / 2 + 1] = pack_bf16(g1.x, g1.y);
+                }
+                // the sums of two steps before have read this buffer
+                if (cc >= 2 && !(ok = pipe.wait_warp(kBarSum + w, ((cc >> 1) - 1) & 1))) break;
+                tc_fence_after();
+                if (!DQ) tmem_st16(p_col, p);
+                tmem_st16(d_col, ds);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 pipe.arrive_if(lane == 0, kBarP + w);
             }
             if (!ok) break;
-            c += steps;
-            if (steps > 0) {
-                if (!(ok = pipe.wait_warp(kBarDone, n & 1))) break;
+            c += it.steps;
+            // ---- the item's sums, by the warps of its last step: dQ's halves of the columns, or dV and dK
+            if (it.steps > 0 ? ((c - 1) & 1) != w : w != 0) continue;
+            if (it.steps > 0) {
+                if (!(ok = pipe.wait_warp(kBarSum + w, ((c - 1) >> 1) & 1))) break;
                 tc_fence_after();
-                ++n;
             }
-            // ---- warps 0-3: dV, warps 4-7: dK
-            const float f_out = w ? a.scale : 1.f;
-            const MutView &v = w ? a.dK : a.dV;
-            bf16 *orow = static_cast<bf16 *>(v.ptr) + it.b * v.sb + it.hk * v.sh + (int64_t)key * v.st;
-            float *prow = it.nseg > 1 ? a.part + ((int64_t)it.index * 2 * kSinkKeys + (w ? 0 : kSinkKeys) + row) * D : nullptr;
+            const float fac = DQ || half ? a.scale : 1.f;
+            const uint32_t o_col = lanes + 256 + (DQ ? half * (D / 2) : half * 128);
+            const int cols = DQ ? D / 2 : D;
+            const bool part = !DQ && it.nseg > 1;  // float32 partial rows
+            const MutView &v = DQ ? a.dQ : half ? a.dK : a.dV;
+            uint64_t mine = 0;
+            if (part)
+                mine = (uint64_t)(a.part + ((int64_t)it.index * 2 * kSinkKeys + (half ? 0 : kSinkKeys) + row) * D);
+            else if (have)
+                mine = (uint64_t)(static_cast<bf16 *>(v.ptr) + it.b * v.sb + (DQ ? it.h + hrow : it.hk) * v.sh +
+                                  (int64_t)(DQ ? i_q : key) * v.st + (DQ ? half * (D / 2) : 0));
+            char *to[4];  // the rows of a lane's group of four, at this lane's unit
+            bool live[4];
 #pragma unroll
-            for (int part = 0; part < D / 32; ++part) {
+            for (int k = 0; k < 4; ++k) {
+                const uint64_t x = __shfl_sync(kFull, mine, (lane & ~3) + k);
+                live[k] = x != 0;
+                to[k] = reinterpret_cast<char *>(x) + (lane & 3) * 16;
+            }
+#pragma unroll 1
+            for (int col = 0; col < cols; col += 32) {
                 uint32_t o[32];
-                if (steps > 0) {
-                    tmem_ld32(o_col + part * 32, o);
+                if (it.steps > 0) {
+                    tmem_ld32(o_col + col, o);
                     tmem_wait_ld();
                 } else {
 #pragma unroll
                     for (int q = 0; q < 32; ++q) o[q] = 0u;
                 }
-                if (prow) {
 #pragma unroll
-                    for (int q = 0; q < 32; q += 4)
-                        *reinterpret_cast<float4 *>(prow + part * 32 + q) =
-                            make_float4(__uint_as_float(o[q]) * f_out, __uint_as_float(o[q + 1]) * f_out,
-                                        __uint_as_float(o[q + 2]) * f_out, __uint_as_float(o[q + 3]) * f_out);
-                } else if (key < a.N) {
+                for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * fac);
+                if (part) {
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        uint4 x[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            x[q] = make_uint4(o[16 * g + 4 * q], o[16 * g + 4 * q + 1], o[16 * g + 4 * q + 2], o[16 * g + 4 * q + 3]);
+                        swap_units(x);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4 *>(to[k] + col * 4 + g * 64) = x[k];
+                    }
+                } else {
+                    uint4 x[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        uint32_t x[4];
+                        uint32_t y[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            x[k] = pack_bf16(__uint_as_float(o[8 * q + 2 * k]) * f_out, __uint_as_float(o[8 * q + 2 * k + 1]) * f_out);
-                        reinterpret_cast<uint4 *>(orow + part * 32)[q] = make_uint4(x[0], x[1], x[2], x[3]);
+                            y[k] = pack_bf16(__uint_as_float(o[8 * q + 2 * k]), __uint_as_float(o[8 * q + 2 * k + 1]));
+                        x[q] = make_uint4(y[0], y[1], y[2], y[3]);
                     }
+                    swap_units(x);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (live[k]) *reinterpret_cast<uint4 *>(to[k] + col * 2) = x[k];
                 }
             }
-            if (steps > 0) {
+            if (it.steps > 0) {
                 tc_fence_before();
                 __syncwarp();
                 pipe.arrive_if(lane == 0, kBarOfree);
@@ -610,29 +525,22 @@ __global__ void __launch_bounds__(kThreads, 1) sink_dkv_tc_kernel(const __grid_c
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == kStWarp) {
         tc_fence_after();
         tmem_free(tmem, kTmemCols);
     }
 }
-}  // namespace dkv
 
-template <int D>
-hils_status run(const SinkBwdArgs &a, const CUtensorMap (&m)[10], dq::Args q, dkv::Args k, int total, cudaStream_t s) {
-    static KernelSetup s0, s1;
-    int p0 = 0, p1 = 0;
-    const auto f0 = dq::sink_dq_tc_kernel<D>;
-    const auto f1 = dkv::sink_dkv_tc_kernel<D>;
-    hils_status st = kernel_setup(s0, (const void *)f0, kThreads, dq::Smem<D>::kBytes, &p0);
+template <int D, bool DQ>
+hils_status run(const Args &f, const CUtensorMap *m, cudaStream_t s) {
+    static KernelSetup setup;
+    int per_sm = 0;
+    const auto k = sink_bwd_tc_kernel<D, DQ>;
+    const hils_status st = kernel_setup(setup, (const void *)k, kThreads, Smem<D>::kBytes, &per_sm);
     if (st != HILS_OK) return st;
-    st = kernel_setup(s1, (const void *)f1, kThreads, dkv::Smem<D>::kBytes, &p1);
-    if (st != HILS_OK) return st;
-    if (p0 < 1 || p1 < 1) return HILS_ERR_CUDA;
+    if (per_sm < 1) return HILS_ERR_CUDA;
     const int sms = device_sm_count();
-    f0<<<q.items < sms ? q.items : sms, kThreads, dq::Smem<D>::kBytes, s>>>(m[0], m[1], m[2], m[3], m[4], m[5], q);
-    st = record_cuda_error(cudaGetLastError());
-    if (st != HILS_OK) return st;
-    f1<<<total < sms ? total : sms, kThreads, dkv::Smem<D>::kBytes, s>>>(m[6], m[7], m[8], m[9], k, total);
+    k<<<f.total < sms ? f.total : sms, kThreads, Smem<D>::kBytes, s>>>(m[0], m[1], m[2], m[3], m[4], m[5], f);
     return record_cuda_error(cudaGetLastError());
 }
 
@@ -641,29 +549,32 @@ hils_status run(const SinkBwdArgs &a, const CUtensorMap (&m)[10], dq::Args q, dk
 bool launch_sink_backward_tc(hils_dtype dt, int d, const SinkBwdArgs &a, cudaStream_t s, hils_status *st) {
     if (dt != HILS_BF16 || a.N == 0) return false;
     const int Hk = a.H / a.G;
-    dq::Args q{};
-    q.a = a;
+    Args q{}, k{};
+    q.a = k.a = a;
     q.P = sink_pack(a.G);
-    q.qt = dq::kM / q.P;
-    q.nqb = (a.Lq + 2 * q.qt - 1) / (2 * q.qt);
-    const int64_t qi = (int64_t)a.B * (a.H / q.P) * q.nqb;
-    dkv::Args k{};
-    k.a = a;
+    q.qt = kM / q.P;
+    q.tiles = (a.Lq + q.qt - 1) / q.qt;
+    const int64_t qi = (int64_t)a.B * (a.H / q.P) * q.tiles;
     k.items = (int)sink_key_items(a);
     const int64_t ki = (int64_t)k.items * a.B * Hk;
     if (qi > 0x7fffffffll - 1024 || ki > 0x7fffffffll - 1024) return false;
-    q.items = (int)qi;
+    q.total = (int)qi;
+    k.total = (int)ki;
     const int sinks = a.A > 0 ? a.A : 1;
-    q.sink_box = sinks < dq::kKeys ? (sinks + 15) & ~15 : dq::kKeys;
-    CUtensorMap m[10];
-    if (!make_view_map(&m[0], a.Q, a.B, a.H, a.Lq, d, q.qt, q.P) || !make_view_map(&m[1], a.dO, a.B, a.H, a.Lq, d, q.qt, q.P) ||
-        !make_view_map(&m[2], a.K, a.B, Hk, a.N, d, dq::kKeys, 1) || !make_view_map(&m[3], a.V, a.B, Hk, a.N, d, dq::kKeys, 1) ||
-        !make_view_map(&m[4], a.K, a.B, Hk, sinks, d, q.sink_box, 1) ||
-        !make_view_map(&m[5], a.V, a.B, Hk, sinks, d, q.sink_box, 1) ||
-        !make_view_map(&m[6], a.Q, a.B, a.H, a.Lq, d, dkv::kRows, 1) || !make_view_map(&m[7], a.dO, a.B, a.H, a.Lq, d, dkv::kRows, 1) ||
-        !make_view_map(&m[8], a.K, a.B, Hk, a.N, d, dkv::kM, 1) || !make_view_map(&m[9], a.V, a.B, Hk, a.N, d, dkv::kM, 1))
+    q.sink_box = sinks < kRows ? (sinks + 15) & ~15 : kRows;
+    CUtensorMap mq[6], mk[6];
+    if (!make_view_map(&mq[0], a.Q, a.B, a.H, a.Lq, d, q.qt, q.P) || !make_view_map(&mq[1], a.dO, a.B, a.H, a.Lq, d, q.qt, q.P) ||
+        !make_view_map(&mq[2], a.K, a.B, Hk, a.N, d, kRows, 1) || !make_view_map(&mq[3], a.V, a.B, Hk, a.N, d, kRows, 1) ||
+        // the sinks alone: their maps end at the last one
+        !make_view_map(&mq[4], a.K, a.B, Hk, sinks, d, q.sink_box, 1) ||
+        !make_view_map(&mq[5], a.V, a.B, Hk, sinks, d, q.sink_box, 1) ||
+        !make_view_map(&mk[0], a.K, a.B, Hk, a.N, d, kM, 1) || !make_view_map(&mk[1], a.V, a.B, Hk, a.N, d, kM, 1) ||
+        !make_view_map(&mk[2], a.Q, a.B, a.H, a.Lq, d, kRows, 1) || !make_view_map(&mk[3], a.dO, a.B, a.H, a.Lq, d, kRows, 1))
         return false;
-    *st = d == 64 ? run<64>(a, m, q, k, (int)ki, s) : run<128>(a, m, q, k, (int)ki, s);
+    mk[4] = mk[2];  // not used
+    mk[5] = mk[3];
+    *st = d == 64 ? run<64, true>(q, mq, s) : run<128, true>(q, mq, s);
+    if (*st == HILS_OK) *st = d == 64 ? run<64, false>(k, mk, s) : run<128, false>(k, mk, s);
     return true;
 }
 

@@ -228,23 +228,29 @@ __global__ void __launch_bounds__(kThr) sink_fwd_kernel(SinkArgs a, int tiles) {
     }
 }
 
-// D_i = dO_i . o_i, one warp per query row.
+// D_i = dO_i . o_i: D / kV lanes a row, four rounds of rows a warp in flight (bound by HBM).
 template <typename T, int D>
 __global__ void __launch_bounds__(256) sink_dot_kernel(SinkBwdArgs a, float *Dv) {
-    const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
-    const int lane = threadIdx.x % 32;
-    if (row >= (int64_t)a.B * a.H * a.Lq) return;
-    const int64_t i = row % a.Lq, bh = row / a.Lq, b = bh / a.H, h = bh % a.H;
-    const T *o = static_cast<const T *>(a.O.ptr) + b * a.O.sb + h * a.O.sh + i * a.O.st;
-    const T *g = static_cast<const T *>(a.dO.ptr) + b * a.dO.sb + h * a.dO.sh + i * a.dO.st;
-    float s = 0.f;
+    constexpr int kL = D / Vec<T>::kN, kPer = 32 / kL, kRounds = 4;  // lanes of a row, rows of a round
+    const int64_t rows = (int64_t)a.B * a.H * a.Lq;
+    const int64_t r0 = ((int64_t)blockIdx.x * 8 + threadIdx.x / 32) * (kPer * kRounds) + threadIdx.x % 32 / kL;
+    const int u = threadIdx.x % kL;
+    uint4 x[kRounds], y[kRounds];
 #pragma unroll
-    for (int x = 2 * lane; x < D; x += 64) {
-        const float2 u = load2(o + x), v = load2(g + x);
-        s = fmaf(u.x, v.x, fmaf(u.y, v.y, s));
+    for (int k = 0; k < kRounds; ++k) {
+        const int64_t row = min(r0 + k * kPer, rows - 1);
+        const int64_t bh = row / a.Lq, i = row - bh * a.Lq;
+        const int b = (int)bh / a.H, h = (int)bh - b * a.H;
+        x[k] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(a.O.ptr) + b * a.O.sb + h * a.O.sh + i * a.O.st) + u);
+        y[k] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(a.dO.ptr) + b * a.dO.sb + h * a.dO.sh + i * a.dO.st) + u);
     }
-    s = warp_sum(s);
-    if (lane == 0) Dv[row] = s;
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+        float s = dot16<T>(x[k], y[k], 0.f);
+#pragma unroll
+        for (int o = kL / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+        if (u == 0 && r0 + k * kPer < rows) Dv[r0 + k * kPer] = s;
+    }
 }
 
 // Whether any query row sees key j: the slots of acc_out that a weights call writes.
@@ -404,21 +410,23 @@ __global__ void __launch_bounds__(kThr) sink_bwd_kernel(SinkBwdArgs a, int tiles
     }
 }
 
-// One warp per key row of a block with several segments: the partials in segment order.
+// The partials of key blocks with several segments, in segment order: one warp per key row
+// (weights: one thread per key). `keys`: the first keys of each head, that such blocks hold.
 template <bool WEIGHTS, typename T, int D>
-__global__ void __launch_bounds__(256) sink_reduce_kernel(SinkBwdArgs a, int items) {
-    const int64_t g = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+__global__ void __launch_bounds__(256) sink_reduce_kernel(SinkBwdArgs a, int items, int keys) {
     const int lane = threadIdx.x % 32, Hk = a.H / a.G;
-    if (g >= (int64_t)a.B * Hk * a.N) return;
-    const int j = (int)(g % a.N);
-    const int64_t xb = g / a.N;
+    const int64_t g = WEIGHTS ? (int64_t)blockIdx.x * 256 + threadIdx.x : (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+    if (g >= (int64_t)a.B * Hk * keys) return;
+    const int64_t xb = g / keys;
+    const int j = (int)(g - xb * keys);
     const int blk = j / a.keys, kr = j % a.keys;
     const int nseg = blk < a.nsink ? a.seg_s : a.seg_w;
     if (nseg <= 1) return;
     const int64_t first = xb * items + (blk < a.nsink ? blk * a.seg_s : a.nsink * a.seg_s + (blk - a.nsink) * a.seg_w);
     if (WEIGHTS) {
-        if (lane != 0 || !seen_key(a, j)) return;
+        if (!seen_key(a, j)) return;
         float s = 0.f;
+#pragma unroll 4
         for (int q = 0; q < nseg; ++q) s += a.part[(first + q) * a.keys + kr];
         const int64_t at = xb * a.T + j;
         a.acc_out[at] = a.acc[at] + s;
@@ -431,6 +439,7 @@ __global__ void __launch_bounds__(256) sink_reduce_kernel(SinkBwdArgs a, int ite
         T *dst = static_cast<T *>(v.ptr) + b * v.sb + hk * v.sh + (int64_t)j * v.st;
         for (int x = 2 * lane; x < D; x += 64) {
             float2 s = make_float2(0.f, 0.f);
+#pragma unroll 8
             for (int q = 0; q < nseg; ++q) {
                 const float2 p = load2(a.part + ((first + q) * 2 * kSinkKeys + which * kSinkKeys + kr) * D + x);
                 s.x += p.x;
@@ -461,7 +470,8 @@ hils_status forward(const SinkArgs &a, cudaStream_t s) {
 template <typename T, int D>
 hils_status dot(const SinkBwdArgs &a, float *Dv, cudaStream_t s) {
     static KernelSetup setup;
-    return run(setup, sink_dot_kernel<T, D>, ((int64_t)a.B * a.H * a.Lq + 7) / 8, 256, 0, s, a, Dv);
+    constexpr int kRows = 8 * 4 * 32 * Vec<T>::kN / D;  // of a CTA
+    return run(setup, sink_dot_kernel<T, D>, ((int64_t)a.B * a.H * a.Lq + kRows - 1) / kRows, 256, 0, s, a, Dv);
 }
 template <typename T, int D>
 hils_status backward(const SinkBwdArgs &a, cudaStream_t s) {
@@ -484,10 +494,12 @@ template <typename T, int D>
 hils_status reduce(const SinkBwdArgs &a, bool w, cudaStream_t s) {
     static KernelSetup s0, s1;
     if (a.seg_s <= 1 && a.seg_w <= 1) return HILS_OK;
-    const int64_t grid = ((int64_t)a.B * (a.H / a.G) * a.N + 7) / 8;
+    const int64_t last = (int64_t)a.nsink * a.keys;  // (without segments behind the sinks' blocks)
+    const int keys = a.seg_w > 1 || last > a.N ? a.N : (int)last;
+    const int64_t rows = (int64_t)a.B * (a.H / a.G) * keys;
     const int items = (int)sink_key_items(a);
-    return w ? run(s0, sink_reduce_kernel<true, T, D>, grid, 256, 0, s, a, items)
-             : run(s1, sink_reduce_kernel<false, T, D>, grid, 256, 0, s, a, items);
+    return w ? run(s0, sink_reduce_kernel<true, T, D>, (rows + 255) / 256, 256, 0, s, a, items, keys)
+             : run(s1, sink_reduce_kernel<false, T, D>, (rows + 7) / 8, 256, 0, s, a, items, keys);
 }
 
 }  // namespace
