@@ -59,7 +59,7 @@ struct Smem {
 struct Args {
     SinkBwdArgs a;
     int P, qt, tiles, sink_box;  // dQ: packed heads, queries of a tile, tiles of (b, packed heads)
-    int items;                   // dK, dV: items of one (b, key-value head)
+    int items, first;            // dK, dV: items of one (b, key-value head), the one to begin with
     int total;
 };
 
@@ -88,7 +88,8 @@ __device__ __forceinline__ Item decode(const Args &f, int j) {
         it.nseg = 1;
     } else {
         const int Hk = a.H / a.G, heads = a.B * Hk;
-        const int x = j / heads, xb = j - x * heads;  // the blocks with most steps come first
+        // the longer items first: the sinks' segments may follow the other blocks
+        const int q = j / heads, xb = j - q * heads, x0 = q + f.first, x = x0 < f.items ? x0 : x0 - f.items;
         it.b = xb / Hk;
         it.hk = xb - it.b * Hk;
         it.h = it.hk * a.G;
@@ -557,6 +558,8 @@ bool launch_sink_backward_tc(hils_dtype dt, int d, const SinkBwdArgs &a, cudaStr
     const int64_t qi = (int64_t)a.B * (a.H / q.P) * q.tiles;
     k.items = (int)sink_key_items(a);
     const int64_t ki = (int64_t)k.items * a.B * Hk;
+    const int64_t window_rows = (int64_t)a.W + kM < a.Lq ? (int64_t)a.W + kM : a.Lq;
+    if (window_rows / a.seg_w >= a.Lq / a.seg_s && a.nblk > a.nsink) k.first = a.nsink * a.seg_s;
     if (qi > 0x7fffffffll - 1024 || ki > 0x7fffffffll - 1024) return false;
     q.total = (int)qi;
     k.total = (int)ki;

@@ -411,11 +411,12 @@ __global__ void __launch_bounds__(kThr) sink_bwd_kernel(SinkBwdArgs a, int tiles
 }
 
 // The partials of key blocks with several segments, in segment order: one warp per key row
-// (weights: one thread per key). `keys`: the first keys of each head, that such blocks hold.
+// of dK and one of dV (weights: one thread per key). `keys`: the first keys of each head, that such blocks hold.
 template <bool WEIGHTS, typename T, int D>
 __global__ void __launch_bounds__(256) sink_reduce_kernel(SinkBwdArgs a, int items, int keys) {
     const int lane = threadIdx.x % 32, Hk = a.H / a.G;
-    const int64_t g = WEIGHTS ? (int64_t)blockIdx.x * 256 + threadIdx.x : (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+    const int g_which = blockIdx.x & 1;
+    const int64_t g = WEIGHTS ? (int64_t)blockIdx.x * 256 + threadIdx.x : (int64_t)(blockIdx.x / 2) * 8 + threadIdx.x / 32;
     if (g >= (int64_t)a.B * Hk * keys) return;
     const int64_t xb = g / keys;
     const int j = (int)(g - xb * keys);
@@ -432,22 +433,24 @@ __global__ void __launch_bounds__(256) sink_reduce_kernel(SinkBwdArgs a, int ite
         a.acc_out[at] = a.acc[at] + s;
         return;
     }
-    const int b = (int)(xb / Hk), hk = (int)(xb % Hk);
+    // a lane's D / 32 columns, 16 segments in flight
+    constexpr int kE = D / 32;
+    const int b = (int)(xb / Hk), hk = (int)(xb % Hk), which = g_which;
+    const MutView &v = which ? a.dV : a.dK;
+    T *dst = static_cast<T *>(v.ptr) + b * v.sb + hk * v.sh + (int64_t)j * v.st + lane * kE;
+    const float *p = a.part + (first * 2 * kSinkKeys + which * kSinkKeys + kr) * D + lane * kE;
+    float s[kE] = {};
+#pragma unroll 16
+    for (int q = 0; q < nseg; ++q) {
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        const MutView &v = which ? a.dV : a.dK;
-        T *dst = static_cast<T *>(v.ptr) + b * v.sb + hk * v.sh + (int64_t)j * v.st;
-        for (int x = 2 * lane; x < D; x += 64) {
-            float2 s = make_float2(0.f, 0.f);
-#pragma unroll 8
-            for (int q = 0; q < nseg; ++q) {
-                const float2 p = load2(a.part + ((first + q) * 2 * kSinkKeys + which * kSinkKeys + kr) * D + x);
-                s.x += p.x;
-                s.y += p.y;
-            }
-            store2(dst + x, s.x, s.y);
+        for (int e = 0; e < kE; e += 2) {
+            const float2 x = load2(p + (int64_t)q * 2 * kSinkKeys * D + e);
+            s[e] += x.x;
+            s[e + 1] += x.y;
         }
     }
+#pragma unroll
+    for (int e = 0; e < kE; e += 2) store2(dst + e, s[e], s[e + 1]);
 }
 
 template <typename K>
@@ -499,7 +502,7 @@ hils_status reduce(const SinkBwdArgs &a, bool w, cudaStream_t s) {
     const int64_t rows = (int64_t)a.B * (a.H / a.G) * keys;
     const int items = (int)sink_key_items(a);
     return w ? run(s0, sink_reduce_kernel<true, T, D>, (rows + 255) / 256, 256, 0, s, a, items, keys)
-             : run(s1, sink_reduce_kernel<false, T, D>, (rows + 7) / 8, 256, 0, s, a, items, keys);
+             : run(s1, sink_reduce_kernel<false, T, D>, (rows + 7) / 8 * 2, 256, 0, s, a, items, keys);
 }
 
 }  // namespace

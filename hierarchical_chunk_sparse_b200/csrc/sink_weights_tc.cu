@@ -9,9 +9,10 @@
 // the next steps are loaded meanwhile. The rows' lse (log2 units) are staged in shared memory.
 // The exponentials bound it (16 a cycle and SM on the MUFU against 8192 products): every
 // fourth one is evaluated on the FMA pipe instead.
-// Warps 0-7, 8-15: the keys of tile A, B (TMEM lane quadrant w % 4), each key's columns in two
-// halves: with one warp per quadrant and tile the loads and exponentials waited on their
-// latencies; 16, 17: tcgen05.mma of A, B; 18: TMA and lse.
+// Warps 0-7, 8-15: the keys of tile A, B (TMEM lane quadrant w % 4), four warps for its even
+// steps and four for the odd: with one warp per quadrant and tile the loads and exponentials
+// waited on their latencies; 16, 17: tcgen05.mma of A, B; 18: TMA; 19: lse, fetched two steps
+// ahead.
 // TMEM: S_A [0,128), [128,256); S_B [256,384), [384,512).
 #include "fast_math.cuh"
 #include "sink_tc.cuh"
@@ -21,7 +22,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kM = 128, kKeys = 2 * kM, kRows = 128, kStages = 3, kThreads = 608, kMmaWarp = 16, kLoadWarp = 18;
+constexpr int kM = 128, kKeys = 2 * kM, kRows = 128, kStages = 3, kThreads = 640, kMmaWarp = 16, kLoadWarp = 18, kLseWarp = 19;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -29,11 +30,11 @@ enum {
     kBarXfull = 0,   // + buffer: the item's keys
     kBarXfree = 2,   // + buffer (both tiles)
     kBarYfull = 4,   // + stage: query rows (bytes) and lse (32 arrivals)
-    kBarYfree = 7,   // + stage: both tiles' products, and the 16 warps' reads of lse
+    kBarYfree = 7,   // + stage: lse read by both tiles' 4 warps (so the products are done too)
     kBarS = 10,      // + 2 * tile + buffer: S^T written
-    kBarSfree = 14,  // + 2 * tile + buffer: S^T read (8 warps)
+    kBarSfree = 14,  // + 2 * tile + buffer: S^T read (4 warps)
     kBarDrain = 18,  // + tile
-    kBarHalf = 20,   // + 4 tile + quadrant: the second half's sums are in hsum
+    kBarHalf = 20,   // + 4 tile + quadrant: the odd steps' sums are in hsum
     kBarHalfFree = 28,  // + the same: read
     kNumBars = 36
 };
@@ -41,7 +42,7 @@ template <int D>
 struct Smem {
     static constexpr int kX = kM * D * 2, kY = kRows * D * 2;
     static constexpr int kK = 0, kQ = 4 * kX, kL = kQ + kStages * kY;
-    static constexpr int kH = kL + kStages * kRows * 4;  // sums of the keys' second halves
+    static constexpr int kH = kL + kStages * kRows * 4;  // sums of the odd steps
     static constexpr int kBars = kH + kKeys * 4, kMisc = kBars + 8 * kNumBars;
     static constexpr int kBytes = kMisc + 16;
 };
@@ -52,37 +53,58 @@ struct Args {
 };
 struct Item {
     int xb, b, hk, j0, i0, tiles, s0, s1, nseg, index;
-    int r0[2], r1[2];  // the queries that see a key of A, B
-
-    __device__ __forceinline__ bool valid(int x, int q0, int qn) const { return q0 < r1[x] && q0 + qn > r0[x]; }
+    int a0, a1, b0, b1;  // the queries that see a key of A, B
 };
 __device__ __forceinline__ Item decode(const Args &f, int j) {
     const SinkBwdArgs &a = f.a;
     const int Hk = a.H / a.G, heads = a.B * Hk;
     Item it;
-    it.xb = j % heads;  // the blocks with most steps (the first ones of a causal range) come first
     const int y = j / heads;
+    it.xb = j - y * heads;  // the blocks with most steps (the first ones of a causal range) come first
     it.b = it.xb / Hk;
-    it.hk = it.xb % Hk;
+    it.hk = it.xb - it.b * Hk;
     const SinkItem k = sink_item(a, y);
     it.j0 = k.blk * kKeys;
     it.nseg = k.nseg;
     it.index = it.xb * f.items + y;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const int j1 = it.j0 + x * kM;
-        it.r0[x] = it.r1[x] = 0;
-        if (j1 < a.N) sink_rows_of_block(a, j1, min(kM, a.N - j1), &it.r0[x], &it.r1[x]);
-    }
-    const bool hasA = it.r0[0] < it.r1[0], hasB = it.r0[1] < it.r1[1];
-    it.i0 = hasA ? it.r0[0] : it.r0[1];
-    const int i1 = hasB ? max(it.r1[1], hasA ? it.r1[0] : 0) : it.r1[0];
+    it.b0 = it.b1 = 0;
+    sink_rows_of_block(a, it.j0, min(kM, a.N - it.j0), &it.a0, &it.a1);
+    if (it.j0 + kM < a.N) sink_rows_of_block(a, it.j0 + kM, min(kM, a.N - it.j0 - kM), &it.b0, &it.b1);
+    const bool hasA = it.a0 < it.a1, hasB = it.b0 < it.b1;
+    it.i0 = hasA ? it.a0 : it.b0;
+    const int i1 = hasB ? max(it.b1, hasA ? it.a1 : 0) : it.a1;
     it.tiles = hasA || hasB ? (i1 - it.i0 + f.qn - 1) / f.qn : 0;
-    const int64_t steps = (int64_t)(a.G / f.P) * it.tiles;
-    it.s0 = (int)(steps * k.seg / k.nseg);
-    it.s1 = (int)(steps * (k.seg + 1) / k.nseg);
+    const int steps = (a.G / f.P) * it.tiles;
+    it.s0 = 0;
+    it.s1 = steps;
+    if (k.nseg > 1) {
+        it.s0 = (int)((int64_t)steps * k.seg / k.nseg);
+        it.s1 = (int)((int64_t)steps * (k.seg + 1) / k.nseg);
+    }
     return it;
 }
+
+// A walk over an item's steps: the step's query tile and head pack, and its stage with the
+// stage's phase (kept over the items).
+struct Walk {
+    int st = 0;
+    uint32_t ph = 0;
+    int tile = 0, h = 0;
+    __device__ __forceinline__ void start(const Item &it) {
+        h = it.s0 > 0 ? it.s0 / it.tiles : 0;
+        tile = it.s0 - h * it.tiles;
+    }
+    __device__ __forceinline__ void next(const Item &it) {
+        if (++st == kStages) {
+            st = 0;
+            ph ^= 1u;
+        }
+        if (++tile == it.tiles) {
+            tile = 0;
+            ++h;
+        }
+    }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -108,8 +130,8 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
             uint32_t cnt = 1;
             if (i == kBarXfree || i == kBarXfree + 1) cnt = 2;
             if (i >= kBarYfull && i < kBarYfull + kStages) cnt = 33;
-            if (i >= kBarYfree && i < kBarYfree + kStages) cnt = 18;
-            if (i >= kBarSfree && i < kBarSfree + 4) cnt = 8;
+            if (i >= kBarYfree && i < kBarYfree + kStages) cnt = 8;
+            if (i >= kBarSfree && i < kBarSfree + 4) cnt = 4;
             mbar_init(pipe.bar(i), cnt);
         }
         misc[1] = 0u;
@@ -124,6 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
     if (warp == kLoadWarp) {
         int n = 0, g = 0;  // items with steps, steps
         bool ok = true;
+        Walk w;
         for (int r = 0; ok; ++r) {
             const int j = item_of_round(r, cta, G);
             if (j >= total) break;
@@ -131,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
             if (it.s0 >= it.s1) continue;
             const int xb = n & 1;
             if (n >= 2 && !(ok = pipe.wait_warp(kBarXfree + xb, ((n >> 1) - 1) & 1))) break;
-            if (lane == 0) {
+            if (elect_one()) {
                 mbar_expect_tx(pipe.bar(kBarXfull + xb), 2 * L::kX);
 #pragma unroll
                 for (int x = 0; x < 2; ++x)  // B's keys may lie behind the last one: zeros
@@ -140,33 +163,20 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
                         tma_load_4d(sbase + L::kK + (2 * xb + x) * L::kX + c * kBlk, &tmK, pipe.bar(kBarXfull + xb), c * 64,
                                     it.j0 + x * kM, it.hk, it.b);
             }
+            __syncwarp();
             ++n;
-            float sc[4];  // lse of rows lane + 32 m of the next step
-            auto scalars = [&](int s) {
-                const int h0 = it.hk * a.G + s / it.tiles * f.P, q0 = it.i0 + (s % it.tiles) * f.qn;
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int row = lane + 32 * m, i = q0 + row % f.qn;
-                    float v = -INFINITY;
-                    if (i < a.Lq) v = __ldg(a.lse + ((int64_t)it.b * a.H + h0 + row / f.qn) * a.Lq + i);
-                    sc[m] = v == -INFINITY ? v : -v * kLog2e;  // -lse; nothing seen: exp2(s - inf) = 0
-                }
-            };
-            scalars(it.s0);
+            w.start(it);
             for (int s = it.s0; s < it.s1; ++s, ++g) {
-                const int st = g % kStages;
-                if (g >= kStages && !(ok = pipe.wait_warp(kBarYfree + st, (g / kStages - 1) & 1))) break;
-                if (lane == 0) {
-                    mbar_expect_tx(pipe.bar(kBarYfull + st), L::kY);
+                if (g >= kStages && !(ok = pipe.wait_warp(kBarYfree + w.st, w.ph ^ 1u))) break;
+                if (elect_one()) {
+                    mbar_expect_tx(pipe.bar(kBarYfull + w.st), L::kY);
 #pragma unroll
                     for (int c = 0; c < kBlocks; ++c)
-                        tma_load_4d(sbase + L::kQ + st * L::kY + c * kBlk, &tmQ, pipe.bar(kBarYfull + st), c * 64,
-                                    it.i0 + (s % it.tiles) * f.qn, it.hk * a.G + s / it.tiles * f.P, it.b);
+                        tma_load_4d(sbase + L::kQ + w.st * L::kY + c * kBlk, &tmQ, pipe.bar(kBarYfull + w.st), c * 64,
+                                    it.i0 + w.tile * f.qn, it.hk * a.G + w.h * f.P, it.b);
                 }
-#pragma unroll
-                for (int m = 0; m < 4; ++m) lse[st * kRows + lane + 32 * m] = sc[m];
-                pipe.arrive(kBarYfull + st);
-                if (s + 1 < it.s1) scalars(s + 1);
+                __syncwarp();
+                w.next(it);
             }
         }
         if (lane == 0) {
@@ -174,32 +184,77 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
             for (int s = 0; s < kStages; ++s) pipe.drain(kBarYfull + s, g > s ? (g - s + kStages - 1) / kStages : 0);
         }
         __syncwarp();
+    } else if (warp == kLseWarp) {
+        const int qshift = 31 - __clz(f.qn);
+        int g = 0;
+        bool ok = true;
+        Walk w;
+        for (int r = 0; ok; ++r) {
+            const int j = item_of_round(r, cta, G);
+            if (j >= total) break;
+            const Item it = decode(f, j);
+            if (it.s0 >= it.s1) continue;
+            w.start(it);
+            int tile = w.tile, h = w.h, next = it.s0;
+            float sc[2][4];  // lse of rows lane + 32 m of the next two steps
+            auto fetch = [&](float(&d)[4]) {
+                if (next >= it.s1) return;
+                ++next;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int row = lane + 32 * m, i = it.i0 + tile * f.qn + (row & (f.qn - 1));
+                    const int64_t bh = (int64_t)it.b * a.H + it.hk * a.G + h * f.P + (row >> qshift);
+                    d[m] = i < a.Lq ? __ldg(a.lse + bh * a.Lq + i) : -INFINITY;
+                }
+                if (++tile == it.tiles) {
+                    tile = 0;
+                    ++h;
+                }
+            };
+            auto put = [&](float(&d)[4]) {
+                if (g >= kStages && !(ok = pipe.wait_warp(kBarYfree + w.st, w.ph ^ 1u))) return;
+#pragma unroll
+                for (int m = 0; m < 4; ++m)  // nothing seen: exp2(s - inf) = 0
+                    lse[w.st * kRows + lane + 32 * m] = d[m] == -INFINITY ? d[m] : -d[m] * kLog2e;
+                pipe.arrive(kBarYfull + w.st);
+                ++g;
+                w.next(it);
+                fetch(d);
+            };
+            fetch(sc[0]);
+            fetch(sc[1]);
+            for (int s = it.s0; s < it.s1 && ok; s += 2) {
+                put(sc[0]);
+                if (ok && s + 1 < it.s1) put(sc[1]);
+            }
+        }
+        __syncwarp();
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         const int x = warp - kMmaWarp;
-        int n = 0, g = 0, c = 0;  // items with steps, steps, steps of x
+        int n = 0, c = 0;  // items with steps, steps of x
         bool ok = true;
+        Walk w;
         const uint64_t kd0 = tile_desc(sbase + L::kK + x * L::kX, 16), qd0 = tile_desc(sbase + L::kQ, 16);
         for (int r = 0; ok; ++r) {
             const int j = item_of_round(r, cta, G);
             if (j >= total) break;
             const Item it = decode(f, j);
             if (it.s0 >= it.s1) continue;
-            const int xb = n & 1;
-            const uint64_t kd = kd0 + xb * (2 * L::kX / 16);
-            if (!(ok = pipe.wait_warp(kBarXfull + xb, (n >> 1) & 1))) break;
-            int tile = it.s0 % it.tiles;
-            for (int s = it.s0; s < it.s1; ++s, ++g) {
-                const int st = g % kStages, q0 = it.i0 + tile * f.qn;
-                if (++tile == it.tiles) tile = 0;
-                if (!(ok = pipe.wait_warp(kBarYfull + st, (g / kStages) & 1))) break;
-                if (!it.valid(x, q0, f.qn)) {
-                    pipe.arrive_if(lane == 0, kBarYfree + st);
+            const uint64_t kd = kd0 + (n & 1) * (2 * L::kX / 16);
+            if (!(ok = pipe.wait_warp(kBarXfull + (n & 1), (n >> 1) & 1))) break;
+            w.start(it);
+            // first queries of the steps that x takes part in
+            const int q_lo = (x ? it.b0 : it.a0) - f.qn - it.i0, q_hi = (x ? it.b1 : it.a1) - it.i0;
+            for (int s = it.s0; s < it.s1; ++s, w.next(it)) {
+                const int q = w.tile * f.qn, sb = 2 * x + (c & 1);
+                if (!(ok = pipe.wait_warp(kBarYfull + w.st, w.ph))) break;
+                if (q <= q_lo || q >= q_hi) {  // for the softmax warps
+                    pipe.arrive_if(lane == 0, kBarYfree + w.st, 4);
                     continue;
                 }
-                const int sb = 2 * x + (c & 1);
                 if (c >= 2 && !(ok = pipe.wait_warp(kBarSfree + sb, ((c >> 1) - 1) & 1))) break;
                 tc_fence_after();
-                const uint64_t qd = qd0 + st * (L::kY / 16);
+                const uint64_t qd = qd0 + w.st * (L::kY / 16);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
@@ -207,13 +262,12 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
                         mma_ss(tmem + sb * 128, kd + o, qd + o, idesc_bf16(kM, kRows, false), k > 0);
                     }
                     mma_commit(pipe.bar(kBarS + sb));
-                    mma_commit(pipe.bar(kBarYfree + st));
                 }
                 __syncwarp();
                 ++c;
             }
             if (!ok) break;
-            if (elect_one()) mma_commit(pipe.bar(kBarXfree + xb));
+            if (elect_one()) mma_commit(pipe.bar(kBarXfree + (n & 1)));
             __syncwarp();
             ++n;
         }
@@ -222,76 +276,83 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
             pipe.drain(kBarDrain + x, 1);
         }
         __syncwarp();
-    } else if (warp < 16) {
-        const int x = warp >> 3, quad = warp & 3, half = (warp >> 2) & 1, row = quad * 32 + lane;
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    } else {
+        const int x = warp >> 3, quad = warp & 3, odd = (warp >> 2) & 1, row = quad * 32 + lane, pair = 4 * x + quad;
+        const int sb = 2 * x + odd;
+        const uint32_t s_col = tmem + ((uint32_t)(quad * 32) << 16) + sb * 128;
         const float scale2 = a.scale * kLog2e, lowest = scale2 > 0.f ? -INFINITY : INFINITY;  // its logit is -inf
         const float2 scale22 = make_float2(scale2, scale2);
         const int off = a.N - a.Lq, Hk = a.H / a.G;
         bool ok = true;
-        int g = 0, c = 0, n = 0;
+        int c = 0, n = 0;
+        Walk walk;
         for (int r = 0; ok; ++r) {
             const int j = item_of_round(r, cta, G);
             if (j >= total) break;
             const Item it = decode(f, j);
             const int key = it.j0 + x * kM + row;
             float w = 0.f;
-            int tile = it.s0 % max(it.tiles, 1);
-            for (int s = it.s0; s < it.s1; ++s, ++g) {
-                const int st = g % kStages, q0 = it.i0 + tile * f.qn;
-                if (++tile == it.tiles) tile = 0;
-                if (!(ok = pipe.wait_warp(kBarYfull + st, (g / kStages) & 1))) break;
-                if (!it.valid(x, q0, f.qn)) {
-                    pipe.arrive_if(lane == 0, kBarYfree + st);
-                    continue;
-                }
-                // queries of each head that see this key
-                const int lo = key - off - q0, end = min(f.qn, a.Lq - q0);
-                const int hi = key < a.A ? end : min(end, (int)min((int64_t)key + a.W - off - q0, (int64_t)kRows));
+            walk.start(it);
+            const int q_lo = (x ? it.b0 : it.a0) - f.qn - it.i0, q_hi = (x ? it.b1 : it.a1) - it.i0;
+            // queries that see this key, from the item's first on
+            const int see0 = key - off - it.i0;
+            const int see1 = (int)min(key < a.A ? (int64_t)a.Lq : (int64_t)key + a.W - off, (int64_t)a.Lq) - it.i0;
+            for (int s = it.s0; s < it.s1; ++s, walk.next(it)) {
+                const int q = walk.tile * f.qn;
+                if (q <= q_lo || q >= q_hi || (c++ & 1) != odd) continue;
+                const int lo = see0 - q, hi = min(f.qn, see1 - q);  // of each head
                 const bool full = __all_sync(kFull, lo <= 0 && hi == f.qn);
-                const int sb = 2 * x + (c & 1);
-                if (!(ok = pipe.wait_warp(kBarS + sb, (c >> 1) & 1))) break;
+                if (!(ok = pipe.wait_warp(kBarS + sb, ((c - 1) >> 1) & 1))) break;
+                if (!(ok = pipe.wait_warp(kBarYfull + walk.st, walk.ph))) break;  // complete: S came of it
                 tc_fence_after();
-                const uint32_t s_col = tmem + lanes + sb * 128 + half * 64;
-                const float *lr = lse + st * kRows + half * 64;
+                const float *lr = lse + walk.st * kRows;
                 float2 z0 = make_float2(0.f, 0.f), z1 = z0;
 #pragma unroll
                 for (int ch = 0; ch < 2; ++ch) {
-                    uint32_t mk = kFull;
-                    if (!full) {
-                        mk = range_bits(lo, hi, (half * 64 + ch * 32) & (f.qn - 1));
-                        if (f.qn == 16) mk |= mk << 16;
-                        if (!__any_sync(kFull, mk != 0)) continue;
-                    }
-                    uint32_t v[32];
-                    tmem_ld32(s_col + ch * 32, v);
+                    uint32_t v[64];
+                    tmem_ld32(s_col + ch * 64, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+                    tmem_ld32(s_col + ch * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
                     tmem_wait_ld();
+                    if (ch == 1) {  // S is handed back before the last exponentials
+                        tc_fence_before();
+                        __syncwarp();
+                        pipe.arrive_if(lane == 0, kBarSfree + sb);
+                    }
                     if (!full) {
+                        uint32_t mk0 = range_bits(lo, hi, (ch * 64) & (f.qn - 1)), mk1 = range_bits(lo, hi, (ch * 64 + 32) & (f.qn - 1));
+                        if (f.qn == 16) {
+                            mk0 |= mk0 << 16;
+                            mk1 |= mk1 << 16;
+                        }
 #pragma unroll
-                        for (int q = 0; q < 32; ++q) v[q] = (mk >> q) & 1u ? v[q] : __float_as_uint(lowest);
+                        for (int e = 0; e < 32; ++e) {
+                            v[e] = (mk0 >> e) & 1u ? v[e] : __float_as_uint(lowest);
+                            v[32 + e] = (mk1 >> e) & 1u ? v[32 + e] : __float_as_uint(lowest);
+                        }
                     }
 #pragma unroll
-                    for (int q = 0; q < 32; q += 4) {
-                        const float4 L4 = *reinterpret_cast<const float4 *>(lr + ch * 32 + q);
-                        const float2 e0 = fma2(as2(v + q), scale22, make_float2(L4.x, L4.y));
-                        const float2 e1 = fma2(as2(v + q + 2), scale22, make_float2(L4.z, L4.w));
-                        z0 = add2(z0, make_float2(exp2_ftz(e0.x), exp2_ftz(e0.y)));
-                        z1 = add2(z1, make_float2(exp2_ftz(e1.x), exp2_fma(e1.y)));
+                    for (int q4 = 0; q4 < 64; q4 += 8) {
+                        float2 e[4];
+#pragma unroll
+                        for (int k = 0; k < 4; k += 2) {
+                            const float4 L4 = *reinterpret_cast<const float4 *>(lr + ch * 64 + q4 + 2 * k);
+                            e[k] = fma2(as2(v + q4 + 2 * k), scale22, make_float2(L4.x, L4.y));
+                            e[k + 1] = fma2(as2(v + q4 + 2 * k + 2), scale22, make_float2(L4.z, L4.w));
+                        }
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) e[k] = make_float2(exp2_ftz(e[k].x), exp2_ftz(e[k].y));
+                        e[3] = exp2_fma2(e[3]);
+                        z0 = add2(z0, add2(e[0], e[1]));
+                        z1 = add2(z1, add2(e[2], e[3]));
                     }
                 }
                 w += (z0.x + z0.y) + (z1.x + z1.y);
-                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    pipe.arrive(kBarSfree + sb);
-                    pipe.arrive(kBarYfree + st);
-                }
-                ++c;
+                pipe.arrive_if(lane == 0, kBarYfree + walk.st);
             }
             if (!ok) break;
-            // the two halves of a key, the first one's sum first
-            const int pair = 4 * x + quad;
-            if (half == 1) {
+            // the sum of the even steps, then that of the odd ones
+            if (odd) {
                 if (n > 0 && !(ok = pipe.wait_warp(kBarHalfFree + pair, (n - 1) & 1))) break;
                 hsum[x * kM + row] = w;
                 __syncwarp();
