@@ -17,8 +17,8 @@
 //          write its sums while the others begin the next item.
 //   16, 17 tcgen05.mma of S and T; of the sums;  18  TMA;  19  lse and D of a step's queries
 //          (dK, dV: a thread owns a key and runs over the queries), fetched two steps ahead.
-// TMEM: S [0,64), T [64,128), P [128,160), [160,192), dS [192,224), [224,256), dV or dQ
-// [256,384), dK [384,512). Bound by the products: S, T take 48 cycles an MMA with N = 64 (their
+// TMEM, dK and dV: S [0,64), T [64,128), P [128,160), [160,192), dS [192,224), [224,256), dV
+// [256,384), dK [384,512); dQ: S, T [0,128), [128,256), dS [256,288), [288,320), dQ [384,512). Bound by the products: S, T take 48 cycles an MMA with N = 64 (their
 // operands come from shared memory), 1024 cycles a step for dQ and 1280 for dK, dV.
 #include "sink_tc.cuh"
 
@@ -39,12 +39,12 @@ enum {
     kBarYfull = 4,   // + stage: rows (bytes); dK, dV: lse and D (32 arrivals)
     kBarYfree = 7,   // + stage: the sums that read it completed
     kBarST = 10,     // + step parity: S, T written
-    kBarSTfree = 12, // S, T read (8 warps)
-    kBarP = 13,      // + step parity: P, dS written (8 warps)
-    kBarSum = 15,    // + step parity: the sums that read them, and every one before, completed
-    kBarOfree = 17,  // an item's sums read (8 warps)
-    kBarDrain = 18,  // + MMA warp
-    kNumBars = 20
+    kBarSTfree = 12, // + buffer: S, T read (8 warps)
+    kBarP = 14,      // + step parity: P, dS written (8 warps)
+    kBarSum = 16,    // + step parity: the sums that read them, and every one before, completed
+    kBarOfree = 18,  // an item's sums read (8 warps)
+    kBarDrain = 19,  // + MMA warp
+    kNumBars = 21
 };
 
 template <int D>
@@ -59,7 +59,7 @@ struct Smem {
 struct Args {
     SinkBwdArgs a;
     int P, qt, tiles, sink_box;  // dQ: packed heads, queries of a tile, tiles of (b, packed heads)
-    int items, first;            // dK, dV: items of one (b, key-value head), the one to begin with
+    int items;                   // dK, dV: items of one (b, key-value head)
     int total;
 };
 
@@ -88,8 +88,7 @@ __device__ __forceinline__ Item decode(const Args &f, int j) {
         it.nseg = 1;
     } else {
         const int Hk = a.H / a.G, heads = a.B * Hk;
-        // the longer items first: the sinks' segments may follow the other blocks
-        const int q = j / heads, xb = j - q * heads, x0 = q + f.first, x = x0 < f.items ? x0 : x0 - f.items;
+        const int x = j / heads, xb = j - x * heads;
         it.b = xb / Hk;
         it.hk = xb - it.b * Hk;
         it.h = it.hk * a.G;
@@ -148,6 +147,8 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
     extern __shared__ __align__(1024) uint8_t smem[];
     using L = Smem<D>;
     constexpr int kBlocks = D / 64, kXBlk = kM * 128, kYBlk = kRows * 128;
+    // TMEM columns; dQ's one sum leaves room for two buffers of S, T
+    constexpr int kBufs = DQ ? 2 : 1, kP = 128, kDs = DQ ? 256 : 192, kAcc = DQ ? 384 : 256;
     const SinkBwdArgs &a = f.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = smem_u32(smem);
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
         for (int i = 0; i < kNumBars; ++i) {
             uint32_t cnt = 1;
             if (!DQ && i >= kBarYfull && i < kBarYfull + kStages) cnt = 33;
-            if (i == kBarSTfree || i == kBarP || i == kBarP + 1 || i == kBarOfree) cnt = 8;
+            if (i == kBarSTfree || i == kBarSTfree + 1 || i == kBarP || i == kBarP + 1 || i == kBarOfree) cnt = 8;
             mbar_init(pipe.bar(i), cnt);
         }
         misc[1] = 0u;
@@ -290,16 +291,17 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
                 const uint64_t yo = w.st * (L::kY / 16);
                 const uint32_t id = idesc_bf16(kM, DQ ? (step_keys(it, i) + 15) & ~15 : kRows, false);
                 if (!(ok = pipe.wait_warp(kBarYfull + w.st, w.ph))) break;
-                if (c > 0 && !(ok = pipe.wait_warp(kBarSTfree, (c - 1) & 1))) break;
+                const int buf = c & (kBufs - 1);
+                if (c >= kBufs && !(ok = pipe.wait_warp(kBarSTfree + buf, (c / kBufs - 1) & 1))) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        mma_ss(tmem, x1 + xo + ((k >> 2) * kXBlk + (k & 3) * 32) / 16, y1 + yo + ((k >> 2) * kYBlk + (k & 3) * 32) / 16,
+                        mma_ss(tmem + buf * 128, x1 + xo + ((k >> 2) * kXBlk + (k & 3) * 32) / 16, y1 + yo + ((k >> 2) * kYBlk + (k & 3) * 32) / 16,
                                id, k > 0);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        mma_ss(tmem + 64, x2 + xo + ((k >> 2) * kXBlk + (k & 3) * 32) / 16,
+                        mma_ss(tmem + buf * 128 + 64, x2 + xo + ((k >> 2) * kXBlk + (k & 3) * 32) / 16,
                                y2 + yo + ((k >> 2) * kYBlk + (k & 3) * 32) / 16, id, k > 0);
                     mma_commit(pipe.bar(kBarST + (c & 1)));
                     if (i + 1 == it.steps) mma_commit(pipe.bar(kBarXfree + (n & 1)));
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
             for (int i = 0; i < it.steps; ++i, ++c) {
                 const uint64_t yo = w.st * (L::kY / 16);
                 const int k16 = DQ ? (step_keys(it, i) + 15) / 16 : kRows / 16;
-                const uint32_t p = tmem + 128 + (c & 1) * 32, ds = tmem + 192 + (c & 1) * 32;
+                const uint32_t p = tmem + kP + (c & 1) * 32, ds = tmem + kDs + (c & 1) * 32;
                 if (!(ok = pipe.wait_warp(kBarP + (c & 1), (c >> 1) & 1))) break;
                 if (!(ok = pipe.wait_warp(kBarYfull + w.st, w.ph))) break;  // (P came of it)
                 if (i == 0 && n > 0 && !(ok = pipe.wait_warp(kBarOfree, (n - 1) & 1))) break;
@@ -338,12 +340,12 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
                     if (DQ) {
 #pragma unroll
                         for (int k = 0; k < kRows / 16; ++k)
-                            if (k < k16) mma_ts(tmem + 256, ds + k * 8, y1 + yo + k * (2048 / 16), id, i > 0 || k > 0);
+                            if (k < k16) mma_ts(tmem + kAcc, ds + k * 8, y1 + yo + k * (2048 / 16), id, i > 0 || k > 0);
                     } else {
 #pragma unroll
-                        for (int k = 0; k < kRows / 16; ++k) mma_ts(tmem + 256, p + k * 8, y2 + yo + k * (2048 / 16), id, i > 0 || k > 0);
+                        for (int k = 0; k < kRows / 16; ++k) mma_ts(tmem + kAcc, p + k * 8, y2 + yo + k * (2048 / 16), id, i > 0 || k > 0);
 #pragma unroll
-                        for (int k = 0; k < kRows / 16; ++k) mma_ts(tmem + 384, ds + k * 8, y1 + yo + k * (2048 / 16), id, i > 0 || k > 0);
+                        for (int k = 0; k < kRows / 16; ++k) mma_ts(tmem + kAcc + 128, ds + k * 8, y1 + yo + k * (2048 / 16), id, i > 0 || k > 0);
                     }
                     mma_commit(pipe.bar(kBarSum + (c & 1)));
                     mma_commit(pipe.bar(kBarYfree + w.st));
@@ -362,8 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
         // ---------------------------------------------------------------- rows of X
         const int w = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-        const uint32_t s_col = lanes + half * 32, t_col = s_col + 64;
-        const uint32_t p_col = lanes + 128 + w * 32 + half * 16, d_col = p_col + 64;
+        const uint32_t s_col = lanes + (DQ ? w * 128 : 0) + half * 32, t_col = s_col + 64;
+        const uint32_t p_col = lanes + kP + w * 32 + half * 16, d_col = lanes + kDs + w * 32 + half * 16;
         const float scale2 = a.scale * kLog2e, lowest = scale2 > 0.f ? -INFINITY : INFINITY;  // its logit is -inf
         const float2 scale22 = make_float2(scale2, scale2);
         const int off = a.N - a.Lq;
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
-                pipe.arrive_if(lane == 0, kBarSTfree);
+                pipe.arrive_if(lane == 0, kBarSTfree + (DQ ? w : 0));
                 if (!full) {
 #pragma unroll
                     for (int q = 0; q < 32; ++q) {
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
                 tc_fence_after();
             }
             const float fac = DQ || half ? a.scale : 1.f;
-            const uint32_t o_col = lanes + 256 + (DQ ? half * (D / 2) : half * 128);
+            const uint32_t o_col = lanes + kAcc + (DQ ? half * (D / 2) : half * 128);
             const int cols = DQ ? D / 2 : D;
             const bool part = !DQ && it.nseg > 1;  // float32 partial rows
             const MutView &v = DQ ? a.dQ : half ? a.dK : a.dV;
@@ -558,8 +560,6 @@ bool launch_sink_backward_tc(hils_dtype dt, int d, const SinkBwdArgs &a, cudaStr
     const int64_t qi = (int64_t)a.B * (a.H / q.P) * q.tiles;
     k.items = (int)sink_key_items(a);
     const int64_t ki = (int64_t)k.items * a.B * Hk;
-    const int64_t window_rows = (int64_t)a.W + kM < a.Lq ? (int64_t)a.W + kM : a.Lq;
-    if (window_rows / a.seg_w >= a.Lq / a.seg_s && a.nblk > a.nsink) k.first = a.nsink * a.seg_s;
     if (qi > 0x7fffffffll - 1024 || ki > 0x7fffffffll - 1024) return false;
     q.total = (int)qi;
     k.total = (int)ki;
