@@ -10,16 +10,21 @@ namespace {
 // Order of the accumulated weights: larger float, larger key; -0 equals +0, NaN is lowest.
 __device__ __forceinline__ unsigned weight_key(float f) { return f != f ? 0u : ordered_key(f + 0.f); }
 
-// One CTA per (b, head): the m-th largest key bit by bit, each bit a count over keys held in
-// registers (32 counts of up to 32 keys a thread; a histogram's shared atomics collide on the
-// few exponents that the weights have, and took 70 us of this kernel's 77 at 64 x 32K). It
-// ends early once exactly m keys reach the trial. Warp w holds the keys of R * 32 consecutive
-// slots; those behind THR * R slots are read again for each bit.
+// One CTA per (b, head): the m-th largest key by histograms of 2048 bins over the keys' range,
+// then over the bin that holds it (three at most), with the keys in registers. It ends early
+// once a bin's lower border leaves exactly m keys. Equal bins within a warp are counted by one
+// lane: many weights are zero, and their atomics on one address took 70 us of the 77 at 64 x 32K
+// slots. Warp w holds the keys of R * 32 consecutive slots; those behind THR * R slots are read
+// again for each histogram.
+constexpr int kBins = 2048;
+
 template <int THR, int R>
 __global__ void __launch_bounds__(THR) evict_select_kernel(EvictArgs a) {
-    constexpr int kW = THR / 32;
+    constexpr int kW = THR / 32, kPer = kBins / THR;
+    __shared__ int hist[kBins];
     __shared__ int sh[2][kW];
     __shared__ int2 base[kW];
+    __shared__ int found[3];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int64_t bk = blockIdx.x;
     const int b = (int)(bk / a.Hk);
@@ -36,27 +41,85 @@ __global__ void __launch_bounds__(THR) evict_select_kernel(EvictArgs a) {
     if (m == 0) return;
     const int mid = m1 - m0, far = THR * R;  // slots [far, mid) of the middle stay in memory
     unsigned key[R];
+    unsigned low = 0xffffffffu, high = 0u;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int i = (warp * R + r) * 32 + lane;
         key[r] = i < mid ? weight_key(__ldg(acc + m0 + i)) : 0u;
     }
-    unsigned thr = 0u;  // the largest trial that at least m keys reach
-    bool exact = false; // exactly m do
-    for (int bit = 31; bit >= 0 && !exact; --bit) {
-        const unsigned trial = thr | (1u << bit);
-        int c = 0;
 #pragma unroll
-        for (int r = 0; r < R; ++r) c += key[r] >= trial;
-        for (int i = far + tid; i < mid; i += THR) c += weight_key(__ldg(acc + m0 + i)) >= trial;
-        c = __reduce_add_sync(kFull, c);
-        if (lane == 0) sh[bit & 1][warp] = c;
+    for (int r = 0; r < R; ++r) {
+        const bool in = (warp * R + r) * 32 + lane < mid;
+        low = min(low, in ? key[r] : 0xffffffffu);
+        high = max(high, key[r]);
+    }
+    for (int i = far + tid; i < mid; i += THR) {
+        const unsigned k = weight_key(__ldg(acc + m0 + i));
+        low = min(low, k);
+        high = max(high, k);
+    }
+    low = __reduce_min_sync(kFull, low);
+    high = __reduce_max_sync(kFull, high);
+    if (lane == 0) {
+        sh[0][warp] = (int)low;
+        sh[1][warp] = (int)high;
+    }
+    __syncthreads();
+    low = __reduce_min_sync(kFull, lane < kW ? (unsigned)sh[0][lane] : 0xffffffffu);
+    high = __reduce_max_sync(kFull, lane < kW ? (unsigned)sh[1][lane] : 0u);
+    unsigned thr = low;  // the keys of the bins: [thr, high]
+    int shift = high > low ? max(0, 32 - __clz(high - low) - 11) : 0, left = m;
+    bool exact = false;  // exactly the keys from thr on are kept
+    auto count = [&](bool in, unsigned k) {
+        const unsigned bin = (k - thr) >> shift;
+        in = in && k >= thr && k <= high;
+        const unsigned act = __ballot_sync(kFull, in);
+        if (act == 0u) return;
+        const unsigned first = __shfl_sync(kFull, bin, __ffs(act) - 1);
+        const unsigned same = __ballot_sync(kFull, in && bin == first);
+        if (lane == __ffs(act) - 1) atomicAdd(&hist[first], __popc(same));
+        else if (in && bin != first) atomicAdd(&hist[bin], 1);
+    };
+    while (true) {
+        for (int i = tid; i < kBins; i += THR) hist[i] = 0;
         __syncthreads();
-        c = __reduce_add_sync(kFull, lane < kW ? sh[bit & 1][lane] : 0);
-        if (c >= m) {
-            thr = trial;
-            exact = c == m;
+#pragma unroll
+        for (int r = 0; r < R; ++r) count((warp * R + r) * 32 + lane < mid, key[r]);
+        for (int i0 = far; i0 < mid; i0 += THR) {
+            const int i = i0 + tid;
+            count(i < mid, i < mid ? weight_key(__ldg(acc + m0 + i)) : 0u);
         }
+        __syncthreads();
+        // thread t has bins [kBins - kPer (t + 1), kBins - kPer t): sums from the top
+        const int top = kBins - kPer * tid;
+        int mine = 0;
+#pragma unroll
+        for (int q = 1; q <= kPer; ++q) mine += hist[top - q];
+        int sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(kFull, sum, o);
+            if (lane >= o) sum += x;
+        }
+        if (lane == 31) sh[0][warp] = sum;
+        __syncthreads();
+        const int before = __reduce_add_sync(kFull, lane < warp ? sh[0][lane] : 0);
+        int cum = before + sum - mine;  // in the bins above this thread's
+        if (cum < left && cum + mine >= left) {
+            int q = 1;
+            while (cum + hist[top - q] < left) cum += hist[top - q++];
+            found[0] = top - q;
+            found[1] = cum;
+            found[2] = hist[top - q];
+        }
+        __syncthreads();
+        thr += (unsigned)found[0] << shift;
+        high = min(high, thr + ((1u << shift) - 1u));  // (thr + 2^shift - 1 does not wrap: thr <= the bin's keys)
+        left -= found[1];
+        exact = found[2] == left;
+        if (exact || shift == 0) break;
+        shift = max(0, shift - 11);
+        __syncthreads();  // hist and found are free again
     }
     // keys above thr are kept, and of those equal to it the first need (all of them if exact)
     auto kind = [&](int i, unsigned k) { return i >= mid ? 0 : k > thr || (exact && k == thr) ? 2 : k == thr ? 1 : 0; };
@@ -68,13 +131,8 @@ __global__ void __launch_bounds__(THR) evict_select_kernel(EvictArgs a) {
         mine.y += __popc(__ballot_sync(kFull, t == 1));
     }
     if (lane == 0) base[warp] = mine;
-    int c = 0;  // above, in all
-    for (int i = far + tid; i < mid; i += THR) c += kind(i, weight_key(__ldg(acc + m0 + i))) == 2;
-    c = __reduce_add_sync(kFull, c);
-    __syncthreads();  // (sh: every warp is behind its last read)
-    if (lane == 0) sh[0][warp] = c + mine.x;
     __syncthreads();
-    const int above = __reduce_add_sync(kFull, lane < kW ? sh[0][lane] : 0), need = m - above;
+    const int need = left;  // of the keys equal to thr
     int2 at = make_int2(0, 0), all = make_int2(0, 0);
     for (int w = 0; w < kW; ++w) {
         const int2 x = base[w];
@@ -122,7 +180,7 @@ __global__ void __launch_bounds__(256) evict_gather_kernel(EvictArgs a, int esiz
         for (int b = threadIdx.x; b < a.B; b += 256) a.len_out[b] = min(min(max(a.cache_len[b], 0), a.T), a.budget);
     if (r0 >= rows) return;
     const int my = lane < kRows && r0 + lane < rows ? a.idx[r0 + lane] : -1;
-    if (my >= 0) {
+    if ((unsigned)my < (unsigned)a.T) {
         const int64_t bk = (r0 + lane) / a.budget;
         a.acc_out[r0 + lane] = __ldg(a.acc + bk * a.T + my);
     }
@@ -146,7 +204,7 @@ __global__ void __launch_bounds__(256) evict_gather_kernel(EvictArgs a, int esiz
         const View &s = val ? a.V : a.K;
         const MutView &d = val ? a.Vout : a.Kout;
         to[i] = nullptr;
-        if (j >= 0) {
+        if ((unsigned)j < (unsigned)a.T) {
             const int x = (val ? u - U / 2 : u) * 16;
             v[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const char *>(s.ptr) +
                                                          (b * s.sb + h * s.sh + (int64_t)j * s.st) * esize + x));

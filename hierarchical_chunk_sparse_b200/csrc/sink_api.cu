@@ -59,7 +59,7 @@ size_t key_ws(const hils_params *p, int Lq, int N, int A, int per_key, SinkBwdAr
     a->B = p->B;
     a->H = p->H;
     a->G = groups(p);
-    sink_key_plan(p->B, p->H / a->G, a->G, Lq, N, clip(p->W, N), clip(A, N),
+    sink_key_plan(p->dtype, p->B, p->H / a->G, a->G, Lq, N, clip(p->W, N), clip(A, N),
                   per_key == 1 && p->dtype == HILS_BF16 ? 2 * kSinkKeys : kSinkKeys, a);
     return sink_align(sink_key_part_floats(*a, per_key) * 4);
 }
@@ -108,7 +108,7 @@ size_t sink_ws_bytes(const hils_params *p, int call, int rows, int other) {
     SinkBwdArgs a{};
     switch (call) {
     case HILS_CALL_SINK_PREFILL: {
-        const int s = sink_prefill_splits(p->B, p->H, groups(p), rows, prefill_keys(p, other, rows), device_sm_count());
+        const int s = sink_prefill_splits(p->dtype, p->B, p->H, groups(p), rows, prefill_keys(p, other, rows), device_sm_count());
         return kSinkStatusBytes + (s > 1 ? sink_part_bytes(all, s, p->d) : 0);
     }
     case HILS_CALL_SINK_BACKWARD:
@@ -159,7 +159,7 @@ int hils_sink_prefill(const hils_params *p, int A, hils_ctensor Q, int Lq, hils_
     Carve ws{static_cast<uint8_t *>(workspace)};
     a.status = ws.take<uint32_t>(kSinkStatusBytes / 4);
     const int64_t keys = prefill_keys(p, A, Lq);
-    a.splits = sink_prefill_splits(a.B, a.H, a.G, Lq, keys < N ? keys : N, device_sm_count());
+    a.splits = sink_prefill_splits(p->dtype, a.B, a.H, a.G, Lq, keys < N ? keys : N, device_sm_count());
     if (a.splits > 1) {
         a.slots = a.splits;
         a.part_o = ws.take<float>((size_t)rows * a.slots * p->d);

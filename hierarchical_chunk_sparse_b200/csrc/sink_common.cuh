@@ -59,13 +59,16 @@ inline int sink_pack(int G) {
     while (P < 8 && G % (2 * P) == 0) P *= 2;
     return P;
 }
-// Key splits of a prefill call whose 256-row tiles alone would leave most SMs idle. `keys`:
-// the longest key range of a row tile (for the workspace's size, a bound of it).
-inline int sink_prefill_splits(int B, int H, int G, int Lq, int64_t keys, int sms) {
-    const int P = sink_pack(G);
-    const int64_t tiles = (int64_t)B * (H / P) * (((int64_t)Lq * P + 255) / 256);
-    const int64_t fill = tiles > 0 ? sms / tiles : 1;
-    const int64_t most = keys / 512;  // four 128-key tiles or more each
+// Key splits of a prefill call whose row tiles alone would leave most SMs idle. `keys`: the
+// longest key range of a row tile (for the workspace's size, a bound of it). bf16: 256-row
+// tiles, one an SM, 512 keys or more each; float32: 64-row tiles, three an SM, and a 64-key
+// tile costs 7 us there, so that each may be a split (47 -> 16 us at 12 heads, 333 rows, W 200).
+inline int sink_prefill_splits(hils_dtype dt, int B, int H, int G, int Lq, int64_t keys, int sms) {
+    const bool f32 = dt == HILS_F32;
+    const int P = f32 ? 1 : sink_pack(G), rows = f32 ? 64 : 256;
+    const int64_t tiles = (int64_t)B * (H / P) * (((int64_t)Lq * P + rows - 1) / rows);
+    const int64_t fill = tiles > 0 ? (f32 ? 3 : 1) * sms / tiles : 1;
+    const int64_t most = f32 ? (keys + 63) / 64 : keys / 512;
     const int64_t s = fill < most ? fill : most;
     return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
@@ -141,16 +144,18 @@ __host__ __device__ inline void sink_rows_of_block(const SinkBwdArgs &a, int j0,
     if (*i1 < *i0) *i1 = *i0;
 }
 
-// The division of the key blocks: enough items for every SM, at least eight steps each.
-inline void sink_key_plan(int B, int Hk, int G, int Lq, int N, int W, int A, int keys, SinkBwdArgs *a) {
+// The division of the key blocks: enough items for every SM, at least eight steps each
+// (float32: one 64-row tile, which costs more than its share of the reduction).
+inline void sink_key_plan(hils_dtype dt, int B, int Hk, int G, int Lq, int N, int W, int A, int keys, SinkBwdArgs *a) {
+    const int step = dt == HILS_F32 ? 64 : kSinkRows, least = dt == HILS_F32 ? 1 : 8;
     a->keys = keys;
     a->nblk = (N + keys - 1) / keys;
     a->nsink = (A + keys - 1) / keys;
     if (a->nsink > a->nblk) a->nsink = a->nblk;
     auto segments = [&](int blocks, int64_t rows) {
-        const int64_t steps = (int64_t)G * ((rows + kSinkRows - 1) / kSinkRows);
+        const int64_t steps = (int64_t)G * ((rows + step - 1) / step);
         const int64_t fill = 592 / ((int64_t)B * Hk * (blocks > 0 ? blocks : 1));
-        int64_t s = steps / 8 < fill ? steps / 8 : fill;
+        int64_t s = steps / least < fill ? steps / least : fill;
         return (int)(s < 1 ? 1 : s);
     };
     a->seg_s = segments(a->nsink, Lq);

@@ -482,13 +482,13 @@ __global__ void __launch_bounds__(kWarps * 32, 8 / kWarps) sink_decode_kernel(Si
     pdl_wait();  // the prefix kernel's partial results are complete when this grid is
 }
 
-// One warp per row (b, h): the partial results of the prefix kernel's slots and of the decode
+// W warps per row (b, h; 4 / W rows a CTA): the partial results of the prefix kernel's slots and of the decode
 // CTAs' segments, in that order; weights exp(lse_s - max). Rows that one CTA has finished are left.
-template <typename T, int D>
+template <typename T, int D, int W>
 __global__ void __launch_bounds__(128) sink_decode_combine_kernel(SinkDecodeArgs a, int ctas) {
     constexpr int KT = tile_keys<T>(), kE = D / 32;
-    const int Hk = a.H / a.G, lane = threadIdx.x % 32;
-    const int64_t rows = (int64_t)a.B * a.H, row = min((int64_t)blockIdx.x * 4 + threadIdx.x / 32, rows - 1);
+    const int Hk = a.H / a.G, lane = threadIdx.x % 32, part = threadIdx.x / 32 % W;
+    const int64_t rows = (int64_t)a.B * a.H, at = (int64_t)blockIdx.x * (4 / W) + threadIdx.x / 32 / W, row = min(at, rows - 1);
     const int b = (int)divide(row, a.H), h = (int)(row - (int64_t)b * a.H), hk = h / a.G, g = h % a.G;
     int64_t before = 0, total = 0;
     for (int i = lane; i < a.B; i += 32) {
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(128) sink_decode_combine_kernel(SinkDecodeArgs
     const int64_t c0 = cta_of(first), seg0 = c0 + (int64_t)b * Hk + hk;
     const int ns = (int)(cta_of(first + tiles - 1) - c0) + 1, all = a.slots + ns;
     pdl_wait();  // every thread: this grid must not be over before the one that it follows
-    if (all == 1 || (int64_t)blockIdx.x * 4 + threadIdx.x / 32 >= rows) return;
+    if (all == 1 || at >= rows) return;
     auto lse_of = [&](int s) {
         return s < a.slots ? a.part_lse[row * a.slots + s] : a.seg_lse[(seg0 + (s - a.slots)) * a.G + g];
     };
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(128) sink_decode_combine_kernel(SinkDecodeArgs
         z += wl;
         const int m = min(32, all - s0);
 #pragma unroll 8
-        for (int i = 0; i < m; ++i) {
+        for (int i = part; i < m; i += W) {
             const float w = __shfl_sync(kFull, wl, i);
             const float *src = row_of(s0 + i);
 #pragma unroll
@@ -535,6 +535,17 @@ __global__ void __launch_bounds__(128) sink_decode_combine_kernel(SinkDecodeArgs
         }
     }
     z = warp_sum(z);
+    if (W > 1) {  // (the CTA's rows are one)
+        __shared__ float rest[W][D];
+#pragma unroll
+        for (int e = 0; e < kE; ++e) rest[part][lane * kE + e] = r[e];
+        __syncthreads();
+        if (part) return;
+#pragma unroll
+        for (int w = 1; w < W; ++w)
+#pragma unroll
+            for (int e = 0; e < kE; ++e) r[e] += rest[w][lane * kE + e];
+    }
     const float inv = z > 0.f ? 1.f / z : 0.f;
     T *dst = static_cast<T *>(a.O.ptr) + b * a.O.sb + h * a.O.sh + lane * kE;
 #pragma unroll
@@ -645,7 +656,10 @@ hils_status decode(const SinkDecodeArgs &a, int ctas, cudaStream_t s) {
     }
     if (st != HILS_OK) return st;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((int64_t)a.B * a.H + 3) / 4));
+    // with a prefix's slots, or few rows for many CTAs, there is much to join
+    const int64_t rows = (int64_t)a.B * a.H;
+    const bool many = a.slots + ctas * (int64_t)a.G / rows >= 8;
+    cfg.gridDim = dim3((unsigned)(many ? rows : (rows + 3) / 4));
     cfg.blockDim = dim3(128);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -653,7 +667,8 @@ hils_status decode(const SinkDecodeArgs &a, int ctas, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return record_cuda_error(cudaLaunchKernelEx(&cfg, sink_decode_combine_kernel<T, D>, a, ctas));
+    return record_cuda_error(many ? cudaLaunchKernelEx(&cfg, sink_decode_combine_kernel<T, D, 4>, a, ctas)
+                                  : cudaLaunchKernelEx(&cfg, sink_decode_combine_kernel<T, D, 1>, a, ctas));
 }
 }  // namespace
 

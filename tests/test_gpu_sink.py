@@ -328,6 +328,37 @@ def test_evict(cuda_device, B, Hk, d, T, budget, W, A, lens, dtype):
             assert (Ko[b, h, m:] == 3.0).all() and (Vo[b, h, m:] == 3.0).all() and (ao[b, h, m:] == 3.0).all()
 
 
+@pytest.mark.parametrize("T,budget,W,A", [(33, 20, 3, 1), (2048, 700, 30, 4), (2300, 1000, 0, 0), (16384, 5000, 512, 4),
+                                          (16500, 16000, 100, 0), (40000, 9000, 64, 4)])
+@pytest.mark.parametrize("spread", [1.5, 1e-4])
+def test_evict_by_distinct_weights(cuda_device, T, budget, W, A, spread):
+    """Weights without ties but for a fifth of zeros, close together or far apart: several
+    histograms deep, and (40000) with slots beyond a CTA's registers."""
+    B, Hk, d = 2, 2, 64
+    g = torch.Generator().manual_seed(T)
+    acc = torch.exp(spread * torch.randn(B, Hk, T, generator=g) - 2.0)
+    acc[torch.rand(acc.shape, generator=g) < 0.2] = 0.0
+    acc = acc.to(cuda_device)
+    K = torch.randn(B, Hk, T, d, generator=g).to(BF).to(cuda_device)
+    lens = [T, T - T // 9]
+    n = torch.tensor(lens, dtype=torch.int32, device=cuda_device)
+    p = params(B, Hk, Hk, d, W, BF)
+    Ko, Vo = (torch.zeros(B, Hk, budget, d, dtype=BF, device=cuda_device) for _ in range(2))
+    ao = torch.zeros(B, Hk, budget, device=cuda_device)
+    idx = torch.full((B, Hk, budget), -7, dtype=torch.int32, device=cuda_device)
+    out = torch.zeros(B, dtype=torch.int32, device=cuda_device)
+    ws = hils.alloc_workspace(p, hils.HILS_CALL_CACHE_EVICT, T, budget, device=cuda_device)
+    hils.hils_cache_evict(p, A, budget, K, K, acc, n, Ko, Vo, ao, idx, out, workspace=ws)
+    rows, new = ref.evict(acc, torch.tensor(lens), budget, W, A)
+    assert out.tolist() == new
+    for b in range(B):
+        for h in range(Hk):
+            m = len(rows[b][h])
+            assert idx[b, h].tolist() == rows[b][h] + [-1] * (budget - m), (b, h)
+            at = torch.tensor(rows[b][h], dtype=torch.long, device=cuda_device)
+            assert torch.equal(Ko[b, h, :m], K[b, h, at]) and torch.equal(ao[b, h, :m], acc[b, h, at])
+
+
 def test_prompt_then_evict_then_decode(cuda_device):
     """The calls as a server makes them: a prompt in two pieces, its weights, the cache cut,
     then tokens decoded on the cut cache with their weights added, and a second cut."""
