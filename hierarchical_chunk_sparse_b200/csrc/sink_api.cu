@@ -352,6 +352,7 @@ int hils_prefix_decode(const hils_params *p, hils_ctensor Q, hils_ctensor Kp, hi
         s.P = P;
         s.whole = (int64_t)P + T <= kSinkWholeRow;
     } else {
+        s.whole = T <= kSinkWholeRow;
         HILS_TRY(forward(p, a, stream));
     }
     return launch_sink_decode(p->dtype, p->d, s, plan.ctas, stream);

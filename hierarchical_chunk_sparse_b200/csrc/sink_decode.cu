@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kWarps * 32, 8 / kWarps) sink_decode_kernel(Si
             rows.finish(sm + warp * kMaxGroupHeads, sl + warp * kMaxGroupHeads, so + warp * a.G * D, a.G);
             __syncthreads();
             const int64_t rowidx = (int64_t)cur.b * Hk + cur.hk;
-            const bool alone = a.slots == 0 && row0 >= t0 && row0 + cur.v.tiles <= t1;
+            const bool alone = a.slots == 0 && (a.whole || (row0 >= t0 && row0 + cur.v.tiles <= t1));
             for (int g = warp; g < a.G; g += kWarps) {
                 float mx = -INFINITY, z = 0.f, r[kE] = {};
 #pragma unroll
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kWarps * 32, 8 / kWarps) sink_decode_kernel(Si
                     for (int e = 0; e < kE; e += 2) store2(dst + e, r[e] * inv, r[e + 1] * inv);
                     if (lane == 0) a.lse[(int64_t)cur.b * a.H + h] = lse;
                 } else {
-                    const int64_t seg = (c + rowidx) * a.G + g;
+                    const int64_t seg = (a.whole ? rowidx : c + rowidx) * a.G + g;
 #pragma unroll
                     for (int e = 0; e < kE; e += 2) store2(a.seg_o + seg * D + lane * kE + e, r[e] * inv, r[e + 1] * inv);
                     if (lane == 0) a.seg_lse[seg] = lse;
@@ -504,8 +504,14 @@ __global__ void __launch_bounds__(128) sink_decode_combine_kernel(SinkDecodeArgs
     const int tiles = visible<KT>(a, b).tiles;
     const int64_t first = before + (int64_t)hk * tiles, n_cta = min((int64_t)ctas, total);
     auto cta_of = [&](int64_t tile) { return divide((tile + 1) * n_cta - 1, total); };
-    const int64_t c0 = cta_of(first), seg0 = c0 + (int64_t)b * Hk + hk;
-    const int ns = (int)(cta_of(first + tiles - 1) - c0) + 1, all = a.slots + ns;
+    int64_t seg0 = (int64_t)b * Hk + hk;
+    int ns = 1;
+    if (!a.whole) {
+        const int64_t c0 = cta_of(first);
+        ns = (int)(cta_of(first + tiles - 1) - c0) + 1;
+        seg0 += c0;
+    }
+    const int all = a.slots + ns;
     pdl_wait();  // every thread: this grid must not be over before the one that it follows
     if (all == 1 || at >= rows) return;
     auto lse_of = [&](int s) {
@@ -634,27 +640,24 @@ int sink_decode_ctas(hils_dtype dt, int B, int Hk, int64_t keys, int sms) {
 namespace {
 template <typename T, int D>
 hils_status decode(const SinkDecodeArgs &a, int ctas, cudaStream_t s) {
-    static KernelSetup setup, whole;
+    static KernelSetup setup, whole;  // (the latter: eight warps a CTA)
     hils_status st;
+    const void *k = a.whole ? (const void *)sink_decode_kernel<T, D, 8> : (const void *)sink_decode_kernel<T, D, 4>;
+    const int most = a.whole ? decode_smem<T, D, 8>(kMaxGroupHeads) : decode_smem<T, D, 4>(kMaxGroupHeads);
+    const int smem = a.whole ? decode_smem<T, D, 8>(a.G) : decode_smem<T, D, 4>(a.G), threads = a.whole ? 256 : 128;
+    st = kernel_setup(a.whole ? whole : setup, k, threads, most, nullptr);
+    if (st != HILS_OK) return st;
     if (a.whole) {
-        const auto k = sink_decode_kernel<T, D, 8>;
-        st = kernel_setup(whole, (const void *)k, 256, decode_smem<T, D, 8>(kMaxGroupHeads), nullptr);
-        if (st != HILS_OK) return st;
         const int64_t rows = (int64_t)a.B * (a.H / a.G), sms = device_sm_count();
-        k<<<(unsigned)(rows < sms ? rows : sms), 256, decode_smem<T, D, 8>(a.G), s>>>(a);
-        return record_cuda_error(cudaGetLastError());
+        ctas = (int)(rows < sms ? rows : sms);
     }
-    const auto k = sink_decode_kernel<T, D, 4>;
-    const int smem = decode_smem<T, D, 4>(a.G);
-    st = kernel_setup(setup, (const void *)k, 128, decode_smem<T, D, 4>(kMaxGroupHeads), nullptr);
-    if (st != HILS_OK) return st;
     if (a.slots) {  // it may begin while the prefix kernel ends
-        st = launch_dependent((const void *)k, dim3(ctas), dim3(128), smem, s, a);
+        st = launch_dependent(k, dim3(ctas), dim3(threads), smem, s, a);
     } else {
-        k<<<ctas, 128, smem, s>>>(a);
-        st = record_cuda_error(cudaGetLastError());
+        void *argv[] = {const_cast<SinkDecodeArgs *>(&a)};
+        st = record_cuda_error(cudaLaunchKernel(k, dim3(ctas), dim3(threads), argv, smem, s));
     }
-    if (st != HILS_OK) return st;
+    if (st != HILS_OK || (a.whole && a.slots == 0)) return st;
     cudaLaunchConfig_t cfg = {};
     // with a prefix's slots, or few rows for many CTAs, there is much to join
     const int64_t rows = (int64_t)a.B * a.H;

@@ -25,25 +25,34 @@ __device__ __forceinline__ float sum16(float v) {
     return v;
 }
 
-// Row r of a [64][D + 4] float tile from element pointer src (null: zeros).
-template <typename T, int D, typename F>
-__device__ __forceinline__ void load_tile(float *dst, F row_ptr) {
-    constexpr int kV = Vec<T>::kN, kU = D / kV;  // 16-byte units per row
-    for (int e = threadIdx.x; e < kT * kU; e += kThr) {
-        const int r = e / kU, u = e % kU;
-        const T *p = row_ptr(r);
-        float f[kV];
-        if (p) {
-            widen(__ldg(reinterpret_cast<const uint4 *>(p) + u), f, T());
-        } else {
+// Rows r of [64][D + 4] float tiles from element pointers row_ptr(r) (null: zeros): `fetch` has
+// all of a thread's loads in flight (one after another they took half of a tile's time), `put`
+// stores them.
+template <typename T, int D>
+struct TileLoad {
+    static constexpr int kV = Vec<T>::kN, kU = D / kV, kN = kT * kU / kThr;  // 16-byte units of a row, of a thread
+    uint4 v[kN];
+    template <typename F>
+    __device__ __forceinline__ void fetch(F row_ptr) {
 #pragma unroll
-            for (int i = 0; i < kV; ++i) f[i] = 0.f;
+        for (int i = 0; i < kN; ++i) {
+            const int e = threadIdx.x + i * kThr;
+            const T *p = row_ptr(e / kU);
+            v[i] = p ? __ldg(reinterpret_cast<const uint4 *>(p) + e % kU) : make_uint4(0u, 0u, 0u, 0u);
         }
-        float *d = dst + r * (D + 4) + u * kV;
-#pragma unroll
-        for (int i = 0; i < kV; i += 4) *reinterpret_cast<float4 *>(d + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
     }
-}
+    __device__ __forceinline__ void put(float *dst) const {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int e = threadIdx.x + i * kThr;
+            float f[kV];
+            widen(v[i], f, T());
+            float *d = dst + (e / kU) * (D + 4) + (e % kU) * kV;
+#pragma unroll
+            for (int k = 0; k < kV; k += 4) *reinterpret_cast<float4 *>(d + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+        }
+    }
+};
 
 // acc[r][c] = X row (4 ty + r) . Y row (tx + 16 c) over D
 template <int D>
@@ -148,7 +157,8 @@ __global__ void __launch_bounds__(kThr) sink_fwd_kernel(SinkArgs a, int tiles) {
     const int nt = sp.ns + sp.nw;
     const int i0 = (int)((int64_t)nt * split / a.splits), i1 = (int)((int64_t)nt * (split + 1) / a.splits);
 
-    load_tile<T, D>(Qs, [&](int r) -> const T * {
+    TileLoad<T, D> first;
+    first.fetch([&](int r) -> const T * {
         const T *q = nullptr;
         int64_t place;
         return row(r, &q, &place) >= 0 ? q : nullptr;
@@ -171,9 +181,13 @@ __global__ void __launch_bounds__(kThr) sink_fwd_kernel(SinkArgs a, int tiles) {
         const bool sink = i < sp.ns;
         const int k0 = sink ? i * kT : sp.lo + (i - sp.ns) * kT;
         const int end = sink ? sp.sinks : sp.hi;
+        TileLoad<T, D> lk, lv;
+        lk.fetch([&](int r) -> const T * { return k0 + r < end ? Kb + (int64_t)(k0 + r) * a.K.st : nullptr; });
+        lv.fetch([&](int r) -> const T * { return k0 + r < end ? Vb + (int64_t)(k0 + r) * a.V.st : nullptr; });
         __syncthreads();
-        load_tile<T, D>(Ks, [&](int r) -> const T * { return k0 + r < end ? Kb + (int64_t)(k0 + r) * a.K.st : nullptr; });
-        load_tile<T, D>(Vs, [&](int r) -> const T * { return k0 + r < end ? Vb + (int64_t)(k0 + r) * a.V.st : nullptr; });
+        if (i == i0) first.put(Qs);
+        lk.put(Ks);
+        lv.put(Vs);
         __syncthreads();
         float s[4][4];
         dot_tile<D>(s, Qs, Ks, ty, tx);
@@ -313,13 +327,18 @@ __global__ void __launch_bounds__(kThr) sink_bwd_kernel(SinkBwdArgs a, int tiles
         s0 = (int)(steps * it.seg / it.nseg);
         s1 = (int)(steps * (it.seg + 1) / it.nseg);
     }
-    load_tile<T, D>(X1, [&](int r) -> const T * {
-        return r < nrows ? (MODE == kModeDq ? at(a.Q, b, h, r0 + r) : at(a.K, b, hk, r0 + r)) : nullptr;
-    });
-    if (kTwo)
-        load_tile<T, D>(X2, [&](int r) -> const T * {
-            return r < nrows ? (MODE == kModeDq ? at(a.dO, b, h, r0 + r) : at(a.V, b, hk, r0 + r)) : nullptr;
+    {
+        TileLoad<T, D> x1, x2;
+        x1.fetch([&](int r) -> const T * {
+            return r < nrows ? (MODE == kModeDq ? at(a.Q, b, h, r0 + r) : at(a.K, b, hk, r0 + r)) : nullptr;
         });
+        if (kTwo)
+            x2.fetch([&](int r) -> const T * {
+                return r < nrows ? (MODE == kModeDq ? at(a.dO, b, h, r0 + r) : at(a.V, b, hk, r0 + r)) : nullptr;
+            });
+        x1.put(X1);
+        if (kTwo) x2.put(X2);
+    }
     float o1[4][D / 16], o2[4][D / 16], w[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int r = 0; r < 4; ++r)
@@ -340,9 +359,12 @@ __global__ void __launch_bounds__(kThr) sink_bwd_kernel(SinkBwdArgs a, int tiles
             if (MODE == kModeDq) return k0 + r < end ? at(kv, b, hk, k0 + r) : nullptr;
             return q0 + r < ilim ? at(qv, b, hh, q0 + r) : nullptr;
         };
+        TileLoad<T, D> y1, y2;
+        y1.fetch([&](int r) { return y(a.K, a.Q, r); });
+        if (kTwo) y2.fetch([&](int r) { return y(a.V, a.dO, r); });
         __syncthreads();
-        load_tile<T, D>(Y1, [&](int r) { return y(a.K, a.Q, r); });
-        if (kTwo) load_tile<T, D>(Y2, [&](int r) { return y(a.V, a.dO, r); });
+        y1.put(Y1);
+        if (kTwo) y2.put(Y2);
         __syncthreads();
         float s[4][4], dp[4][4];
         dot_tile<D>(s, X1, Y1, ty, tx);
