@@ -154,6 +154,10 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+# The current stream's handle by device index (torch.cuda.current_stream takes 3 us for it).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _expect(call: str, name: str, t, shape, dtype=None) -> None:
     """Shape (and dtype) check of one argument against the parameters; raises before the
     C call, so that a mismatched tensor can never be read or written out of bounds."""
@@ -444,7 +448,7 @@ def _sink_call(call: str, p: Params, views, arrays, workspace, stream):
             with torch.cuda.device(dev):
                 rc = fn(p.c(), *args, ws, ws_bytes, _stream(stream))
         else:
-            rc = fn(p.c(), *args, ws, ws_bytes, torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream))
+            rc = fn(p.c(), *args, ws, ws_bytes, _raw_stream(dev) if stream is None and dev >= 0 else _stream(stream))
         if rc != 0:
             _check(call, rc)
 

@@ -225,17 +225,7 @@ hils_status select(const EvictArgs &a, cudaStream_t s) {
 template <int U>
 hils_status gather(const EvictArgs &a, int esize, cudaStream_t s) {
     const int64_t rows = (int64_t)a.B * a.Hk * a.budget, per = 8 * (256 / U), grid = rows > 0 ? (rows + per - 1) / per : 1;
-    if (grid > 0x7fffffffll) return HILS_ERR_UNSUPPORTED;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = rows > 0 ? 1 : 0;
-    return record_cuda_error(cudaLaunchKernelEx(&cfg, evict_gather_kernel<U>, a, esize));
+    return sink_launch(rows > 0, evict_gather_kernel<U>, grid, 256, 0, s, a, esize);
 }
 
 }  // namespace

@@ -372,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
         bool ok = true;
         int c = 0;
         Walk walk;
+        if (DQ) pdl_wait();  // D. (dK, dV: a dQ CTA on this SM ended only after that wait)
         for (int r = 0; ok; ++r) {
             const int j = item_of_round(r, cta, G);
             if (j >= f.total) break;
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
             int see0 = 0, see1 = 0;  // dK, dV: the queries that see the key, from the item's first on
             if (DQ) {
                 const int64_t place = ((int64_t)it.b * a.H + it.h + hrow) * a.Lq + i_q;
-                const float lse = have ? __ldg(a.lse + place) : -INFINITY, Dr = have ? __ldg(a.Dv + place) : 0.f;
+                const float lse = have ? __ldg(a.lse + place) : -INFINITY, Dr = have ? a.Dv[place] : 0.f;
                 nl.x = nl.y = lse == -INFINITY ? lse : -lse * kLog2e;
                 nd.x = nd.y = -Dr;
             } else {
@@ -526,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
             }
         }
     }
+    if (!DQ) pdl_wait();  // the grid is not over before dQ's
     tc_fence_before();
     __syncthreads();
     if (warp == kStWarp) {
@@ -543,8 +545,8 @@ hils_status run(const Args &f, const CUtensorMap *m, cudaStream_t s) {
     if (st != HILS_OK) return st;
     if (per_sm < 1) return HILS_ERR_CUDA;
     const int sms = device_sm_count();
-    k<<<f.total < sms ? f.total : sms, kThreads, Smem<D>::kBytes, s>>>(m[0], m[1], m[2], m[3], m[4], m[5], f);
-    return record_cuda_error(cudaGetLastError());
+    // dQ follows the kernel of D; dK, dV need only that one too, so that their CTAs begin as dQ's end
+    return sink_launch(true, k, f.total < sms ? f.total : sms, kThreads, Smem<D>::kBytes, s, m[0], m[1], m[2], m[3], m[4], m[5], f);
 }
 
 }  // namespace

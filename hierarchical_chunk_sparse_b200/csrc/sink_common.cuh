@@ -13,6 +13,26 @@
 
 namespace hils {
 
+// Launches a kernel; `early`: it may be scheduled while the kernel before it on the stream ends,
+// and calls pdl_wait() before it touches what that one writes. Every thread that writes, and one
+// of each CTA at least, waits: a grid is then never over before the one that it follows.
+template <typename... P, typename... A>
+hils_status sink_launch(bool early, void (*kernel)(P...), int64_t grid, int threads, int smem, cudaStream_t s, const A &...args) {
+    if (grid <= 0) return HILS_OK;
+    if (grid > 0x7fffffffll) return HILS_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return record_cuda_error(cudaLaunchKernelEx(&cfg, kernel, args...));
+}
+
 // ------------------------------------------------------------------ forward
 
 // One call's rows over one key range. Prefill: row (b, h, i) at position N - Lq + i. A

@@ -564,6 +564,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(256) sink_combine_kernel(SinkCombineArgs a) {
     const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
+    pdl_wait();
     if (row >= a.rows) return;
     const float *lse = a.part_lse + row * a.slots;
     float mx = -INFINITY;
@@ -651,27 +652,14 @@ hils_status decode(const SinkDecodeArgs &a, int ctas, cudaStream_t s) {
         const int64_t rows = (int64_t)a.B * (a.H / a.G), sms = device_sm_count();
         ctas = (int)(rows < sms ? rows : sms);
     }
-    if (a.slots) {  // it may begin while the prefix kernel ends
-        st = launch_dependent(k, dim3(ctas), dim3(threads), smem, s, a);
-    } else {
-        void *argv[] = {const_cast<SinkDecodeArgs *>(&a)};
-        st = record_cuda_error(cudaLaunchKernel(k, dim3(ctas), dim3(threads), argv, smem, s));
-    }
+    // after a prefix kernel: it may begin while that one ends
+    st = a.whole ? sink_launch(a.slots > 0, sink_decode_kernel<T, D, 8>, ctas, threads, smem, s, a)
+                 : sink_launch(a.slots > 0, sink_decode_kernel<T, D, 4>, ctas, threads, smem, s, a);
     if (st != HILS_OK || (a.whole && a.slots == 0)) return st;
-    cudaLaunchConfig_t cfg = {};
     // with a prefix's slots, or few rows for many CTAs, there is much to join
     const int64_t rows = (int64_t)a.B * a.H;
-    const bool many = a.slots + ctas * (int64_t)a.G / rows >= 8;
-    cfg.gridDim = dim3((unsigned)(many ? rows : (rows + 3) / 4));
-    cfg.blockDim = dim3(128);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return record_cuda_error(many ? cudaLaunchKernelEx(&cfg, sink_decode_combine_kernel<T, D, 4>, a, ctas)
-                                  : cudaLaunchKernelEx(&cfg, sink_decode_combine_kernel<T, D, 1>, a, ctas));
+    return a.slots + ctas * (int64_t)a.G / rows >= 8 ? sink_launch(true, sink_decode_combine_kernel<T, D, 4>, rows, 128, 0, s, a, ctas)
+                                                     : sink_launch(true, sink_decode_combine_kernel<T, D, 1>, (rows + 3) / 4, 128, 0, s, a, ctas);
 }
 }  // namespace
 
@@ -683,33 +671,18 @@ hils_status launch_sink_decode(hils_dtype dt, int d, const SinkDecodeArgs &a, in
 
 hils_status launch_sink_combine(hils_dtype dt, int d, const SinkCombineArgs &a, cudaStream_t s) {
     const int64_t grid = (a.rows + 7) / 8;
-    if (grid == 0) return HILS_OK;
-    if (dt == HILS_BF16) {
-        if (d == 64) sink_combine_kernel<bf16, 64><<<(unsigned)grid, 256, 0, s>>>(a);
-        else sink_combine_kernel<bf16, 128><<<(unsigned)grid, 256, 0, s>>>(a);
-    } else {
-        if (d == 64) sink_combine_kernel<float, 64><<<(unsigned)grid, 256, 0, s>>>(a);
-        else sink_combine_kernel<float, 128><<<(unsigned)grid, 256, 0, s>>>(a);
-    }
-    return record_cuda_error(cudaGetLastError());
+    if (dt == HILS_BF16)
+        return d == 64 ? sink_launch(true, sink_combine_kernel<bf16, 64>, grid, 256, 0, s, a)
+                       : sink_launch(true, sink_combine_kernel<bf16, 128>, grid, 256, 0, s, a);
+    return d == 64 ? sink_launch(true, sink_combine_kernel<float, 64>, grid, 256, 0, s, a)
+                   : sink_launch(true, sink_combine_kernel<float, 128>, grid, 256, 0, s, a);
 }
 
 hils_status launch_sink_decode_acc(const SinkDecodeArgs &a, const float *lse, const float *acc, float *acc_out,
                                    cudaStream_t s) {
     const int chunks = (int)((a.logit_stride + 256 * kAcc - 1) / (256 * kAcc));
     const int64_t grid = (int64_t)a.B * (a.H / a.G) * chunks;
-    if (grid == 0) return HILS_OK;
-    if (grid > 0x7fffffffll) return HILS_ERR_UNSUPPORTED;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return record_cuda_error(cudaLaunchKernelEx(&cfg, sink_acc_kernel, a, lse, acc, acc_out, chunks));
+    return sink_launch(true, sink_acc_kernel, grid, 256, 0, s, a, lse, acc, acc_out, chunks);
 }
 
 }  // namespace hils

@@ -626,8 +626,7 @@ hils_status run(const FwdTc &f, const CUtensorMap (&m)[5], cudaStream_t s) {
     if (st != HILS_OK) return st;
     if (per_sm < 1) return HILS_ERR_CUDA;
     const int sms = device_sm_count();
-    k<<<f.items < sms ? f.items : sms, kThreads, Smem<D, PREFIX>::kBytes, s>>>(m[0], m[1], m[2], m[3], m[4], f);
-    return record_cuda_error(cudaGetLastError());
+    return sink_launch(false, k, f.items < sms ? f.items : sms, kThreads, Smem<D, PREFIX>::kBytes, s, m[0], m[1], m[2], m[3], m[4], f);
 }
 
 }  // namespace

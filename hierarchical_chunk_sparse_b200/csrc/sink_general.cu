@@ -300,6 +300,7 @@ __global__ void __launch_bounds__(kThr) sink_bwd_kernel(SinkBwdArgs a, int tiles
     SinkSpan sp{};
     SinkItem it{};
     int xb = 0;
+    if (MODE != kModeWeights) pdl_wait();  // Dv; and dK, dV's grid must not be over before dQ's
     if (MODE == kModeDq) {
         const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
         b = bh / a.H;
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(kThr) sink_bwd_kernel(SinkBwdArgs a, int tiles
                 const float L = in ? __ldg(a.lse + q) : -INFINITY;
                 const float p = in && L != -INFINITY ? exp2f(s[r][c] * scale2 - L * kLog2e) : 0.f;
                 if (kTwo) {
-                    const float ds = in ? a.scale * p * (dp[r][c] - __ldg(a.Dv + q)) : 0.f;
+                    const float ds = in ? a.scale * p * (dp[r][c] - a.Dv[q]) : 0.f;
                     if (MODE == kModeDkv) Ps[rr * kPS + cc] = p;
                     Ss[rr * kPS + cc] = ds;
                 } else {
@@ -439,6 +440,7 @@ __global__ void __launch_bounds__(256) sink_reduce_kernel(SinkBwdArgs a, int ite
     const int lane = threadIdx.x % 32, Hk = a.H / a.G;
     const int g_which = blockIdx.x & 1;
     const int64_t g = WEIGHTS ? (int64_t)blockIdx.x * 256 + threadIdx.x : (int64_t)(blockIdx.x / 2) * 8 + threadIdx.x / 32;
+    pdl_wait();
     if (g >= (int64_t)a.B * Hk * keys) return;
     const int64_t xb = g / keys;
     const int j = (int)(g - xb * keys);
@@ -475,14 +477,12 @@ __global__ void __launch_bounds__(256) sink_reduce_kernel(SinkBwdArgs a, int ite
     for (int e = 0; e < kE; e += 2) store2(dst + e, s[e], s[e + 1]);
 }
 
-template <typename K>
-hils_status run(KernelSetup &setup, K kernel, int64_t grid, int threads, int smem, cudaStream_t s, auto... args) {
+template <typename K, typename... A>
+hils_status run(KernelSetup &setup, bool early, K kernel, int64_t grid, int threads, int smem, cudaStream_t s, const A &...args) {
     if (grid <= 0) return HILS_OK;
-    if (grid > 0x7fffffffll) return HILS_ERR_UNSUPPORTED;
     const hils_status st = kernel_setup(setup, (const void *)kernel, threads, smem, nullptr);
     if (st != HILS_OK) return st;
-    kernel<<<(unsigned)grid, threads, smem, s>>>(args...);
-    return record_cuda_error(cudaGetLastError());
+    return sink_launch(early, kernel, grid, threads, smem, s, args...);
 }
 
 template <typename T, int D>
@@ -490,29 +490,29 @@ hils_status forward(const SinkArgs &a, cudaStream_t s) {
     static KernelSetup setup;
     const int tiles = a.prefix ? (a.B + kT / a.G - 1) / (kT / a.G) : (a.Lq + kT - 1) / kT;
     const int64_t grid = (int64_t)tiles * a.splits * (a.prefix ? a.H / a.G : (int64_t)a.B * a.H);
-    return run(setup, sink_fwd_kernel<T, D>, grid, kThr, fwd_smem<D>(), s, a, tiles);
+    return run(setup, false, sink_fwd_kernel<T, D>, grid, kThr, fwd_smem<D>(), s, a, tiles);
 }
 template <typename T, int D>
 hils_status dot(const SinkBwdArgs &a, float *Dv, cudaStream_t s) {
     static KernelSetup setup;
     constexpr int kRows = 8 * 4 * 32 * Vec<T>::kN / D;  // of a CTA
-    return run(setup, sink_dot_kernel<T, D>, ((int64_t)a.B * a.H * a.Lq + kRows - 1) / kRows, 256, 0, s, a, Dv);
+    return run(setup, false, sink_dot_kernel<T, D>, ((int64_t)a.B * a.H * a.Lq + kRows - 1) / kRows, 256, 0, s, a, Dv);
 }
 template <typename T, int D>
 hils_status backward(const SinkBwdArgs &a, cudaStream_t s) {
     static KernelSetup sq, sk;
     const int tiles = (a.Lq + kT - 1) / kT;
     const hils_status st =
-        run(sq, sink_bwd_kernel<kModeDq, T, D>, (int64_t)tiles * a.B * a.H, kThr, bwd_smem<D>(kModeDq), s, a, tiles);
+        run(sq, true, sink_bwd_kernel<kModeDq, T, D>, (int64_t)tiles * a.B * a.H, kThr, bwd_smem<D>(kModeDq), s, a, tiles);
     if (st != HILS_OK) return st;
     const int items = (int)sink_key_items(a);
-    return run(sk, sink_bwd_kernel<kModeDkv, T, D>, (int64_t)(a.keys / kT) * items * a.B * (a.H / a.G), kThr, bwd_smem<D>(kModeDkv), s, a, items);
+    return run(sk, true, sink_bwd_kernel<kModeDkv, T, D>, (int64_t)(a.keys / kT) * items * a.B * (a.H / a.G), kThr, bwd_smem<D>(kModeDkv), s, a, items);
 }
 template <typename T, int D>
 hils_status weights(const SinkBwdArgs &a, cudaStream_t s) {
     static KernelSetup setup;
     const int items = (int)sink_key_items(a);
-    return run(setup, sink_bwd_kernel<kModeWeights, T, D>, (int64_t)(a.keys / kT) * items * a.B * (a.H / a.G), kThr, bwd_smem<D>(kModeWeights), s,
+    return run(setup, false, sink_bwd_kernel<kModeWeights, T, D>, (int64_t)(a.keys / kT) * items * a.B * (a.H / a.G), kThr, bwd_smem<D>(kModeWeights), s,
                a, items);
 }
 template <typename T, int D>
@@ -523,8 +523,8 @@ hils_status reduce(const SinkBwdArgs &a, bool w, cudaStream_t s) {
     const int keys = a.seg_w > 1 || last > a.N ? a.N : (int)last;
     const int64_t rows = (int64_t)a.B * (a.H / a.G) * keys;
     const int items = (int)sink_key_items(a);
-    return w ? run(s0, sink_reduce_kernel<true, T, D>, (rows + 255) / 256, 256, 0, s, a, items, keys)
-             : run(s1, sink_reduce_kernel<false, T, D>, (rows + 7) / 8 * 2, 256, 0, s, a, items, keys);
+    return w ? run(s0, true, sink_reduce_kernel<true, T, D>, (rows + 255) / 256, 256, 0, s, a, items, keys)
+             : run(s1, true, sink_reduce_kernel<false, T, D>, (rows + 7) / 8 * 2, 256, 0, s, a, items, keys);
 }
 
 }  // namespace

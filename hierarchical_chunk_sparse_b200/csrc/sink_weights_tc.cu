@@ -393,8 +393,7 @@ hils_status run(const Args &f, const CUtensorMap (&m)[2], int total, cudaStream_
     if (st != HILS_OK) return st;
     if (per_sm < 1) return HILS_ERR_CUDA;
     const int sms = device_sm_count();
-    k<<<total < sms ? total : sms, kThreads, Smem<D>::kBytes, s>>>(m[0], m[1], f, total);
-    return record_cuda_error(cudaGetLastError());
+    return sink_launch(false, k, total < sms ? total : sms, kThreads, Smem<D>::kBytes, s, m[0], m[1], f, total);
 }
 
 }  // namespace
