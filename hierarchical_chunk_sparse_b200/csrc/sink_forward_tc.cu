@@ -13,7 +13,7 @@
 //   prefix   a tile is 128 / G sequences with the G heads of a group each, so that the
 //            prefix is read once for all of them; A and B are the same rows over two key
 //            ranges, which are joined later.
-// Warp roles (608 threads), hand-offs through mbarriers:
+// Warp roles (640 threads), hand-offs through mbarriers:
 //   warps 0-15   softmax: two warpgroups for each of A and B, which take its key tiles in turn;
 //                a thread owns a row (TMEM lane). Their maxima and sums are their own; the
 //                row's reference goes from one to the other through shared memory, before the
@@ -21,7 +21,8 @@
 //                tile's maximum passes it by more than 8 in log2 units (P <= 2^8: exact in the
 //                float32 sums, rounded in bf16 as well as below 1). The warpgroup of an item's
 //                last tile writes its output, while the other begins the next item.
-//   warps 16, 17 tcgen05.mma of A, B;   warp 18  TMA.
+//   warps 16, 17 tcgen05.mma of A, B;   warps 18, 19  TMA of Q and K, of V (one warp for both
+//                held the keys of later tiles back until a PV had freed room for values).
 // A softmax warp takes its 64 scores into registers and hands S back before anything else, and
 // P has two buffers of its own, so that neither S of the next tile nor the next softmax waits
 // for a PV. The MMA warp issues whatever product is ready, over the borders of items.
@@ -33,8 +34,8 @@ namespace {
 
 using namespace tc;
 
-constexpr int kM = 128, kKeys = 64, kThreads = 608;
-constexpr int kMmaWarp = 16, kLoadWarp = 18;
+constexpr int kM = 128, kKeys = 64, kThreads = 640;
+constexpr int kMmaWarp = 16, kLoadWarp = 18;  // K (and Q), V
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -186,47 +187,36 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
     tc_fence_after();
     const uint32_t tmem = misc[0];
 
-    if (warp == kLoadWarp) {
+    if (warp >= kLoadWarp) {
         // ---------------------------------------------------------------- TMA
+        const bool vals = warp > kLoadWarp;
+        const int stages = vals ? L::kVst : L::kKst, full0 = vals ? kBarVfull : kBarKfull, free0 = vals ? kBarVfree : kBarKfree;
+        const CUtensorMap *own_map = vals ? &tmV : &tmK, *sink_map = vals ? &tmVs : &tmKs;
+        const uint32_t store = sbase + (vals ? L::kV : L::kK);
+        volatile uint32_t *note_of_stage = notes + (vals ? 8 : 0);
         int nq[2] = {0, 0};
         bool ok = true;
         auto tile = [&](uint32_t dst, int blk, const CUtensorMap *m, int bar, int y, int z, int w) {
 #pragma unroll
             for (int c = 0; c < kBlocks; ++c) tma_load_4d(dst + c * blk, m, pipe.bar(bar), c * 64, y, z, w);
         };
-        Ring kr[2], vr[2];  // of each ring: the next stage
+        Ring ring_at[2];  // of each ring: the next stage
         int loads[2] = {0, 0};
-        // One entry: `note` tells the MMA warps which tiles take it (0: none), for K and V alike.
-        auto load_kv = [&](int ring, uint32_t note, int k0, bool sink, int hk, int b) {
-            const int ks = ring * L::kKst + kr[ring].st, vs = ring * L::kVst + vr[ring].st;
-            const uint32_t bytes = (uint32_t)(sink ? f.sink_box : kKeys) * D * 2;
-            if (loads[ring] >= L::kKst && !(ok = pipe.wait_warp(kBarKfree + ks, kr[ring].ph ^ 1u))) return;
+        // One entry: `note` tells the MMA warps which tiles take it (0: none).
+        auto load = [&](int ring, uint32_t note, int k0, bool sink, int hk, int b) {
+            const int s = ring * stages + ring_at[ring].st;
+            if (loads[ring] >= stages && !(ok = pipe.wait_warp(free0 + s, ring_at[ring].ph ^ 1u))) return;
             if (elect_one()) {
-                notes[ks] = note;
+                note_of_stage[s] = note;
                 if (note & kNoteEnd) {
-                    pipe.arrive(kBarKfull + ks);
+                    pipe.arrive(full0 + s);
                 } else {
-                    mbar_expect_tx(pipe.bar(kBarKfull + ks), bytes);
-                    tile(sbase + L::kK + ks * L::kY, kYBlk, sink ? &tmKs : &tmK, kBarKfull + ks, k0, hk, b);
+                    mbar_expect_tx(pipe.bar(full0 + s), (uint32_t)(sink ? f.sink_box : kKeys) * D * 2);
+                    tile(store + s * L::kY, kYBlk, sink ? sink_map : own_map, full0 + s, k0, hk, b);
                 }
             }
             __syncwarp();
-            kr[ring].next(L::kKst);
-            if (loads[ring] >= L::kVst && !(ok = pipe.wait_warp(kBarVfree + vs, vr[ring].ph ^ 1u))) {
-                ++loads[ring];
-                return;
-            }
-            if (elect_one()) {
-                notes[8 + vs] = note;
-                if (note & kNoteEnd) {
-                    pipe.arrive(kBarVfull + vs);
-                } else {
-                    mbar_expect_tx(pipe.bar(kBarVfull + vs), bytes);
-                    tile(sbase + L::kV + vs * L::kY, kYBlk, sink ? &tmVs : &tmV, kBarVfull + vs, k0, hk, b);
-                }
-            }
-            __syncwarp();
-            vr[ring].next(L::kVst);
+            ring_at[ring].next(stages);
             ++loads[ring];
         };
         auto note_of = [](int keys, bool first, bool last) -> uint32_t {
@@ -237,57 +227,57 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
             if (j >= f.items) break;
             const auto it = decode_item<PREFIX>(f, j);
             if constexpr (PREFIX) {
-                if (nq[0] > 0 && !(ok = pipe.wait_warp(kBarQfree, (nq[0] - 1) & 1))) break;
                 const int n0 = it.r1 - it.r0, n1 = it.r2 - it.r1;
-                if (elect_one()) {
-                    mbar_expect_tx(pipe.bar(kBarQfull), (uint32_t)(f.nb * a.G) * D * 2);
-                    tile(sbase + L::kQ, kXBlk, &tmQ, kBarQfull, it.h, it.i0, 0);
-                    // a range that is not there lets the queries go at once
-                    if (n0 == 0) pipe.arrive(kBarQfree);
-                    if (n1 == 0) pipe.arrive(kBarQfree);
+                if (!vals) {
+                    if (nq[0] > 0 && !(ok = pipe.wait_warp(kBarQfree, (nq[0] - 1) & 1))) break;
+                    if (elect_one()) {
+                        mbar_expect_tx(pipe.bar(kBarQfull), (uint32_t)(f.nb * a.G) * D * 2);
+                        tile(sbase + L::kQ, kXBlk, &tmQ, kBarQfull, it.h, it.i0, 0);
+                        // a range that is not there lets the queries go at once
+                        if (n0 == 0) pipe.arrive(kBarQfree);
+                        if (n1 == 0) pipe.arrive(kBarQfree);
+                    }
+                    __syncwarp();
+                    ++nq[0];
                 }
-                __syncwarp();
-                ++nq[0];
                 for (int i = 0; i < max(n0, n1) && ok; ++i) {
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const int n = x ? n1 : n0, e = (x ? it.r1 : it.r0) + i;
-                        if (i < n && ok)
-                            load_kv(x, note_of(min(kKeys, a.N - e * kKeys), i == 0, i + 1 == n), e * kKeys, false, it.hk, 0);
+                        if (i < n && ok) load(x, note_of(min(kKeys, a.N - e * kKeys), i == 0, i + 1 == n), e * kKeys, false, it.hk, 0);
                     }
                 }
             } else {
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (it.last(x) < 0) continue;
-                    if (nq[x] > 0 && !(ok = pipe.wait_warp(kBarQfree + x, (nq[x] - 1) & 1))) break;
-                    if (elect_one()) {
-                        mbar_expect_tx(pipe.bar(kBarQfull + x), L::kX);
-                        tile(sbase + L::kQ + x * L::kX, kXBlk, &tmQ, kBarQfull + x, it.i0 + x * f.qt, it.h, it.b);
-                    }
-                    __syncwarp();
-                    ++nq[x];
-                }
                 const int l0 = it.last(0), l1 = it.last(1);
+                if (!vals) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if ((x ? l1 : l0) < 0) continue;
+                        if (nq[x] > 0 && !(ok = pipe.wait_warp(kBarQfree + x, (nq[x] - 1) & 1))) break;
+                        if (elect_one()) {
+                            mbar_expect_tx(pipe.bar(kBarQfull + x), L::kX);
+                            tile(sbase + L::kQ + x * L::kX, kXBlk, &tmQ, kBarQfull + x, it.i0 + x * f.qt, it.h, it.b);
+                        }
+                        __syncwarp();
+                        ++nq[x];
+                    }
+                }
                 bool first0 = true, first1 = true;
                 for (int e = it.e0; e < it.e1 && ok; ++e) {
                     const uint32_t n0 = note_of(it.keys(0, e), first0, e == l0), n1 = note_of(it.keys(1, e), first1, e == l1);
                     first0 = first0 && n0 == 0u;
                     first1 = first1 && n1 == 0u;
-                    load_kv(0, n0 | n1 << 16, it.first_key(e), e < it.sp.ns, it.hk, it.b);
+                    load(0, n0 | n1 << 16, it.first_key(e), e < it.sp.ns, it.hk, it.b);
                 }
             }
         }
-        for (int ring = 0; ring < L::kRings && ok; ++ring) load_kv(ring, kNoteEnd, 0, false, 0, 0);
+        for (int ring = 0; ring < L::kRings && ok; ++ring) load(ring, kNoteEnd, 0, false, 0, 0);
         // what was started lands before the CTA's memory is released
         if (lane == 0) {
             for (int x = 0; x < 2; ++x) pipe.drain(kBarQfull + x, nq[x]);
-            for (int ring = 0; ring < L::kRings; ++ring) {  // (the last load may lack its V: then 100 ms at most)
-                for (int q = 0; q < L::kKst; ++q)
-                    pipe.drain(kBarKfull + ring * L::kKst + q, loads[ring] > q ? (loads[ring] - q + L::kKst - 1) / L::kKst : 0);
-                for (int q = 0; q < L::kVst; ++q)
-                    pipe.drain(kBarVfull + ring * L::kVst + q, loads[ring] > q ? (loads[ring] - q + L::kVst - 1) / L::kVst : 0);
-            }
+            for (int ring = 0; ring < L::kRings; ++ring)
+                for (int q = 0; q < stages; ++q)
+                    pipe.drain(full0 + ring * stages + q, loads[ring] > q ? (loads[ring] - q + stages - 1) / stages : 0);
         }
         __syncwarp();
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
@@ -399,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
             pipe.drain(kBarDrain + x, 1);
         }
         __syncwarp();
-    } else if (warp < 16) {
+    } else {
         // ---------------------------------------------------------------- softmax rows of tile x
         const int x = warp >> 3, w = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane, pair = 4 * x + quad;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
