@@ -60,6 +60,7 @@ struct Args {
     SinkBwdArgs a;
     int P, qt, tiles, sink_box;  // dQ: packed heads, queries of a tile, tiles of (b, packed heads)
     int items;                   // dK, dV: items of one (b, key-value head)
+    int hp, units;               // head packs (dK, dV: key-value heads) of a batch, and of all
     int total;
 };
 
@@ -76,9 +77,9 @@ __device__ __forceinline__ Item decode(const Args &f, int j) {
     const SinkBwdArgs &a = f.a;
     Item it;
     if (DQ) {
-        const int hp = a.H / f.P, units = a.B * hp, q = j / units, u = j - q * units;
-        it.b = u / hp;
-        it.h = (u - it.b * hp) * f.P;
+        const int q = j / f.units, u = j - q * f.units;
+        it.b = u / f.hp;
+        it.h = (u - it.b * f.hp) * f.P;
         it.hk = it.h / a.G;
         it.row0 = (f.tiles - 1 - q) * f.qt;  // latest queries (most keys) first
         const int t0 = a.N - a.Lq + it.row0;
@@ -87,10 +88,9 @@ __device__ __forceinline__ Item decode(const Args &f, int j) {
         it.i0 = it.i1 = it.tiles = it.s0 = it.index = 0;
         it.nseg = 1;
     } else {
-        const int Hk = a.H / a.G, heads = a.B * Hk;
-        const int x = j / heads, xb = j - x * heads;
-        it.b = xb / Hk;
-        it.hk = xb - it.b * Hk;
+        const int x = j / f.units, xb = j - x * f.units;
+        it.b = xb / f.hp;
+        it.hk = xb - it.b * f.hp;
         it.h = it.hk * a.G;
         const SinkItem k = sink_item(a, x);
         it.row0 = k.blk * kM;
@@ -287,27 +287,34 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
             if (it.steps <= 0) continue;
             const uint64_t xo = (n & 1) * (L::kX / 16);
             if (!(ok = pipe.wait_warp(kBarXfull + (n & 1), (n >> 1) & 1))) break;
+            auto shape = [&](int i) { return idesc_bf16(kM, DQ ? (step_keys(it, i) + 15) & ~15 : kRows, false); };
+            uint32_t id = shape(0);
             for (int i = 0; i < it.steps; ++i, ++c) {
                 const uint64_t yo = w.st * (L::kY / 16);
-                const uint32_t id = idesc_bf16(kM, DQ ? (step_keys(it, i) + 15) & ~15 : kRows, false);
-                if (!(ok = pipe.wait_warp(kBarYfull + w.st, w.ph))) break;
                 const int buf = c & (kBufs - 1);
+                if (!(ok = pipe.wait_warp(kBarYfull + w.st, w.ph))) break;
                 if (c >= kBufs && !(ok = pipe.wait_warp(kBarSTfree + buf, (c / kBufs - 1) & 1))) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        mma_ss(tmem + buf * 128, x1 + xo + ((k >> 2) * kXBlk + (k & 3) * 32) / 16, y1 + yo + ((k >> 2) * kYBlk + (k & 3) * 32) / 16,
-                               id, k > 0);
+                        mma_ss(tmem + buf * 128, x1 + xo + ((k >> 2) * kXBlk + (k & 3) * 32) / 16,
+                               y1 + yo + ((k >> 2) * kYBlk + (k & 3) * 32) / 16, id, k > 0);
+                }
+                __syncwarp();
+                // the next step's numbers while S is computed: T's issue waits for the pipe anyhow
+                const uint32_t id_t = id;
+                w.next(it);
+                if (DQ && i + 1 < it.steps) id = shape(i + 1);
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
                         mma_ss(tmem + buf * 128 + 64, x2 + xo + ((k >> 2) * kXBlk + (k & 3) * 32) / 16,
-                               y2 + yo + ((k >> 2) * kYBlk + (k & 3) * 32) / 16, id, k > 0);
+                               y2 + yo + ((k >> 2) * kYBlk + (k & 3) * 32) / 16, id_t, k > 0);
                     mma_commit(pipe.bar(kBarST + (c & 1)));
                     if (i + 1 == it.steps) mma_commit(pipe.bar(kBarXfree + (n & 1)));
                 }
                 __syncwarp();
-                w.next(it);
             }
             ++n;
         }
@@ -559,7 +566,11 @@ bool launch_sink_backward_tc(hils_dtype dt, int d, const SinkBwdArgs &a, cudaStr
     q.P = sink_pack(a.G);
     q.qt = kM / q.P;
     q.tiles = (a.Lq + q.qt - 1) / q.qt;
-    const int64_t qi = (int64_t)a.B * (a.H / q.P) * q.tiles;
+    q.hp = a.H / q.P;
+    q.units = a.B * q.hp;
+    k.hp = Hk;
+    k.units = a.B * Hk;
+    const int64_t qi = (int64_t)q.units * q.tiles;
     k.items = (int)sink_key_items(a);
     const int64_t ki = (int64_t)k.items * a.B * Hk;
     if (qi > 0x7fffffffll - 1024 || ki > 0x7fffffffll - 1024) return false;

@@ -198,8 +198,9 @@ __host__ __device__ inline SinkItem sink_item(const SinkBwdArgs &a, int x) {
     SinkItem it;
     const int ns = a.nsink * a.seg_s;
     it.nseg = x < ns ? a.seg_s : a.seg_w;
-    it.blk = x < ns ? x / a.seg_s : a.nsink + (x - ns) / a.seg_w;
-    it.seg = x < ns ? x % a.seg_s : (x - ns) % a.seg_w;
+    const int y = x < ns ? x : x - ns, q = it.nseg > 1 ? y / it.nseg : y;
+    it.blk = x < ns ? q : a.nsink + q;
+    it.seg = y - q * it.nseg;
     return it;
 }
 

@@ -63,7 +63,8 @@ constexpr uint32_t kNoteFirst = 128u, kNoteLast = 256u, kNoteEnd = 0x80000000u;
 
 struct FwdTc {
     SinkArgs a;
-    int P, qt, nqb;     // prefill: packed heads, queries of a tile, row items per (b, packed heads)
+    int P, qt, nqb;     // prefill: packed heads, queries of a tile, row items per (b, pack)
+    int hp, units;      // packs of a batch, (b, pack) pairs
     int nb, tiles;      // prefix: sequences of a tile, tiles
     int items, sink_box;
 };
@@ -124,7 +125,7 @@ __device__ __forceinline__ auto decode_item(const FwdTc &f, int j) {
         it.r2 = it.hasB ? (int)((int64_t)nt * (r + 2) / a.splits) : it.r1;
         return it;
     } else {
-        return RowItem<kKeys>(j, a.B, a.H, a.G, f.P, f.qt, f.nqb, a.Lq, a.N, a.W, a.A, a.splits);
+        return RowItem<kKeys>(j, f.hp, f.units, a.G, f.P, f.qt, f.nqb, a.Lq, a.N, a.W, a.A, a.splits);
     }
 }
 template <bool PREFIX, typename I>
@@ -637,7 +638,9 @@ bool launch_sink_forward_tc(hils_dtype dt, int d, const SinkArgs &a, cudaStream_
         f.P = sink_pack(a.G);
         f.qt = kM / f.P;
         f.nqb = (a.Lq + 2 * f.qt - 1) / (2 * f.qt);
-        items = (int64_t)a.B * (a.H / f.P) * f.nqb * a.splits;
+        f.hp = a.H / f.P;
+        f.units = a.B * f.hp;
+        items = (int64_t)f.units * f.nqb * a.splits;
         if (!make_view_map(&m[0], a.Q, a.B, a.H, a.Lq, d, f.qt, f.P)) return false;
     }
     if (items > 0x7fffffffll - 1024) return false;

@@ -206,7 +206,7 @@ struct RowItem {
     bool hasB;          // B has rows
 
     RowItem() = default;
-    __device__ __forceinline__ RowItem(int j, int B, int H, int G, int P, int qt, int nqb, int Lq, int N, int W, int A_,
+    __device__ __forceinline__ RowItem(int j, int hp, int units, int G, int P, int qt, int nqb, int Lq, int N, int W, int A_,
                                        int splits) {
         split = 0;
         if (splits > 1) {
@@ -214,7 +214,7 @@ struct RowItem {
             split = j - q * splits;
             j = q;
         }
-        const int hp = H / P, units = B * hp, q = j / units, u = j - q * units;
+        const int q = j / units, u = j - q * units;  // units: (b, pack) pairs, hp: packs of a batch
         const int qb = nqb - 1 - q;  // latest queries (most keys) first
         b = u / hp;
         h = (u - b * hp) * P;

@@ -50,6 +50,7 @@ struct Args {
     SinkBwdArgs a;
     int P, qn;   // heads and queries of each in a step
     int items;   // of one (b, key-value head)
+    int Hk, heads, packs, qshift;  // key-value heads of a batch, of all; head packs of a group; qn = 1 << qshift
 };
 struct Item {
     int xb, b, hk, j0, i0, tiles, s0, s1, nseg, index;
@@ -57,12 +58,11 @@ struct Item {
 };
 __device__ __forceinline__ Item decode(const Args &f, int j) {
     const SinkBwdArgs &a = f.a;
-    const int Hk = a.H / a.G, heads = a.B * Hk;
     Item it;
-    const int y = j / heads;
-    it.xb = j - y * heads;  // the blocks with most steps (the first ones of a causal range) come first
-    it.b = it.xb / Hk;
-    it.hk = it.xb - it.b * Hk;
+    const int y = j / f.heads;
+    it.xb = j - y * f.heads;  // the blocks with most steps (the first ones of a causal range) come first
+    it.b = it.xb / f.Hk;
+    it.hk = it.xb - it.b * f.Hk;
     const SinkItem k = sink_item(a, y);
     it.j0 = k.blk * kKeys;
     it.nseg = k.nseg;
@@ -73,8 +73,8 @@ __device__ __forceinline__ Item decode(const Args &f, int j) {
     const bool hasA = it.a0 < it.a1, hasB = it.b0 < it.b1;
     it.i0 = hasA ? it.a0 : it.b0;
     const int i1 = hasB ? max(it.b1, hasA ? it.a1 : 0) : it.a1;
-    it.tiles = hasA || hasB ? (i1 - it.i0 + f.qn - 1) / f.qn : 0;
-    const int steps = (a.G / f.P) * it.tiles;
+    it.tiles = hasA || hasB ? (i1 - it.i0 + f.qn - 1) >> f.qshift : 0;
+    const int steps = f.packs * it.tiles;
     it.s0 = 0;
     it.s1 = steps;
     if (k.nseg > 1) {
@@ -185,7 +185,6 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
         }
         __syncwarp();
     } else if (warp == kLseWarp) {
-        const int qshift = 31 - __clz(f.qn);
         int g = 0;
         bool ok = true;
         Walk w;
@@ -203,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     const int row = lane + 32 * m, i = it.i0 + tile * f.qn + (row & (f.qn - 1));
-                    const int64_t bh = (int64_t)it.b * a.H + it.hk * a.G + h * f.P + (row >> qshift);
+                    const int64_t bh = (int64_t)it.b * a.H + it.hk * a.G + h * f.P + (row >> f.qshift);
                     d[m] = i < a.Lq ? __ldg(a.lse + bh * a.Lq + i) : -INFINITY;
                 }
                 if (++tile == it.tiles) {
@@ -291,6 +290,16 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
             if (j >= total) break;
             const Item it = decode(f, j);
             const int key = it.j0 + x * kM + row;
+            // its weight so far, for the warp that adds to it
+            const int64_t at = ((int64_t)it.b * Hk + it.hk) * a.T + key;
+            float old = 0.f;
+            bool seen = false;
+            if (!odd && it.nseg == 1 && key < a.N) {
+                int k0, k1;
+                sink_rows_of_block(a, key, 1, &k0, &k1);
+                seen = k0 < k1;
+                if (seen) old = a.acc[at];
+            }
             float w = 0.f;
             walk.start(it);
             const int q_lo = (x ? it.b0 : it.a0) - f.qn - it.i0, q_hi = (x ? it.b1 : it.a1) - it.i0;
@@ -368,11 +377,8 @@ __global__ void __launch_bounds__(kThreads, 1) sink_weights_tc_kernel(const __gr
             if (key >= a.N) continue;
             if (it.nseg > 1) {
                 a.part[(int64_t)it.index * kKeys + x * kM + row] = w;
-            } else {
-                int k0, k1;
-                sink_rows_of_block(a, key, 1, &k0, &k1);
-                const int64_t at = ((int64_t)it.b * Hk + it.hk) * a.T + key;
-                if (k0 < k1) a.acc_out[at] = a.acc[at] + w;
+            } else if (seen) {
+                a.acc_out[at] = old + w;
             }
         }
     }
@@ -409,6 +415,10 @@ bool launch_sink_weights_tc(hils_dtype dt, int d, const SinkBwdArgs &a, cudaStre
     f.P = 1;
     while (f.P < 8 && a.G % (2 * f.P) == 0 && rows * 2 * f.P <= kRows) f.P *= 2;
     f.qn = kRows / f.P;
+    f.Hk = Hk;
+    f.heads = a.B * Hk;
+    f.packs = a.G / f.P;
+    for (f.qshift = 4; 1 << f.qshift < f.qn;) ++f.qshift;
     f.items = (int)sink_key_items(a);
     const int64_t total = (int64_t)f.items * a.B * Hk;
     if (total > 0x7fffffffll - 1024) return false;
