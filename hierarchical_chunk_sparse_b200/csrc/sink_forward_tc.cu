@@ -97,7 +97,12 @@ struct Ring {
 // The key tiles of one row tile x of an item, in order: entries [a0, a1), then [b0, b1).
 struct Own {
     int a0, n1, b0, n;  // n in all, n1 of them in the first run
+    int sinks;          // how many of them are sinks' tiles
     __device__ __forceinline__ int entry(int i) const { return i < n1 ? a0 + i : b0 + (i - n1); }
+    __device__ __forceinline__ int first_key(int i, const SinkSpan &sp) const {
+        const int e = entry(i);
+        return i < sinks ? e * kKeys : sp.lo + (e - sp.ns) * kKeys;
+    }
 };
 
 struct PrefixItem {
@@ -147,6 +152,8 @@ __device__ __forceinline__ Own own_tiles(const I &it, int x) {
         o.n = it.hasB ? o.n1 + max(0, it.e1 - o.b0) : 0;
         if (!it.hasB) o.n1 = 0;
     }
+    o.sinks = 0;
+    if constexpr (!PREFIX) o.sinks = min(o.n, max(0, it.sp.ns - it.e0));
     return o;
 }
 
@@ -421,25 +428,33 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                 t = a.N - a.Lq + i;
                 have = i < a.Lq;
             }
+            int see_lo = 0, see_hi = 0, end = 0;  // the window and all that the row sees; the tile's last key
+            if constexpr (!PREFIX) {
+                see_lo = t - a.W + 1;
+                see_hi = have ? t + 1 : 0;
+                end = x ? it.sp.hi : min(it.sp.hi, it.tB);
+            }
             float m = -INFINITY, l = 0.f;  // the reference of this warpgroup's last tile, and its sum
             for (int k = (c ^ w) & 1; k < own.n; k += 2) {  // tiles c + k of this warpgroup's parity
                 const int cc = c + k;
-                int n, lo, hi, as;  // visible columns: [lo, hi) and [0, as)
+                // this row's visible columns of the tile: [lo, hi) and (sinks in a window tile) [0, as)
+                int lo, hi, as = 0;
                 if constexpr (PREFIX) {
-                    n = hi = min(kKeys, a.N - own.entry(k) * kKeys);
-                    lo = as = 0;
+                    lo = 0;
+                    hi = min(kKeys, a.N - own.entry(k) * kKeys);
                 } else {
-                    const int e = own.entry(k);
-                    n = it.keys(x, e);
-                    it.columns(e, n, t, a.W, &lo, &hi, &as);
-                    if (!have) hi = as = 0;
+                    const int k0 = own.first_key(k, it.sp);
+                    const bool sink = k < own.sinks;
+                    lo = sink ? 0 : see_lo - k0;
+                    hi = min(sink ? it.sp.sinks : end, see_hi) - k0;
+                    as = sink ? 0 : min(a.A, see_hi) - k0;
                 }
-                const bool full = __all_sync(kFull, lo <= 0 && hi == kKeys);
+                const bool full = __all_sync(kFull, lo <= 0 && hi >= kKeys);
                 if (!(ok = pipe.wait_warp(kBarS + 2 * x + w, (cc >> 1) & 1))) break;
                 tc_fence_after();
                 uint32_t s[64];
                 tmem_ld32(s_col, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-                if (n > 32) tmem_ld32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+                tmem_ld32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));  // (behind the keys: anything, masked)
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
