@@ -27,30 +27,32 @@ namespace {
 
 using namespace tc;
 
-constexpr int kM = 128, kRows = 64, kStages = 3;
+// A step's rows stay until its sums are done, some 6000 cycles after their load began: with three
+// stages that alone made a step 2000 cycles.
+constexpr int kM = 128, kRows = 64, kStages = 5;
 constexpr int kThreads = 640, kStWarp = 16, kSumWarp = 17, kLoadWarp = 18, kScalarWarp = 19;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 static_assert(kM == kSinkKeys, "a key block is a tile");
 
 enum {
-    kBarXfull = 0,   // + buffer
-    kBarXfree = 2,   // + buffer: its last S, T completed
-    kBarYfull = 4,   // + stage: rows (bytes); dK, dV: lse and D (32 arrivals)
-    kBarYfree = 7,   // + stage: the sums that read it completed
-    kBarST = 10,     // + step parity: S, T written
-    kBarSTfree = 12, // + buffer: S, T read (8 warps)
-    kBarP = 14,      // + step parity: P, dS written (8 warps)
-    kBarSum = 16,    // + step parity: the sums that read them, and every one before, completed
-    kBarOfree = 18,  // an item's sums read (8 warps)
-    kBarDrain = 19,  // + MMA warp
-    kNumBars = 21
+    kBarXfull = 0,
+    kBarXfree = 1,   // the item's last S, T completed
+    kBarYfull = 2,   // + stage: rows (bytes); dK, dV: lse and D (32 arrivals)
+    kBarYfree = kBarYfull + kStages,    // + stage: the sums that read it completed
+    kBarST = kBarYfree + kStages,       // + step parity: S, T written
+    kBarSTfree = kBarST + 2,            // + buffer: S, T read (8 warps)
+    kBarP = kBarSTfree + 2,             // + step parity: P, dS written (8 warps)
+    kBarSum = kBarP + 2,                // + step parity: the sums that read them, and every one before, completed
+    kBarOfree = kBarSum + 2,            // an item's sums read (8 warps)
+    kBarDrain = kBarOfree + 1,          // + MMA warp
+    kNumBars = kBarDrain + 2
 };
 
 template <int D>
 struct Smem {
     static constexpr int kX = kM * D * 2, kY = kRows * D * 2;
-    static constexpr int kX1 = 0, kX2 = 2 * kX, kY1 = 4 * kX, kY2 = kY1 + kStages * kY;
+    static constexpr int kX1 = 0, kX2 = kX, kY1 = 2 * kX, kY2 = kY1 + kStages * kY;
     static constexpr int kSc = kY2 + kStages * kY;  // per stage: -lse (log2 units) [64], -D [64]
     static constexpr int kBars = kSc + kStages * kRows * 8, kMisc = kBars + 8 * kNumBars;
     static constexpr int kBytes = kMisc + 16;
@@ -186,15 +188,14 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
             if (j >= f.total) break;
             const Item it = decode<DQ>(f, j);
             if (it.steps <= 0) continue;
-            const int xb = n & 1;
-            if (n >= 2 && !(ok = pipe.wait_warp(kBarXfree + xb, ((n >> 1) - 1) & 1))) break;
+            if (n > 0 && !(ok = pipe.wait_warp(kBarXfree, (n - 1) & 1))) break;
             if (elect_one()) {
-                mbar_expect_tx(pipe.bar(kBarXfull + xb), 2 * L::kX);
+                mbar_expect_tx(pipe.bar(kBarXfull), 2 * L::kX);
 #pragma unroll
                 for (int c = 0; c < kBlocks; ++c) {
-                    const uint32_t o = sbase + xb * L::kX + c * kXBlk;
-                    tma_load_4d(o + L::kX1, &tmX1, pipe.bar(kBarXfull + xb), c * 64, it.row0, DQ ? it.h : it.hk, it.b);
-                    tma_load_4d(o + L::kX2, &tmX2, pipe.bar(kBarXfull + xb), c * 64, it.row0, DQ ? it.h : it.hk, it.b);
+                    const uint32_t o = sbase + c * kXBlk;
+                    tma_load_4d(o + L::kX1, &tmX1, pipe.bar(kBarXfull), c * 64, it.row0, DQ ? it.h : it.hk, it.b);
+                    tma_load_4d(o + L::kX2, &tmX2, pipe.bar(kBarXfull), c * 64, it.row0, DQ ? it.h : it.hk, it.b);
                 }
             }
             __syncwarp();
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
             }
         }
         if (lane == 0) {  // what was started lands before the CTA's memory is released
-            for (int x = 0; x < 2; ++x) pipe.drain(kBarXfull + x, n > x ? (n - x + 1) / 2 : 0);
+            pipe.drain(kBarXfull, n);
             for (int s = 0; s < kStages; ++s) pipe.drain(kBarYfull + s, g > s ? (g - s + kStages - 1) / kStages : 0);
         }
         __syncwarp();
@@ -285,8 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
             if (j >= f.total) break;
             const Item it = decode<DQ>(f, j);
             if (it.steps <= 0) continue;
-            const uint64_t xo = (n & 1) * (L::kX / 16);
-            if (!(ok = pipe.wait_warp(kBarXfull + (n & 1), (n >> 1) & 1))) break;
+            if (!(ok = pipe.wait_warp(kBarXfull, n & 1))) break;
             auto shape = [&](int i) { return idesc_bf16(kM, DQ ? (step_keys(it, i) + 15) & ~15 : kRows, false); };
             uint32_t id = shape(0);
             for (int i = 0; i < it.steps; ++i, ++c) {
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        mma_ss(tmem + buf * 128, x1 + xo + ((k >> 2) * kXBlk + (k & 3) * 32) / 16,
+                        mma_ss(tmem + buf * 128, x1 + ((k >> 2) * kXBlk + (k & 3) * 32) / 16,
                                y1 + yo + ((k >> 2) * kYBlk + (k & 3) * 32) / 16, id, k > 0);
                 }
                 __syncwarp();
@@ -309,10 +309,10 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        mma_ss(tmem + buf * 128 + 64, x2 + xo + ((k >> 2) * kXBlk + (k & 3) * 32) / 16,
+                        mma_ss(tmem + buf * 128 + 64, x2 + ((k >> 2) * kXBlk + (k & 3) * 32) / 16,
                                y2 + yo + ((k >> 2) * kYBlk + (k & 3) * 32) / 16, id_t, k > 0);
                     mma_commit(pipe.bar(kBarST + (c & 1)));
-                    if (i + 1 == it.steps) mma_commit(pipe.bar(kBarXfree + (n & 1)));
+                    if (i + 1 == it.steps) mma_commit(pipe.bar(kBarXfree));
                 }
                 __syncwarp();
             }
