@@ -7,7 +7,11 @@
 //   dK, dV  X = K, V of 128 keys (a block and a segment of its steps),
 //           Y = Q, dO of 64 queries of one head of the group;   acc: dV += P^T dO, dK += dS^T Q
 //   S = X1 Y1^T, T = X2 Y2^T (M = 128, N = 64, K = d), p = exp2(S scale2 - lse2),
-//   dS = p (T - D); P and dS in bf16 from TMEM; scale once on the float32 sums.
+//   dS = p (T - D); scale once on the float32 sums. P and dS are bf16 operands from TMEM. For dQ
+//   a second product takes what dS lost in the rounding: a row's dS sum to zero, so that dQ is
+//   small against its terms and their rounding showed (relative error 0.0026 instead of the
+//   0.0017 of the result's own rounding; the 8K backward 411 -> 433 us). dK and dV are sums over
+//   queries, without that cancellation.
 // Both recompute S and T: 7 products instead of the 5 of one kernel that would have to add
 // dQ (or dK and dV) across CTAs with atomics, whose order changes the result.
 // Warps (640 threads), hand-offs through mbarriers:
@@ -18,8 +22,8 @@
 //   16, 17 tcgen05.mma of S and T; of the sums;  18  TMA;  19  lse and D of a step's queries
 //          (dK, dV: a thread owns a key and runs over the queries), fetched two steps ahead.
 // TMEM, dK and dV: S [0,64), T [64,128), P [128,160), [160,192), dS [192,224), [224,256), dV
-// [256,384), dK [384,512); dQ: S, T [0,128), [128,256), dS [256,288), [288,320), dQ [384,512). Bound by the products: S, T take 48 cycles an MMA with N = 64 (their
-// operands come from shared memory), 1024 cycles a step for dQ and 1280 for dK, dV.
+// [256,384), dK [384,512); dQ: S, T [0,128), [128,256), dS and its rest [256,320), [320,384), dQ [384,512). Bound by the products: S, T take 48 cycles an MMA with N = 64 (their
+// operands come from shared memory), 1280 cycles a step.
 #include "sink_tc.cuh"
 
 namespace hils {
@@ -48,6 +52,12 @@ enum {
     kBarDrain = kBarOfree + 1,          // + MMA warp
     kNumBars = kBarDrain + 2
 };
+
+// x less its rounding to bf16, rounded to bf16 itself.
+__device__ __forceinline__ uint32_t rest_bf16(float2 x, uint32_t rounded) {
+    const float2 r = fma2(make_float2(bf16lo(rounded), bf16hi(rounded)), make_float2(-1.f, -1.f), x);
+    return pack_bf16(r.x, r.y);
+}
 
 template <int D>
 struct Smem {
@@ -150,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
     using L = Smem<D>;
     constexpr int kBlocks = D / 64, kXBlk = kM * 128, kYBlk = kRows * 128;
     // TMEM columns; dQ's one sum leaves room for two buffers of S, T
-    constexpr int kBufs = DQ ? 2 : 1, kP = 128, kDs = DQ ? 256 : 192, kAcc = DQ ? 384 : 256;
+    constexpr int kBufs = DQ ? 2 : 1, kP = 128, kDs = DQ ? 256 : 192, kDsStep = DQ ? 64 : 32, kAcc = DQ ? 384 : 256;
     const SinkBwdArgs &a = f.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = smem_u32(smem);
@@ -338,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
             for (int i = 0; i < it.steps; ++i, ++c) {
                 const uint64_t yo = w.st * (L::kY / 16);
                 const int k16 = DQ ? (step_keys(it, i) + 15) / 16 : kRows / 16;
-                const uint32_t p = tmem + kP + (c & 1) * 32, ds = tmem + kDs + (c & 1) * 32;
+                const uint32_t p = tmem + kP + (c & 1) * 32, ds = tmem + kDs + (c & 1) * kDsStep;
                 if (!(ok = pipe.wait_warp(kBarP + (c & 1), (c >> 1) & 1))) break;
                 if (!(ok = pipe.wait_warp(kBarYfull + w.st, w.ph))) break;  // (P came of it)
                 if (i == 0 && n > 0 && !(ok = pipe.wait_warp(kBarOfree, (n - 1) & 1))) break;
@@ -347,7 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
                     if (DQ) {
 #pragma unroll
                         for (int k = 0; k < kRows / 16; ++k)
-                            if (k < k16) mma_ts(tmem + kAcc, ds + k * 8, y1 + yo + k * (2048 / 16), id, i > 0 || k > 0);
+                            if (k < k16) {
+                                mma_ts(tmem + kAcc, ds + k * 8, y1 + yo + k * (2048 / 16), id, i > 0 || k > 0);
+                                mma_ts(tmem + kAcc, ds + 32 + k * 8, y1 + yo + k * (2048 / 16), id, 1u);
+                            }
                     } else {
 #pragma unroll
                         for (int k = 0; k < kRows / 16; ++k) mma_ts(tmem + kAcc, p + k * 8, y2 + yo + k * (2048 / 16), id, i > 0 || k > 0);
@@ -372,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
         const int w = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t s_col = lanes + (DQ ? w * 128 : 0) + half * 32, t_col = s_col + 64;
-        const uint32_t p_col = lanes + kP + w * 32 + half * 16, d_col = lanes + kDs + w * 32 + half * 16;
+        const uint32_t p_col = lanes + kP + w * 32 + half * 16, d_col = lanes + kDs + w * kDsStep + half * 16;
         const float scale2 = a.scale * kLog2e, lowest = scale2 > 0.f ? -INFINITY : INFINITY;  // its logit is -inf
         const float2 scale22 = make_float2(scale2, scale2);
         const int off = a.N - a.Lq;
@@ -446,15 +459,20 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
                     e0 = make_float2(exp2_ftz(e0.x), exp2_ftz(e0.y));
                     e1 = make_float2(exp2_ftz(e1.x), exp2_ftz(e1.y));
                     const float2 g0 = mul2(e0, add2(as2(u + q), d0)), g1 = mul2(e1, add2(as2(u + q + 2), d1));
-                    p[q / 2] = pack_bf16(e0.x, e0.y);
-                    p[q / 2 + 1] = pack_bf16(e1.x, e1.y);
                     ds[q / 2] = pack_bf16(g0.x, g0.y);
                     ds[q / 2 + 1] = pack_bf16(g1.x, g1.y);
+                    if (DQ) {  // what the rounding took
+                        p[q / 2] = rest_bf16(g0, ds[q / 2]);
+                        p[q / 2 + 1] = rest_bf16(g1, ds[q / 2 + 1]);
+                    } else {
+                        p[q / 2] = pack_bf16(e0.x, e0.y);
+                        p[q / 2 + 1] = pack_bf16(e1.x, e1.y);
+                    }
                 }
                 // the sums of two steps before have read this buffer
                 if (cc >= 2 && !(ok = pipe.wait_warp(kBarSum + w, ((cc >> 1) - 1) & 1))) break;
                 tc_fence_after();
-                if (!DQ) tmem_st16(p_col, p);
+                tmem_st16(DQ ? d_col + 32 : p_col, p);
                 tmem_st16(d_col, ds);
                 tmem_wait_st();
                 tc_fence_before();
