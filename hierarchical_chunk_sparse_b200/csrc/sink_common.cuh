@@ -92,19 +92,21 @@ inline int sink_prefill_splits(hils_dtype dt, int B, int H, int G, int Lq, int64
     const int64_t s = fill < most ? fill : most;
     return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
-// Key splits of a shared prefix of P tokens: two for each CTA of one wave over the row tiles.
-inline int sink_prefix_splits(int B, int Hk, int G, int P, int sms) {
-    const int nb = 128 / G;
+// Key splits of a shared prefix of P tokens: two for each CTA of one wave over the row tiles
+// (float32: 64-row tiles, three an SM, a 64-key tile each or more).
+inline int sink_prefix_splits(hils_dtype dt, int B, int Hk, int G, int P, int sms) {
+    const bool f32 = dt == HILS_F32;
+    const int nb = (f32 ? 64 : 128) / G;
     const int64_t tiles = (int64_t)Hk * ((B + nb - 1) / nb);
-    const int64_t fill = tiles > 0 && tiles < sms ? 2 * (sms / tiles) : 2;
-    const int64_t most = P / 256;
+    const int64_t fill = f32 ? (tiles > 0 ? 3 * sms / tiles : 1) : tiles > 0 && tiles < sms ? 2 * (sms / tiles) : 2;
+    const int64_t most = f32 ? P / 64 : P / 256;
     const int64_t s = fill < most ? fill : most;
     return (int)(s < 1 ? 1 : s > 128 ? 128 : s);
 }
-// Whether each sequence reads a shared prefix by itself (from L2, after the first): its bytes.
+// Whether each sequence reads a shared prefix by itself (from L2, after the first): by the bytes
+// that takes, about 13 us at the border, as much as the prefix's own pass costs at least.
 inline bool sink_prefix_direct(hils_dtype dt, int d, int B, int Hk, int64_t P) {
-    if (dt == HILS_F32) return B <= 5;
-    return B == 1 || (int64_t)B * Hk * P * d * 4 <= (64ll << 20);
+    return B <= (dt == HILS_F32 ? 2 : 1) || (int64_t)B * Hk * P * d * (dt == HILS_F32 ? 8 : 4) <= (64ll << 20);
 }
 inline size_t sink_part_bytes(int64_t rows, int slots, int d) {
     return sink_align((size_t)rows * slots * d * 4) + sink_align((size_t)rows * slots * 4);
