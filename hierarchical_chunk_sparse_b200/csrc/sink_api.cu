@@ -75,7 +75,7 @@ DecodePlan decode_plan(const hils_params *p, int64_t T, int64_t A, int64_t P, bo
     const int64_t rows = (int64_t)p->B * p->H;
     d.keys = prefix ? T : (T < A + p->W ? T : A + p->W);
     // a prefix that is cheaper read by each sequence than in a pass of its own
-    const bool direct = prefix && sink_prefix_direct(p->dtype, p->d, p->B, Hk, P);
+    const bool direct = prefix && sink_prefix_direct(p->dtype, p->d, p->B, p->H, Hk, P);
     if (direct) d.keys = P + T;
     d.prefix_splits = prefix && !direct ? sink_prefix_splits(p->dtype, p->B, Hk, groups(p), (int)P, sms) : 0;
     d.ctas = sink_decode_ctas(p->dtype, p->B, Hk, d.keys, sms);

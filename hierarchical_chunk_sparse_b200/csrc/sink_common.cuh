@@ -103,10 +103,14 @@ inline int sink_prefix_splits(hils_dtype dt, int B, int Hk, int G, int P, int sm
     const int64_t s = fill < most ? fill : most;
     return (int)(s < 1 ? 1 : s > 128 ? 128 : s);
 }
-// Whether each sequence reads a shared prefix by itself (from L2, after the first): by the bytes
-// that takes, about 13 us at the border, as much as the prefix's own pass costs at least.
-inline bool sink_prefix_direct(hils_dtype dt, int d, int B, int Hk, int64_t P) {
-    return B <= (dt == HILS_F32 ? 2 : 1) || (int64_t)B * Hk * P * d * (dt == HILS_F32 ? 8 : 4) <= (64ll << 20);
+// Whether each sequence reads a shared prefix by itself (from L2, after the first) instead of
+// the prefix's own pass over all of them and a join. bf16 (d = 128): 19 against 24 us with 4 of
+// 4096 tokens and 8 heads, 25.7 each at 8192, 37 against 43 us with 2 of 32K, 58 against 45 with 4;
+// float32 is bound by its products, of which the pass spends 64 rows' a tile however few there
+// are: 59 against 111 us with 8 rows, 62 against 45 with 16; small ones by their launches.
+inline bool sink_prefix_direct(hils_dtype dt, int d, int B, int H, int Hk, int64_t P) {
+    if (dt == HILS_F32) return B == 1 || B * (H / Hk) <= 12 || (int64_t)B * H * P * d <= (8ll << 20);
+    return B <= 2 || (int64_t)B * Hk * P * d <= (24ll << 20);
 }
 inline size_t sink_part_bytes(int64_t rows, int slots, int d) {
     return sink_align((size_t)rows * slots * d * 4) + sink_align((size_t)rows * slots * 4);
