@@ -180,26 +180,28 @@ __global__ void __launch_bounds__(256) evict_gather_kernel(EvictArgs a, int esiz
         for (int b = threadIdx.x; b < a.B; b += 256) a.len_out[b] = min(min(max(a.cache_len[b], 0), a.T), a.budget);
     if (r0 >= rows) return;
     const int my = lane < kRows && r0 + lane < rows ? a.idx[r0 + lane] : -1;
+    // the first row's (b, head) and place; rows number less than 2^31
+    const unsigned bk0 = (unsigned)r0 / (unsigned)a.budget, b0 = bk0 / (unsigned)a.Hk;
+    const int r = (int)((unsigned)r0 - bk0 * (unsigned)a.budget), h0 = (int)(bk0 - b0 * (unsigned)a.Hk);
+    // of a row `on` further: heads passed, and its place
+    auto place = [&](int on, int *rr) {
+        int k = 0;
+        for (*rr = r + on; *rr >= a.budget; ++k) *rr -= a.budget;
+        return k;
+    };
     if ((unsigned)my < (unsigned)a.T) {
-        const int64_t bk = (r0 + lane) / a.budget;
+        int rr;
+        const int64_t bk = (int64_t)bk0 + place(lane, &rr);
         a.acc_out[r0 + lane] = __ldg(a.acc + bk * a.T + my);
     }
     uint4 v[8];
     char *to[8];
-    // a row's (b, head) and place, kept while the rows go on within one head
-    int64_t bk = r0 / a.budget;
-    int r = (int)(r0 - bk * a.budget);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int e = i * 32 + lane, row = e / U, u = e % U;
         const int j = __shfl_sync(kFull, my, row);
-        int64_t k = bk;
-        int rr = r + row;
-        while (rr >= a.budget) {
-            rr -= a.budget;
-            ++k;
-        }
-        const int b = (int)(k / a.Hk), h = (int)(k - (int64_t)b * a.Hk);
+        int rr, h = h0 + place(row, &rr), b = (int)b0;
+        for (; h >= a.Hk; ++b) h -= a.Hk;
         const bool val = u >= U / 2;
         const View &s = val ? a.V : a.K;
         const MutView &d = val ? a.Vout : a.Kout;

@@ -75,7 +75,7 @@ DecodePlan decode_plan(const hils_params *p, int64_t T, int64_t A, int64_t P, bo
     const int64_t rows = (int64_t)p->B * p->H;
     d.keys = prefix ? T : (T < A + p->W ? T : A + p->W);
     // a prefix that is cheaper read by each sequence than in a pass of its own
-    const bool direct = prefix && sink_prefix_direct(p->dtype, p->d, p->B, p->H, Hk, P);
+    const bool direct = prefix && sink_prefix_direct(p->dtype, p->d, p->B, p->H, groups(p), P);
     if (direct) d.keys = P + T;
     d.prefix_splits = prefix && !direct ? sink_prefix_splits(p->dtype, p->B, Hk, groups(p), (int)P, sms) : 0;
     d.ctas = sink_decode_ctas(p->dtype, p->B, Hk, d.keys, sms);
@@ -103,7 +103,9 @@ void decode_space(const hils_params *p, const DecodePlan &plan, Carve &ws, float
 
 size_t sink_ws_bytes(const hils_params *p, int call, int rows, int other) {
     float scale;
-    if (check_sink(p, other, rows, &scale) != HILS_OK) return 0;
+    // query rows: of the other calls `rows` counts cached tokens
+    const int queries = call == HILS_CALL_SINK_PREFILL || call == HILS_CALL_SINK_BACKWARD ? rows : 1;
+    if (rows < 0 || check_sink(p, other, queries, &scale) != HILS_OK) return 0;
     const int64_t all = (int64_t)p->B * p->H * rows;
     SinkBwdArgs a{};
     switch (call) {

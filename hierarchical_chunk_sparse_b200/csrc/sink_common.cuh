@@ -108,9 +108,9 @@ inline int sink_prefix_splits(hils_dtype dt, int B, int Hk, int G, int P, int sm
 // 4096 tokens and 8 heads, 25.7 each at 8192, 37 against 43 us with 2 of 32K, 58 against 45 with 4;
 // float32 is bound by its products, of which the pass spends 64 rows' a tile however few there
 // are: 59 against 111 us with 8 rows, 62 against 45 with 16; small ones by their launches.
-inline bool sink_prefix_direct(hils_dtype dt, int d, int B, int H, int Hk, int64_t P) {
-    if (dt == HILS_F32) return B == 1 || B * (H / Hk) <= 12 || (int64_t)B * H * P * d <= (8ll << 20);
-    return B <= 2 || (int64_t)B * Hk * P * d <= (24ll << 20);
+inline bool sink_prefix_direct(hils_dtype dt, int d, int B, int H, int G, int64_t P) {
+    if (dt == HILS_F32) return B == 1 || (int64_t)B * G <= 12 || (int64_t)B * H * P * d <= (8ll << 20);
+    return B <= 2 || (int64_t)B * (H / G) * P * d <= (24ll << 20);
 }
 inline size_t sink_part_bytes(int64_t rows, int slots, int d) {
     return sink_align((size_t)rows * slots * d * 4) + sink_align((size_t)rows * slots * 4);

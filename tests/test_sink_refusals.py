@@ -163,3 +163,16 @@ def test_binding_refuses_wrong_tensors(lib):
         hils.hils_cache_evict(p, 0, 64, None, kv, None, None, kv, kv, None, None, None)
     with pytest.raises(ValueError, match="lse has dtype"):
         hils._sink_call("x", p, (), (("lse", _z(B, H, LQ), (B, H, LQ), torch.float32),), None, None)
+
+
+@pytest.mark.parametrize("call", (hils.HILS_CALL_SINK_WEIGHTS, hils.HILS_CALL_SINK_DECODE, hils.HILS_CALL_SINK_DECODE_ACC,
+                                  hils.HILS_CALL_PREFIX_DECODE, hils.HILS_CALL_CACHE_EVICT))
+def test_workspaces_of_large_caches_and_of_none(lib, call):
+    """More than 2^31 cached tokens over all heads (the calls' rows are their queries), and a
+    batch without heads."""
+    p = params(B=256, H=64, H_kv=8)
+    assert bytes_of(lib, p, call, 1 << 18, 16) >= 256
+    for dt in (hils.HILS_F32, hils.HILS_BF16):
+        assert bytes_of(lib, params(H=0, dtype=dt), call, 1 << 18, 16) >= 0
+        assert bytes_of(lib, params(B=0, dtype=dt), call, 1 << 18, 16) >= 0
+    assert bytes_of(lib, p, call, -1, 16) == 0
