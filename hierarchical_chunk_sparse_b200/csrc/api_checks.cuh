@@ -33,7 +33,7 @@ inline int check_params(const hils_params *p, float *scale) {
 }
 
 // Query heads per key-value head (parameters already checked).
-inline int groups(const hils_params *p) { return p->H_kv > 0 ? p->H / p->H_kv : 1; }
+inline int groups(const hils_params *p) { return p->H_kv > 0 && p->H > 0 ? p->H / p->H_kv : 1; }
 
 inline bool aligned16(const void *ptr) { return ((uintptr_t)ptr & 15u) == 0; }
 

@@ -180,7 +180,7 @@ inline void sink_key_plan(hils_dtype dt, int B, int Hk, int G, int Lq, int N, in
     if (a->nsink > a->nblk) a->nsink = a->nblk;
     auto segments = [&](int blocks, int64_t rows) {
         const int64_t steps = (int64_t)G * ((rows + step - 1) / step);
-        const int64_t fill = 592 / ((int64_t)B * Hk * (blocks > 0 ? blocks : 1));
+        const int64_t items = (int64_t)B * Hk * blocks, fill = items > 0 ? 592 / items : 1;
         int64_t s = steps / least < fill ? steps / least : fill;
         return (int)(s < 1 ? 1 : s);
     };

@@ -176,3 +176,9 @@ def test_workspaces_of_large_caches_and_of_none(lib, call):
         assert bytes_of(lib, params(H=0, dtype=dt), call, 1 << 18, 16) >= 0
         assert bytes_of(lib, params(B=0, dtype=dt), call, 1 << 18, 16) >= 0
     assert bytes_of(lib, p, call, -1, 16) == 0
+
+
+@pytest.mark.parametrize("name", [n for n in CALLS if n != "hils_cache_evict"])
+def test_no_heads_is_no_error(lib, name):
+    """Nor does a batch without heads launch anything (an eviction still writes len_out)."""
+    assert call(lib, name, p=params(H=0)) == 0
