@@ -26,6 +26,13 @@
 // A softmax warp takes its 64 scores into registers and hands S back before anything else, and
 // P has two buffers of its own, so that neither S of the next tile nor the next softmax waits
 // for a PV. The MMA warp issues whatever product is ready, over the borders of items.
+// An 8K prompt (32 heads, d = 128, W 512, A 4) takes 134 us from a cold L2 (2913 on the CUDA cores;
+// 41 by its bytes, 40 by its products): the tensor pipe is 35 % busy and the MUFU 39 %, a key tile
+// costs its warpgroup some 3570 cycles of which the softmax's dependent steps (TMEM load, maximum,
+// exponentials, TMEM store) are three quarters, and the last wave about a tenth of the time. The
+// prefix pass of 32 sequences over 64K tokens (8 key-value heads) takes 64 us, 4.2 TB/s.
+// 64-key tiles with two warpgroups each took 131 us where 128-key tiles with one took 222.
+// P is rounded to bf16 for its product (relative 2^-9 each, averaged by the sum), as O is.
 // TMEM of tile x, from 128 x: S [0,64), P [64,96), [96,128); O_A [256,384), O_B [384,512).
 #include "sink_tc.cuh"
 

@@ -13,6 +13,10 @@
 // steps and four for the odd: with one warp per quadrant and tile the loads and exponentials
 // waited on their latencies; 16, 17: tcgen05.mma of A, B; 18: TMA; 19: lse, fetched two steps
 // ahead.
+// A prompt of 8192 queries and keys (32 heads on 8, d = 128, causal) takes 342 us (10106 on the CUDA
+// cores; 165 by its products, 240 by its exponentials on the MUFU alone): the MUFU is 66 % busy,
+// the issue slots 58 %. 64 queries of 64K tokens take 72 us, 30 by the MUFU: an item has only two
+// steps, and half its time goes into its keys' arrival and its sums' departure.
 // TMEM: S_A [0,128), [128,256); S_B [256,384), [384,512).
 #include "fast_math.cuh"
 #include "sink_tc.cuh"

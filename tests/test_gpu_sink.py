@@ -359,6 +359,34 @@ def test_evict_by_distinct_weights(cuda_device, T, budget, W, A, spread):
             assert torch.equal(Ko[b, h, :m], K[b, h, at]) and torch.equal(ao[b, h, :m], acc[b, h, at])
 
 
+@pytest.mark.parametrize("T,budget,W,A", [(4000, 1500, 30, 4), (8000, 7000, 100, 1), (16384, 1000, 0, 0), (60000, 9000, 64, 4),
+                                          (131072, 30000, 512, 4), (140000, 9000, 64, 4), (150000, 149000, 64, 4)])
+@pytest.mark.parametrize("steps", [None, 7])
+def test_evict_selects_over_several_ctas(cuda_device, T, budget, W, A, steps):
+    """Rows that several CTAs share, with slots behind all their registers (140000, 150000):
+    distinct weights, or seven values whose ties begin and end anywhere."""
+    g = torch.Generator().manual_seed(T + 1)
+    acc = torch.rand(1, 2, T, generator=g)
+    if steps is not None:
+        acc = torch.floor(acc * steps)
+    acc = acc.to(cuda_device)
+    K = torch.randn(1, 2, T, 64, generator=g).to(BF).to(cuda_device)
+    p = params(1, 2, 2, 64, W, BF)
+    n = torch.tensor([T - 3], dtype=torch.int32, device=cuda_device)
+    Ko, Vo = (torch.zeros(1, 2, budget, 64, dtype=BF, device=cuda_device) for _ in range(2))
+    ao = torch.zeros(1, 2, budget, device=cuda_device)
+    idx = torch.full((1, 2, budget), -7, dtype=torch.int32, device=cuda_device)
+    out = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    ws = hils.alloc_workspace(p, hils.HILS_CALL_CACHE_EVICT, T, budget, device=cuda_device)
+    hils.hils_cache_evict(p, A, budget, K, K, acc, n, Ko, Vo, ao, idx, out, workspace=ws)
+    rows, new = ref.evict(acc, torch.tensor([T - 3]), budget, W, A)
+    assert out.tolist() == new
+    for h in range(2):
+        at = torch.tensor(rows[0][h], dtype=torch.long, device=cuda_device)
+        assert len(rows[0][h]) == budget and torch.equal(idx[0, h].long(), at)
+        assert torch.equal(Ko[0, h], K[0, h, at]) and torch.equal(Vo[0, h], K[0, h, at]) and torch.equal(ao[0, h], acc[0, h, at])
+
+
 def test_prompt_then_evict_then_decode(cuda_device):
     """The calls as a server makes them: a prompt in two pieces, its weights, the cache cut,
     then tokens decoded on the cut cache with their weights added, and a second cut."""
