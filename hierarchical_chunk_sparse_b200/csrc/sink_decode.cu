@@ -1,7 +1,7 @@
 // One query per sequence over the visible slots of its cache (formulas in sink_common.cuh).
 // Bound by HBM: 8 x 128K tokens of 8 key-value heads (32 heads, d = 128, bf16), 3.65 GB with the
-// weights added to acc, take 632 us, 5.8 TB/s (the walk 571, the join 9, acc 38; 7840 with one CTA
-// a row and no split). A window of 512 in one sequence takes 12 us, nearly all of it the launch.
+// weights added to acc, take 632 us, 5.8 TB/s (the walk 571, the join 9, acc 38; 7840 in float32 on
+// the CUDA cores). A window of 512 in one sequence takes 12 us, nearly all of it the launch.
 #include "sink_common.cuh"
 
 namespace hils {
@@ -185,7 +185,8 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 
 // One warp's running softmax of a group's heads over its tiles: bf16 with mma.sync, the up to
 // eight heads as the N of S^T = K Q^T and O^T = V^T P^T (a decode step reads each key once and
-// is bound by that; tcgen05's 128 rows would be 15/16 padding).
+// is bound by that; tcgen05's 128 rows would be 15/16 padding). P is rounded to bf16 for it, at
+// most 2^-8 of each.
 template <typename T, int D>
 struct Rows;
 

@@ -32,7 +32,7 @@
 // exponentials, TMEM store) are three quarters, and the last wave about a tenth of the time. The
 // prefix pass of 32 sequences over 64K tokens (8 key-value heads) takes 64 us, 4.2 TB/s.
 // 64-key tiles with two warpgroups each took 131 us where 128-key tiles with one took 222.
-// P is rounded to bf16 for its product (relative 2^-9 each, averaged by the sum), as O is.
+// P is rounded to bf16 for its product (at most 2^-8 of each, averaged by the sum), as O is.
 // TMEM of tile x, from 128 x: S [0,64), P [64,96), [96,128); O_A [256,384), O_B [384,512).
 #include "sink_tc.cuh"
 

@@ -1,8 +1,8 @@
 // Window-and-sink attention on the CUDA cores: prefill, shared prefix, backward and
 // accumulated weights (formulas in sink_common.cuh). 64 x 64 tiles of scores, 256 threads
 // with 4 x 4 of them each; every product and sum in float32, for float32 tensors and for bf16
-// whose strides or scale the tensor-core kernels do not take. A tile's two products take 33K FMA
-// cycles of a warp scheduler at d = 128; small calls are bound by the latency of one tile (7 us
+// whose strides or scale the tensor-core kernels do not take. A tile's two products take 8192
+// cycles of an SM at d = 128; small calls are bound by the latency of one tile (7 us
 // at d = 64) and the launches, which is why their rows and keys are split to a tile a CTA: 2 x 6
 // heads of 333 queries, W 200, d = 64 take 31 us with the binding, the backward of 2 x 4 heads of
 // 509 tokens 68.
