@@ -360,7 +360,8 @@ int hils_summarize_backward(const hils_params *p, hils_ctensor K, int N, hils_ct
  * Slots that no query of a call sees are never part of a result, whatever they hold (NaN
  * included); a slot that some query sees has to be finite.
  * Sums, softmax statistics and products are float32; for bf16 the probabilities and the
- * score gradients are rounded to bf16 as operands of their matrix products.
+ * score gradients are rounded to bf16 as operands of their matrix products (for dQ the score
+ * gradients are two bf16 parts, as a row of them sums to zero).
  * The first 32-bit word of each workspace is a status word, as in hils_attend_prefill.
  * No result depends on an order of atomic additions: equal calls give equal bits.
  * ------------------------------------------------------------------------------------ */
@@ -408,7 +409,7 @@ int hils_sink_decode(const hils_params *p, int A, hils_ctensor Q, hils_ctensor K
 
 /* One new token for each of B sequences that share a prefix of P tokens and go on in caches
  * of their own: softmax over the prefix and the sequence's cache_len[b] slots together.
- * The prefix is read once for the whole batch. params->W is not used.
+ * A long prefix is read once for the whole batch. params->W is not used.
  *   Q, O [B, H, 1, d];  Kp, Vp [1, Hk, P, d] (their sb is not used);  Kc, Vc [B, Hk, T, d];
  *   cache_len [B] int32, device, each in [0, T] (outside: the nearer end);
  *   lse [B, H] float32 out, or NULL
