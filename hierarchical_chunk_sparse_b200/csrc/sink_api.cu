@@ -35,6 +35,7 @@ int check_sink(const hils_params *p, int A, int64_t rows, float *scale) {
     if ((int64_t)p->B * p->H * rows > 0x7fffffffll) return HILS_ERR_INVALID_ARG;
     return HILS_OK;
 }
+int check_tokens(int64_t n) { return n > kSinkMostTokens ? HILS_ERR_UNSUPPORTED : HILS_OK; }
 
 // Longest key range of a prefill row tile.
 int64_t prefill_keys(const hils_params *p, int A, int Lq) { return (int64_t)p->W + A + (Lq < 256 ? Lq : 256); }
@@ -105,7 +106,8 @@ size_t sink_ws_bytes(const hils_params *p, int call, int rows, int other) {
     float scale;
     // query rows: of the other calls `rows` counts cached tokens
     const int queries = call == HILS_CALL_SINK_PREFILL || call == HILS_CALL_SINK_BACKWARD ? rows : 1;
-    if (rows < 0 || check_sink(p, other, queries, &scale) != HILS_OK) return 0;
+    const int64_t tokens = call == HILS_CALL_PREFIX_DECODE ? (int64_t)rows + other : rows;
+    if (rows < 0 || tokens > kSinkMostTokens || check_sink(p, other, queries, &scale) != HILS_OK) return 0;
     const int64_t all = (int64_t)p->B * p->H * rows;
     SinkBwdArgs a{};
     switch (call) {
@@ -135,6 +137,7 @@ int hils_sink_prefill(const hils_params *p, int A, hils_ctensor Q, int Lq, hils_
     float scale;
     HILS_TRY(check_sink(p, A, Lq, &scale));
     if (N < Lq) return HILS_ERR_INVALID_ARG;
+    HILS_TRY(check_tokens(N));
     HILS_TRY(check(Q, Lq, p));
     HILS_TRY(check(K, N, p));
     HILS_TRY(check(V, N, p));
@@ -177,6 +180,7 @@ int hils_sink_prefill_backward(const hils_params *p, int A, hils_ctensor Q, hils
                                hils_tensor dV, void *workspace, size_t ws_bytes, cudaStream_t stream) {
     float scale;
     HILS_TRY(check_sink(p, A, N, &scale));
+    HILS_TRY(check_tokens(N));
     HILS_TRY(check(Q, N, p));
     HILS_TRY(check(K, N, p));
     HILS_TRY(check(V, N, p));
@@ -223,6 +227,7 @@ int hils_sink_weights(const hils_params *p, int A, hils_ctensor Q, int Lq, hils_
     float scale;
     HILS_TRY(check_sink(p, A, Lq, &scale));
     if (N < Lq || T < N) return HILS_ERR_INVALID_ARG;
+    HILS_TRY(check_tokens(N));
     HILS_TRY(check(Q, Lq, p));
     HILS_TRY(check(K, N, p));
     const int64_t rows = (int64_t)p->B * p->H * Lq;
@@ -260,6 +265,7 @@ int hils_sink_decode(const hils_params *p, int A, hils_ctensor Q, hils_ctensor K
     float scale;
     HILS_TRY(check_sink(p, A, 1, &scale));
     if (T < 0 || (acc == nullptr) != (acc_out == nullptr)) return HILS_ERR_INVALID_ARG;
+    HILS_TRY(check_tokens(T));
     HILS_TRY(check(Q, 1, p));
     HILS_TRY(check(Kc, T, p));
     HILS_TRY(check(Vc, T, p));
@@ -303,6 +309,7 @@ int hils_prefix_decode(const hils_params *p, hils_ctensor Q, hils_ctensor Kp, hi
     float scale;
     HILS_TRY(check_sink(p, 0, 1, &scale));
     if (P < 0 || T < 0) return HILS_ERR_INVALID_ARG;
+    HILS_TRY(check_tokens((int64_t)P + T));
     HILS_TRY(check(Q, 1, p));
     HILS_TRY(check(Kp, P, p));
     HILS_TRY(check(Vp, P, p));
@@ -366,6 +373,7 @@ int hils_cache_evict(const hils_params *p, int A, int budget, hils_ctensor K, hi
     float scale;
     HILS_TRY(check_sink(p, A, 0, &scale));
     if (budget < 0 || T < 0 || (int64_t)A + p->W > budget) return HILS_ERR_INVALID_ARG;
+    HILS_TRY(check_tokens(T > budget ? T : budget));
     if ((int64_t)p->B * p->H * budget > 0x7fffffffll) return HILS_ERR_INVALID_ARG;
     const int Hk = p->H / groups(p);
     const int64_t out = (int64_t)p->B * Hk * budget;

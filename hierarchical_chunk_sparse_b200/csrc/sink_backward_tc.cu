@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
     } else if (warp == kScalarWarp) {
         // ---------------------------------------------------------------- lse and D of the queries
         if (!DQ) {
+            pdl_wait();  // D (its kernel is over before dQ's, which this grid follows)
             int g = 0;
             bool ok = true;
             Walk w;
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_bwd_tc_kernel(const __grid_c
         bool ok = true;
         int c = 0;
         Walk walk;
-        if (DQ) pdl_wait();  // D. (dK, dV: a dQ CTA on this SM ended only after that wait)
+        if (DQ) pdl_wait();  // D
         for (int r = 0; ok; ++r) {
             const int j = item_of_round(r, cta, G);
             if (j >= f.total) break;
@@ -576,7 +577,7 @@ hils_status run(const Args &f, const CUtensorMap *m, cudaStream_t s) {
     if (st != HILS_OK) return st;
     if (per_sm < 1) return HILS_ERR_CUDA;
     const int sms = device_sm_count();
-    // dQ follows the kernel of D; dK, dV need only that one too, so that their CTAs begin as dQ's end
+    // dQ follows the kernel of D; dK, dV begin, but for D, as dQ's CTAs end
     return sink_launch(true, k, f.total < sms ? f.total : sms, kThreads, Smem<D>::kBytes, s, m[0], m[1], m[2], m[3], m[4], m[5], f);
 }
 

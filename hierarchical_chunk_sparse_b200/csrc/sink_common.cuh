@@ -70,6 +70,10 @@ __host__ __device__ inline SinkSpan sink_span(int t0, int t1, int W, int A, int 
     return s;
 }
 
+// Tokens of a call (of the prefix and the own cache together): positions and tiles of them, and
+// what rounds up to a tile, stay within int.
+constexpr int64_t kSinkMostTokens = 0x7fffffffll - 1024;
+
 constexpr size_t kSinkStatusBytes = 256;
 inline size_t sink_align(size_t n) { return (n + 255) & ~(size_t)255; }
 

@@ -182,3 +182,10 @@ def test_workspaces_of_large_caches_and_of_none(lib, call):
 def test_no_heads_is_no_error(lib, name):
     """Nor does a batch without heads launch anything (an eviction still writes len_out)."""
     assert call(lib, name, p=params(H=0)) == 0
+
+
+@pytest.mark.parametrize("name,change", [("hils_sink_prefill", dict(N=2**31 - 1)), ("hils_sink_weights", dict(N=2**31 - 1, T=2**31 - 1)),
+                                         ("hils_sink_decode", dict(T=2**31 - 1)), ("hils_prefix_decode", dict(P=2**30, T=2**30)),
+                                         ("hils_cache_evict", dict(T=2**31 - 1))])
+def test_more_tokens_than_positions_count(lib, name, change):
+    assert call(lib, name, **change) == UNSUPPORTED
