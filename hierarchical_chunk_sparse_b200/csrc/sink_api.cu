@@ -15,6 +15,13 @@ int check(const V &t, int64_t rows, const hils_params *p) {
     return check_view(t.ptr, t.sb, t.sh, t.st, rows, p);
 }
 
+// A view that is written: no two of its rows are one.
+int check_out(const hils_tensor &t, int heads, int64_t rows, const hils_params *p) {
+    HILS_TRY(check(t, rows, p));
+    const bool twice = (t.sb == 0 && p->B > 1) || (t.sh == 0 && heads > 1) || (t.st == 0 && rows > 1);
+    return twice && (int64_t)p->B * heads * rows > 0 ? HILS_ERR_INVALID_ARG : HILS_OK;
+}
+
 // The addresses [*lo, *hi) that a [B, H, T, d] view spans.
 template <typename V>
 void span_of(const V &t, int64_t B, int64_t H, int64_t T, const hils_params *p, uintptr_t *lo, uintptr_t *hi) {
@@ -141,7 +148,7 @@ int hils_sink_prefill(const hils_params *p, int A, hils_ctensor Q, int Lq, hils_
     HILS_TRY(check(Q, Lq, p));
     HILS_TRY(check(K, N, p));
     HILS_TRY(check(V, N, p));
-    HILS_TRY(check(O, Lq, p));
+    HILS_TRY(check_out(O, p->H, Lq, p));
     HILS_TRY(check_array(lse, 0));
     const int64_t rows = (int64_t)p->B * p->H * Lq;
     if (rows == 0) return HILS_OK;
@@ -186,9 +193,9 @@ int hils_sink_prefill_backward(const hils_params *p, int A, hils_ctensor Q, hils
     HILS_TRY(check(V, N, p));
     HILS_TRY(check(O, N, p));
     HILS_TRY(check(dO, N, p));
-    HILS_TRY(check(dQ, N, p));
-    HILS_TRY(check(dK, N, p));
-    HILS_TRY(check(dV, N, p));
+    HILS_TRY(check_out(dQ, p->H, N, p));
+    HILS_TRY(check_out(dK, p->H / groups(p), N, p));
+    HILS_TRY(check_out(dV, p->H / groups(p), N, p));
     const int64_t rows = (int64_t)p->B * p->H * N;
     HILS_TRY(check_array(lse, rows));
     if (rows == 0) return HILS_OK;
@@ -269,7 +276,7 @@ int hils_sink_decode(const hils_params *p, int A, hils_ctensor Q, hils_ctensor K
     HILS_TRY(check(Q, 1, p));
     HILS_TRY(check(Kc, T, p));
     HILS_TRY(check(Vc, T, p));
-    HILS_TRY(check(O, 1, p));
+    HILS_TRY(check_out(O, p->H, 1, p));
     HILS_TRY(check_array(cache_len, p->B));
     HILS_TRY(check_array(lse, 0));
     HILS_TRY(check_array(acc, 0));
@@ -315,7 +322,7 @@ int hils_prefix_decode(const hils_params *p, hils_ctensor Q, hils_ctensor Kp, hi
     HILS_TRY(check(Vp, P, p));
     HILS_TRY(check(Kc, T, p));
     HILS_TRY(check(Vc, T, p));
-    HILS_TRY(check(O, 1, p));
+    HILS_TRY(check_out(O, p->H, 1, p));
     HILS_TRY(check_array(cache_len, p->B));
     HILS_TRY(check_array(lse, 0));
     const int64_t rows = (int64_t)p->B * p->H;
@@ -379,8 +386,8 @@ int hils_cache_evict(const hils_params *p, int A, int budget, hils_ctensor K, hi
     const int64_t out = (int64_t)p->B * Hk * budget;
     HILS_TRY(check(K, T, p));
     HILS_TRY(check(V, T, p));
-    HILS_TRY(check(Kout, budget, p));
-    HILS_TRY(check(Vout, budget, p));
+    HILS_TRY(check_out(Kout, Hk, budget, p));
+    HILS_TRY(check_out(Vout, Hk, budget, p));
     HILS_TRY(check_array(acc, (int64_t)p->B * Hk * T));
     HILS_TRY(check_array(cache_len, p->B));
     HILS_TRY(check_array(acc_out, out));

@@ -363,6 +363,8 @@ int hils_summarize_backward(const hils_params *p, hils_ctensor K, int N, hils_ct
  * score gradients are rounded to bf16 as operands of their matrix products (for dQ the score
  * gradients are two bf16 parts, as a row of them sums to zero).
  * The first 32-bit word of each workspace is a status word, as in hils_attend_prefill.
+ * Outputs overlap neither inputs nor one another, but where it is said; a view that is
+ * written has no stride of zero (HILS_ERR_INVALID_ARG).
  * A call takes up to 2^31 - 1025 tokens (hils_prefix_decode: P + T), more are
  * HILS_ERR_UNSUPPORTED.
  * No result depends on an order of atomic additions: equal calls give equal bits.

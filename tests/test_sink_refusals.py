@@ -189,3 +189,13 @@ def test_no_heads_is_no_error(lib, name):
                                          ("hils_cache_evict", dict(T=2**31 - 1))])
 def test_more_tokens_than_positions_count(lib, name, change):
     assert call(lib, name, **change) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("name,view,rows", [("hils_sink_prefill", "O", LQ), ("hils_sink_prefill_backward", "dQ", N),
+                                            ("hils_sink_prefill_backward", "dK", N), ("hils_sink_prefill_backward", "dV", N),
+                                            ("hils_sink_decode", "O", 1), ("hils_prefix_decode", "O", 1),
+                                            ("hils_cache_evict", "Kout", 100), ("hils_cache_evict", "Vout", 100)])
+def test_written_views_are_not_broadcast(lib, name, view, rows):
+    ptr = CALLS[name][view].ptr
+    for zero in ("sb", "sh") + (("st",) if rows > 1 else ()):
+        assert call(lib, name, **{view: T(ptr, **{zero: 0})}) == INVALID
