@@ -14,8 +14,8 @@
 namespace hils {
 
 // Launches a kernel; `early`: it may be scheduled while the kernel before it on the stream ends,
-// and calls pdl_wait() before it touches what that one writes. Every thread that writes, and one
-// of each CTA at least, waits: a grid is then never over before the one that it follows.
+// and calls pdl_wait() before it touches what that one writes. A CTA of each grid at least waits:
+// a grid is then never over before the one that it follows.
 template <typename... P, typename... A>
 hils_status sink_launch(bool early, void (*kernel)(P...), int64_t grid, int threads, int smem, cudaStream_t s, const A &...args) {
     if (grid <= 0) return HILS_OK;

@@ -4,8 +4,8 @@
 // whose strides or scale the tensor-core kernels do not take. A tile's two products take 8192
 // cycles of an SM at d = 128; small calls are bound by the latency of one tile (7 us
 // at d = 64) and the launches, which is why their rows and keys are split to a tile a CTA: 2 x 6
-// heads of 333 queries, W 200, d = 64 take 31 us with the binding, the backward of 2 x 4 heads of
-// 509 tokens 68.
+// heads of 333 queries, W 200, d = 64 take 28 us with the binding, the backward of 2 x 4 heads of
+// 509 tokens 53.
 #include "sink_common.cuh"
 
 namespace hils {
@@ -308,7 +308,13 @@ __global__ void __launch_bounds__(kThr) sink_bwd_kernel(SinkBwdArgs a, int tiles
     SinkSpan sp{};
     SinkItem it{};
     int xb = 0;
-    if (MODE != kModeWeights) pdl_wait();  // Dv; and dK, dV's grid must not be over before dQ's
+    // dQ follows D's kernel and, once that is complete, lets dK, dV's begin beside it (D is read from
+    // L2), which is not over before dQ's: 68 -> 53 us for 2 x 4 heads of 509 tokens
+    const bool last = MODE == kModeDkv && blockIdx.x == gridDim.x - 1;  // waits for dQ's grid at its end
+    if (MODE == kModeDq) {
+        pdl_wait();
+        pdl_trigger();
+    }
     if (MODE == kModeDq) {
         const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
         b = bh / a.H;
@@ -329,7 +335,10 @@ __global__ void __launch_bounds__(kThr) sink_bwd_kernel(SinkBwdArgs a, int tiles
         it = sink_item(a, x);
         r0 = it.blk * a.keys + part * kT;
         nrows = max(0, min(kT, a.N - r0));
-        if (nrows == 0) return;
+        if (nrows == 0) {
+            if (last) pdl_wait();
+            return;
+        }
         sink_rows_of_block(a, r0, kT, &i0, &ilim);
         qtiles = (ilim - i0 + kT - 1) / kT;
         const int64_t steps = (int64_t)a.G * qtiles;
@@ -392,7 +401,7 @@ __global__ void __launch_bounds__(kThr) sink_bwd_kernel(SinkBwdArgs a, int tiles
                 const float L = in ? __ldg(a.lse + q) : -INFINITY;
                 const float p = in && L != -INFINITY ? exp2f(s[r][c] * scale2 - L * kLog2e) : 0.f;
                 if (kTwo) {
-                    const float ds = in ? a.scale * p * (dp[r][c] - a.Dv[q]) : 0.f;
+                    const float ds = in ? a.scale * p * (dp[r][c] - __ldcg(a.Dv + q)) : 0.f;
                     if (MODE == kModeDkv) Ps[rr * kPS + cc] = p;
                     Ss[rr * kPS + cc] = ds;
                 } else {
@@ -439,6 +448,7 @@ __global__ void __launch_bounds__(kThr) sink_bwd_kernel(SinkBwdArgs a, int tiles
                 store4(d2 + 64 * u + 4 * tx, o2[r][4 * u], o2[r][4 * u + 1], o2[r][4 * u + 2], o2[r][4 * u + 3]);
         }
     }
+    if (last) pdl_wait();
 }
 
 // The partials of key blocks with several segments, in segment order: one warp per key row
