@@ -9,6 +9,12 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// cp_async16, or 16 zero bytes where `in` is false (nothing is read then).
+__device__ __forceinline__ void cp_async16_zfill(void *smem, const void *gmem, bool in) {
+    const unsigned s = (unsigned)__cvta_generic_to_shared(smem);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(gmem), "r"(in ? 16 : 0) : "memory");
+}
+
 template <typename T>
 constexpr int tile_keys() { return sizeof(T) == 2 ? 16 : 8; }
 template <typename T, int D>

@@ -18,13 +18,44 @@
 // the issue slots 58 %. 64 queries of 64K tokens take 72 us, 30 by the MUFU: an item has only two
 // steps, and half its time goes into its keys' arrival and its sums' departure.
 // TMEM: S_A [0,128), [128,256); S_B [256,384), [384,512).
-#include "fast_math.cuh"
 #include "sink_tc.cuh"
 
 namespace hils {
 namespace {
 
 using namespace tc;
+
+// exp2_fma (fast_math.cuh; its polynomial) for two values that are at most 127, in packed float32 arithmetic: 13
+// instructions for the pair. Below -126 the result is some subnormal number, below -127 (-inf too) 2^-149.
+__device__ __forceinline__ float2 exp2_fma2(float2 x) {
+    auto fma = [](float2 a, float2 b, float2 c) {
+        float2 d;
+        asm("fma.rn.f32x2 %0, %1, %2, %3;"
+            : "=l"(reinterpret_cast<unsigned long long &>(d))
+            : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)),
+              "l"(reinterpret_cast<unsigned long long &>(c)));
+        return d;
+    };
+    auto add = [](float2 a, float2 b) {
+        float2 d;
+        asm("add.rn.f32x2 %0, %1, %2;"
+            : "=l"(reinterpret_cast<unsigned long long &>(d))
+            : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
+        return d;
+    };
+    auto both = [](float c) { return make_float2(c, c); };
+    x = make_float2(fmaxf(x.x, -127.f), fmaxf(x.y, -127.f));
+    const float2 t = add(x, both(12582912.f));
+    const float2 f = fma(add(t, both(-12582912.f)), both(-1.f), x);
+    float2 p = fma(both(1.327647129e-03f), f, both(9.675540961e-03f));
+    p = fma(p, f, both(5.550713092e-02f));
+    p = fma(p, f, both(2.402212024e-01f));
+    p = fma(p, f, both(6.931469440e-01f));
+    p = fma(p, f, both(1.000000119e+00f));
+    // t holds 0x4b400000 + j: shifted left by 23 its upper bits fall away
+    return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
+                       __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
+}
 
 constexpr int kM = 128, kKeys = 2 * kM, kRows = 128, kStages = 3, kThreads = 640, kMmaWarp = 16, kLoadWarp = 18, kLseWarp = 19;
 constexpr uint32_t kTmemCols = 512;
