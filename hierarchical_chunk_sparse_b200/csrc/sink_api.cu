@@ -8,7 +8,6 @@ namespace hils {
 namespace {
 
 View view(const hils_ctensor &t) { return {t.ptr, t.sb, t.sh, t.st}; }
-View view(const hils_tensor &t) { return {t.ptr, t.sb, t.sh, t.st}; }
 MutView mut(const hils_tensor &t) { return {t.ptr, t.sb, t.sh, t.st}; }
 template <typename V>
 int check(const V &t, int64_t rows, const hils_params *p) {
