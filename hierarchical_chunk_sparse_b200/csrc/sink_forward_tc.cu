@@ -493,7 +493,10 @@ __global__ void __launch_bounds__(kThreads, 1) sink_fwd_tc_kernel(const __grid_c
                 __syncwarp();
                 pipe.arrive_if(lane == 0, kBarRef + pair);
                 if (__any_sync(kFull, raise && ref != -INFINITY)) {
-                    // O holds the tiles before this one
+                    // O holds the tiles before this one. The other buffer's PV of three tiles before may still
+                    // be open, and by its parity the last one's would pass for complete: this buffer's of two
+                    // tiles before, whose own phase before this warp has waited for, comes first.
+                    if (cc >= 2 && !(ok = pipe.wait_warp(kBarPV + 2 * x + w, ((cc >> 1) - 1) & 1))) break;
                     if (!(ok = pipe.wait_warp(kBarPV + 2 * x + (w ^ 1), ((cc - 1) >> 1) & 1))) break;
                     tc_fence_after();
                     const float fac = raise && ref != -INFINITY ? exp2_ftz(ref - m_new) : 1.f;

@@ -21,6 +21,9 @@ __device__ __forceinline__ bool mbar_test_phase(uint32_t bar, uint32_t parity) {
 // The CTA's waits. Each is bounded by the global timer; the first one that expires sets
 // the abort flag and bit 0 of the call's status word, after which every wait fails, the
 // roles stop issuing, and the CTA drains what it started and returns.
+// A wait knows its phase by the parity alone: with the phase before that one still open it
+// returns at once. So whoever waits has to know that the phase before is complete: from its
+// own earlier wait, or from an event that came after it.
 struct Pipe {
     uint32_t bars;                  // shared address of the first mbarrier
     volatile uint32_t *abort_flag;  // shared
