@@ -292,8 +292,9 @@ constexpr int bwd_smem(int mode) {
 // Query-major (dQ): rows are 64 queries of one head, tiles are keys. Key-major (dK and dV,
 // or the weights): rows are 64 keys of one key-value head, tiles are queries of the
 // group's heads. X1, X2 are the rows' Q, dO or K, V; Y1, Y2 the tiles' K, V or Q, dO.
+// `block`: the CTA among those of its mode.
 template <int MODE, typename T, int D>
-__global__ void __launch_bounds__(kThr) sink_bwd_kernel(SinkBwdArgs a, int tiles) {
+__device__ __forceinline__ void sink_bwd_rows(const SinkBwdArgs &a, int tiles, int block) {
     extern __shared__ float sm[];
     constexpr bool kTwo = MODE != kModeWeights;
     float *X1 = sm, *Y1 = X1 + kT * (D + 4);
@@ -308,15 +309,8 @@ __global__ void __launch_bounds__(kThr) sink_bwd_kernel(SinkBwdArgs a, int tiles
     SinkSpan sp{};
     SinkItem it{};
     int xb = 0;
-    // dQ follows D's kernel and, once that is complete, lets dK, dV's begin beside it (D is read from
-    // L2), which is not over before dQ's: 68 -> 53 us for 2 x 4 heads of 509 tokens
-    const bool last = MODE == kModeDkv && blockIdx.x == gridDim.x - 1;  // waits for dQ's grid at its end
     if (MODE == kModeDq) {
-        pdl_wait();
-        pdl_trigger();
-    }
-    if (MODE == kModeDq) {
-        const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
+        const int tile = block % tiles, bh = block / tiles;
         b = bh / a.H;
         h = bh % a.H;
         hk = h / a.G;
@@ -327,18 +321,15 @@ __global__ void __launch_bounds__(kThr) sink_bwd_kernel(SinkBwdArgs a, int tiles
         s1 = sp.ns + sp.nw;
     } else {
         // an item's key block in parts of 64 keys
-        const int parts = a.keys / kT, part = blockIdx.x % parts, x = (blockIdx.x / parts) % tiles;
-        xb = (blockIdx.x / parts) / tiles;
+        const int parts = a.keys / kT, part = block % parts, x = (block / parts) % tiles;
+        xb = (block / parts) / tiles;
         b = xb / Hk;
         hk = xb % Hk;
         h = 0;
         it = sink_item(a, x);
         r0 = it.blk * a.keys + part * kT;
         nrows = max(0, min(kT, a.N - r0));
-        if (nrows == 0) {
-            if (last) pdl_wait();
-            return;
-        }
+        if (nrows == 0) return;
         sink_rows_of_block(a, r0, kT, &i0, &ilim);
         qtiles = (ilim - i0 + kT - 1) / kT;
         const int64_t steps = (int64_t)a.G * qtiles;
@@ -419,7 +410,7 @@ __global__ void __launch_bounds__(kThr) sink_bwd_kernel(SinkBwdArgs a, int tiles
         const int rr = 4 * ty + r;
         const float ws = MODE == kModeWeights ? sum16(w[r]) : 0.f;
         if (rr >= nrows) continue;
-        const int64_t item = (int64_t)xb * tiles + (blockIdx.x / (a.keys / kT)) % tiles;  // key-major: partial sums' place
+        const int64_t item = (int64_t)xb * tiles + (block / (a.keys / kT)) % tiles;  // key-major: partial sums' place
         const int kr = r0 + rr - it.blk * a.keys;
         if (MODE == kModeWeights) {
             if (tx == 0) {
@@ -448,7 +439,21 @@ __global__ void __launch_bounds__(kThr) sink_bwd_kernel(SinkBwdArgs a, int tiles
                 store4(d2 + 64 * u + 4 * tx, o2[r][4 * u], o2[r][4 * u + 1], o2[r][4 * u + 2], o2[r][4 * u + 3]);
         }
     }
-    if (last) pdl_wait();
+}
+
+// dQ's CTAs [0, nq), then those of dK and dV: side by side, each reads D once its grid is complete
+// (in two kernels, dK and dV behind dQ, 2 x 4 heads of 509 tokens took 68 us, so 53). kPerSm CTAs an
+// SM at d = 64; at d = 128 one fits.
+template <typename T, int D, int kPerSm>
+__global__ void __launch_bounds__(kThr, kPerSm) sink_bwd_kernel(SinkBwdArgs a, int qtiles, int nq, int items) {
+    pdl_wait();
+    if ((int)blockIdx.x < nq) sink_bwd_rows<kModeDq, T, D>(a, qtiles, blockIdx.x);
+    else sink_bwd_rows<kModeDkv, T, D>(a, items, blockIdx.x - nq);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThr) sink_weights_kernel(SinkBwdArgs a, int items) {
+    sink_bwd_rows<kModeWeights, T, D>(a, items, blockIdx.x);
 }
 
 // The partials of key blocks with several segments, in segment order: one warp per key row
@@ -520,19 +525,25 @@ hils_status dot(const SinkBwdArgs &a, float *Dv, cudaStream_t s) {
 }
 template <typename T, int D>
 hils_status backward(const SinkBwdArgs &a, cudaStream_t s) {
-    static KernelSetup sq, sk;
-    const int tiles = (a.Lq + kT - 1) / kT;
-    const hils_status st =
-        run(sq, true, sink_bwd_kernel<kModeDq, T, D>, (int64_t)tiles * a.B * a.H, kThr, bwd_smem<D>(kModeDq), s, a, tiles);
-    if (st != HILS_OK) return st;
-    const int items = (int)sink_key_items(a);
-    return run(sk, true, sink_bwd_kernel<kModeDkv, T, D>, (int64_t)(a.keys / kT) * items * a.B * (a.H / a.G), kThr, bwd_smem<D>(kModeDkv), s, a, items);
+    static KernelSetup one, two;
+    const int tiles = (a.Lq + kT - 1) / kT, items = (int)sink_key_items(a);
+    const int64_t nq = (int64_t)tiles * a.B * a.H, nk = (int64_t)(a.keys / kT) * items * a.B * (a.H / a.G);
+    if (nq > 0x7fffffffll) return HILS_ERR_UNSUPPORTED;
+    // Two CTAs an SM, but for calls that wait for one CTA's walk (dQ's longest) rather than for all
+    // steps of an SM: 8 heads of 2048 causal tokens 629 -> 540 us, 2 x 4 of 1000 with W 96 80 -> 72;
+    // with one, and the registers for deeper unrolling, 4 heads of 2048 375 -> 321 us, 2 x 4 of 509
+    // with W 96 57 -> 53.
+    const int64_t see = ((int64_t)a.W + a.A + kT - 1 + kT - 1) / kT, longest = see < tiles ? see : tiles;
+    const int64_t steps = 2 * (longest * (longest + 1) / 2 + (tiles - longest) * longest) * a.B * a.H;
+    if (D == 64 && steps > longest * device_sm_count())
+        return run(two, true, sink_bwd_kernel<T, D, D == 64 ? 2 : 1>, nq + nk, kThr, bwd_smem<D>(kModeDkv), s, a, tiles, (int)nq, items);
+    return run(one, true, sink_bwd_kernel<T, D, 1>, nq + nk, kThr, bwd_smem<D>(kModeDkv), s, a, tiles, (int)nq, items);
 }
 template <typename T, int D>
 hils_status weights(const SinkBwdArgs &a, cudaStream_t s) {
     static KernelSetup setup;
     const int items = (int)sink_key_items(a);
-    return run(setup, false, sink_bwd_kernel<kModeWeights, T, D>, (int64_t)(a.keys / kT) * items * a.B * (a.H / a.G), kThr, bwd_smem<D>(kModeWeights), s,
+    return run(setup, false, sink_weights_kernel<T, D>, (int64_t)(a.keys / kT) * items * a.B * (a.H / a.G), kThr, bwd_smem<D>(kModeWeights), s,
                a, items);
 }
 template <typename T, int D>
