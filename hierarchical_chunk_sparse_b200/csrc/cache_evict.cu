@@ -16,7 +16,8 @@ __device__ __forceinline__ unsigned weight_key(float f) { return f != f ? 0u : o
 // so that all come to the same threshold. It ends early once a bin's lower border leaves exactly
 // m keys. Equal bins within a warp are counted by one lane: many weights are zero, and their
 // atomics on one address took 70 us of the 77 at 64 x 32K slots. Warp w of CTA c holds the keys of
-// R * 32 consecutive slots; those behind C * THR * R slots are read again for each histogram.
+// R * 32 consecutive slots; those behind C * THR * R slots are read again for each histogram. Slots
+// are counted unsigned: a step past the last one may pass 2^31.
 // Bound by the latencies of its steps.
 constexpr int kBins = 2048;
 
@@ -50,19 +51,19 @@ __global__ void __cluster_dims__(C) __launch_bounds__(THR) evict_select_kernel(E
     const float *acc = a.acc + bk * a.T;
     int32_t *idx = a.idx + bk * a.budget;
     if (n <= a.budget) {
-        for (int i = rank * THR + tid; i < a.budget; i += C * THR) idx[i] = i < n ? i : -1;
+        for (unsigned i = rank * THR + tid; i < (unsigned)a.budget; i += C * THR) idx[i] = i < (unsigned)n ? (int)i : -1;
         return;
     }
     const int m0 = a.A, m1 = n - a.W, m = a.budget - a.A - a.W;  // m of [m0, m1), fewer than there are
-    for (int i = rank * THR + tid; i < a.A; i += C * THR) idx[i] = i;
-    for (int i = rank * THR + tid; i < a.W; i += C * THR) idx[a.budget - a.W + i] = n - a.W + i;
+    for (unsigned i = rank * THR + tid; i < (unsigned)a.A; i += C * THR) idx[i] = i;
+    for (unsigned i = rank * THR + tid; i < (unsigned)a.W; i += C * THR) idx[a.budget - a.W + i] = n - a.W + i;
     if (m == 0) return;
-    const int mid = m1 - m0, far = C * THR * R;  // slots [far, mid) of the middle stay in memory
+    const unsigned mid = m1 - m0, far = C * THR * R;  // slots [far, mid) of the middle stay in memory
     unsigned key[R];
     unsigned low = 0xffffffffu, high = 0u;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int i = (gwarp * R + r) * 32 + lane;
+        const unsigned i = (gwarp * R + r) * 32 + lane;
         key[r] = i < mid ? weight_key(__ldg(acc + m0 + i)) : 0u;
     }
 #pragma unroll
@@ -71,7 +72,7 @@ __global__ void __cluster_dims__(C) __launch_bounds__(THR) evict_select_kernel(E
         low = min(low, in ? key[r] : 0xffffffffu);
         high = max(high, key[r]);
     }
-    for (int i = far + rank * THR + tid; i < mid; i += C * THR) {
+    for (unsigned i = far + rank * THR + tid; i < mid; i += C * THR) {
         const unsigned k = weight_key(__ldg(acc + m0 + i));
         low = min(low, k);
         high = max(high, k);
@@ -110,8 +111,8 @@ __global__ void __cluster_dims__(C) __launch_bounds__(THR) evict_select_kernel(E
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < R; ++r) count((gwarp * R + r) * 32 + lane < mid, key[r]);
-        for (int i0 = far + rank * THR; i0 < mid; i0 += C * THR) {
-            const int i = i0 + tid;
+        for (unsigned i0 = far + rank * THR; i0 < mid; i0 += C * THR) {
+            const unsigned i = i0 + tid;
             count(i < mid, i < mid ? weight_key(__ldg(acc + m0 + i)) : 0u);
         }
         cluster_sync();
@@ -164,7 +165,7 @@ __global__ void __cluster_dims__(C) __launch_bounds__(THR) evict_select_kernel(E
         cluster_sync();  // hist and found are free again
     }
     // keys above thr are kept, and of those equal to it the first need (all of them if exact)
-    auto kind = [&](int i, unsigned k) { return i >= mid ? 0 : k > thr || (exact && k == thr) ? 2 : k == thr ? 1 : 0; };
+    auto kind = [&](unsigned i, unsigned k) { return i >= mid ? 0 : k > thr || (exact && k == thr) ? 2 : k == thr ? 1 : 0; };
     int2 mine = make_int2(0, 0);  // of this warp's register slots: above, equal
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -186,7 +187,7 @@ __global__ void __cluster_dims__(C) __launch_bounds__(THR) evict_select_kernel(E
         at.y += __reduce_add_sync(kFull, w < gwarp ? x.y : 0);
     }
     cluster_sync();  // nobody's shared memory is read any more
-    auto keep = [&](int i, int t, int2 &p) {
+    auto keep = [&](unsigned i, int t, int2 &p) {
         const unsigned up = __ballot_sync(kFull, t == 2), eq = __ballot_sync(kFull, t == 1), lower = (1u << lane) - 1u;
         const int gt = p.x + __popc(up & lower), eb = p.y + __popc(eq & lower);
         if (t == 2 || (t == 1 && eb < need)) idx[a.A + gt + min(eb, need)] = m0 + i;
@@ -195,13 +196,14 @@ __global__ void __cluster_dims__(C) __launch_bounds__(THR) evict_select_kernel(E
     };
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int i = (gwarp * R + r) * 32 + lane;
+        const unsigned i = (gwarp * R + r) * 32 + lane;
         keep(i, kind(i, key[r]), at);
     }
     if (rank > 0) return;
     // the slots that stayed in memory: THR at a time, in order
-    for (int i0 = far; i0 < mid; i0 += THR) {
-        const int i = i0 + tid, t = i < mid ? kind(i, weight_key(__ldg(acc + m0 + i))) : 0;
+    for (unsigned i0 = far; i0 < mid; i0 += THR) {
+        const unsigned i = i0 + tid;
+        const int t = i < mid ? kind(i, weight_key(__ldg(acc + m0 + i))) : 0;
         const int2 x = make_int2(__popc(__ballot_sync(kFull, t == 2)), __popc(__ballot_sync(kFull, t == 1)));
         __syncthreads();
         if (lane == 0) base[warp] = x;
