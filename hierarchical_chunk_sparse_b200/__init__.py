@@ -124,6 +124,9 @@ class Params:
 
     def c(self) -> _Params:
         dt = _DTYPES.get(self.dtype, -1) if isinstance(self.dtype, torch.dtype) else int(self.dtype)
+        sizes = self.B, self.H, self.d, self.S, self.K, self.W, self.H_kv
+        if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:  # ctypes would keep the lower 32 bits
+            raise ValueError(f"Params: B, H, d, S, K, W, H_kv = {sizes}: beyond 32 bits")
         return _Params(self.B, self.H, self.d, self.S, self.K, self.W, dt, self.scale, self.flags, self.H_kv)
 
 
@@ -179,8 +182,16 @@ def _check(call: str, rc: int) -> None:
         raise HilsError(call, rc, detail)
 
 
+def _count(call: str, name: str, x: int) -> int:
+    """A count for a C int, of which ctypes would keep the lower 32 bits."""
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError(f"{call}: {name} = {x}: beyond 32 bits")
+    return x
+
+
 def hils_workspace_bytes(p: Params, call: int, Lq: int, C: int) -> int:
-    return int(load_library().hils_workspace_bytes(ctypes.byref(p.c()), call, Lq, C))
+    return int(load_library().hils_workspace_bytes(ctypes.byref(p.c()), call, _count("hils_workspace_bytes", "Lq", Lq),
+                                                   _count("hils_workspace_bytes", "C", C)))
 
 
 def hils_workspace_init(workspace, ws_bytes: int | None = None, stream=None) -> None:
@@ -482,6 +493,7 @@ def hils_sink_prefill(p: Params, A: int, Q, K, V, O, lse=None, workspace=None, s
     lse [B,H,Lq] float32 (optional). p.W >= N is full causal attention.
     workspace: alloc_workspace(p, HILS_CALL_SINK_PREFILL, Lq, A)."""
     call = "hils_sink_prefill"
+    _count(call, "A", A)
     lq, n = _bhtd(call, "Q", Q), _bhtd(call, "K", K)
     q, kv = (p.B, p.H, lq, p.d), (p.B, p.Hk, n, p.d)
     cq, ck, cv, co, cl, run = _sink_call(call, p, (("Q", Q, q), ("K", K, kv), ("V", V, kv), ("O", O, q)),
@@ -494,6 +506,7 @@ def hils_sink_prefill_backward(p: Params, A: int, Q, K, V, O, lse, dO, dQ, dK, d
     from dO: dQ [B,H,N,d], dK, dV [B,Hk,N,d], all in p.dtype and all written.
     workspace: alloc_workspace(p, HILS_CALL_SINK_BACKWARD, N, A)."""
     call = "hils_sink_prefill_backward"
+    _count(call, "A", A)
     n = _bhtd(call, "Q", Q)
     q, kv = (p.B, p.H, n, p.d), (p.B, p.Hk, n, p.d)
     cq, ck, cv, co, cdo, cdq, cdk, cdv, cl, run = _sink_call(
@@ -508,6 +521,7 @@ def hils_sink_weights(p: Params, A: int, Q, K, lse, acc, acc_out=None, workspace
     [B,Hk,T], T >= N, into acc_out (acc itself if None).
     workspace: alloc_workspace(p, HILS_CALL_SINK_WEIGHTS, N, A)."""
     call = "hils_sink_weights"
+    _count(call, "A", A)
     lq, n = _bhtd(call, "Q", Q), _bhtd(call, "K", K)
     out = acc if acc_out is None else acc_out
     t = acc.shape[-1] if acc is not None else 0
@@ -527,6 +541,7 @@ def hils_sink_decode(p: Params, A: int, Q, Kc, Vc, cache_len, O, lse=None, acc=N
     itself if None). workspace: alloc_workspace(p, HILS_CALL_SINK_DECODE, T, A), with acc
     HILS_CALL_SINK_DECODE_ACC."""
     call = "hils_sink_decode"
+    _count(call, "A", A)
     t = _bhtd(call, "Kc", Kc)
     out = acc if acc_out is None else acc_out
     q, kv, w = (p.B, p.H, 1, p.d), (p.B, p.Hk, t, p.d), (p.B, p.Hk, t)
@@ -559,6 +574,7 @@ def hils_cache_evict(p: Params, A: int, budget: int, K, V, acc, cache_len, Kout,
     last), len_out [B] int32 the new lengths (may be cache_len).
     workspace: alloc_workspace(p, HILS_CALL_CACHE_EVICT, T, budget)."""
     call = "hils_cache_evict"
+    _count(call, "A", A)
     t = _bhtd(call, "K", K)
     kv, out = (p.B, p.Hk, t, p.d), (p.B, p.Hk, budget, p.d)
     ck, cv, cko, cvo, ca, cn, cao, ci, clo, run = _sink_call(
