@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import hierarchical_chunk_sparse_b200 as hils
+from oracle import sink as ref
 from sink_testutil import params
 
 pytestmark = pytest.mark.gpu
@@ -40,3 +41,27 @@ def test_the_most_tokens(cuda_device, heavy_from):
     assert len(want) == budget and idx[0, 0].tolist() == want and out.tolist() == [budget]
     assert torch.equal(Ko[0, 0], K[0, 0, :budget]) and torch.equal(Vo[0, 0], K[0, 0, :budget])
     assert torch.equal(ao[0, 0], acc[0, 0, torch.tensor(want, device=cuda_device)])
+
+
+@pytest.mark.parametrize("T,budget,W,A,lens", [(140001, 70000, 64, 4, [140001, 133000]), (200000, 199000, 0, 0, [200000, 199500]),
+                                               (300007, 1000, 512, 16, [300007, 131600])])
+@pytest.mark.parametrize("spread,dtype,d", [(3.0, BF, 128), (1e-4, F32, 64)])
+def test_more_slots_than_the_registers_hold(cuda_device, T, budget, W, A, lens, spread, dtype, d):
+    """Two sequences with more than 131072 slots between the sinks and the window: weights over
+    many exponents or close together, ties of zeros of both signs, infinities and NaN, on both
+    sides of the border between registers and memory."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    acc = torch.exp(spread * torch.randn(2, 1, T, generator=g, device="cuda") - 2.0)
+    u = torch.rand(acc.shape, generator=g, device="cuda")
+    for lo, hi, x in ((0.0, 0.2, 0.0), (0.2, 0.3, -0.0), (0.3, 0.31, float("inf")), (0.31, 0.33, float("nan")), (0.33, 0.36, float("-inf"))):
+        acc[(u >= lo) & (u < hi)] = x
+    K, V = (torch.randn(2, 1, T, d, generator=g, device="cuda").to(dtype) for _ in range(2))
+    n = torch.tensor(lens, dtype=torch.int32, device=cuda_device)
+    Ko, Vo, ao, idx, out = evict(params(2, 1, 1, d, W, dtype), A, budget, K, V, acc, n)
+    rows, new = ref.evict(acc, torch.tensor(lens), budget, W, A)
+    assert out.tolist() == new == [budget, budget]
+    for b in range(2):
+        at = torch.tensor(rows[b][0], dtype=torch.long, device=cuda_device)
+        assert torch.equal(idx[b, 0].long(), at)
+        assert torch.equal(Ko[b, 0], K[b, 0, at]) and torch.equal(Vo[b, 0], V[b, 0, at])
+        assert torch.equal(ao[b, 0].view(torch.int32), acc[b, 0, at].view(torch.int32))
