@@ -50,10 +50,6 @@ struct Pipe {
         atomicOr(status, 1u);
         return false;
     }
-    // a test that does not wait (a warp's lanes agree)
-    __device__ __forceinline__ bool ready(int i, uint32_t parity) const {
-        return __all_sync(kFull, mbar_test_phase(bar(i), parity));
-    }
     // For a loop over several barriers: false once it has made no progress for the limit since
     // *since (0: none yet) or the CTA stops. `spins` counts the idle rounds.
     __device__ __forceinline__ bool idle(int *spins, uint64_t *since) const {
@@ -202,14 +198,14 @@ __device__ __forceinline__ int item_of_round(int r, int c, int n) { return r * n
 template <int KT>
 struct RowItem {
     int b, h, hk, i0;   // batch, first packed head, its key-value head, first query of A
-    int tA, tB, A;      // first positions, sinks
+    int tA, tB;         // first positions
     SinkSpan sp;
     int e0, e1, eA, wB; // entries of this split; A sees entries < eA, B the sinks' and window tiles >= wB
     int split;
     bool hasB;          // B has rows
 
     RowItem() = default;
-    __device__ __forceinline__ RowItem(int j, int hp, int units, int G, int P, int qt, int nqb, int Lq, int N, int W, int A_,
+    __device__ __forceinline__ RowItem(int j, int hp, int units, int G, int P, int qt, int nqb, int Lq, int N, int W, int A,
                                        int splits) {
         split = 0;
         if (splits > 1) {
@@ -223,7 +219,6 @@ struct RowItem {
         h = (u - b * hp) * P;
         hk = h / G;
         i0 = qb * 2 * qt;
-        A = A_;
         tA = N - Lq + i0;
         tB = tA + qt;
         hasB = tB < N;
@@ -254,16 +249,6 @@ struct RowItem {
         int l = e1 - 1;
         if (l >= sp.ns && l - sp.ns < wB) l = min(l, sp.ns - 1);
         return l >= e0 ? l : -1;
-    }
-    // visible columns of entry e for a row at position t, among n: [*lo, *hi) and [0, *as)
-    __device__ __forceinline__ void columns(int e, int n, int t, int W, int *lo, int *hi, int *as) const {
-        const int k0 = first_key(e);
-        *lo = *as = 0;
-        *hi = min(n, t + 1 - k0);
-        if (e >= sp.ns) {
-            *lo = t - W + 1 - k0;
-            *as = min(A - k0, *hi);
-        }
     }
 };
 

@@ -3,10 +3,10 @@
 // queries, so that no sum crosses threads.
 //
 // Items are 256 keys of one (b, key-value head), two 128-key tiles A and B, and a segment of
-// their steps; a step is 128 query rows: of one head, or, where only few queries see a block,
-// of several heads of the group (the rows stay full). S^T = K Q^T (M = 128 keys, N = 128
-// rows, K = d) into TMEM, double-buffered per tile; the keys of the next item and the rows of
-// the next steps are loaded meanwhile. The rows' lse (log2 units) are staged in shared memory.
+// their steps; a step is 128 query rows: of one head, or, in a call of few queries, of several
+// heads of the group (the rows stay full). S^T = K Q^T (M = 128 keys, N = 128 rows, K = d) into
+// TMEM, double-buffered per tile; the keys of the next item and the rows of the next steps are
+// loaded meanwhile. The rows' lse (log2 units) are staged in shared memory.
 // The exponentials bound it (16 a cycle and SM on the MUFU against 8192 products): every
 // fourth one is evaluated on the FMA pipe instead.
 // Warps 0-7, 8-15: the keys of tile A, B (TMEM lane quadrant w % 4), four warps for its even
@@ -28,30 +28,15 @@ using namespace tc;
 // exp2_fma (fast_math.cuh; its polynomial) for two values that are at most 127, in packed float32 arithmetic: 13
 // instructions for the pair. Below -126 the result is some subnormal number, below -127 (-inf too) 2^-149.
 __device__ __forceinline__ float2 exp2_fma2(float2 x) {
-    auto fma = [](float2 a, float2 b, float2 c) {
-        float2 d;
-        asm("fma.rn.f32x2 %0, %1, %2, %3;"
-            : "=l"(reinterpret_cast<unsigned long long &>(d))
-            : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)),
-              "l"(reinterpret_cast<unsigned long long &>(c)));
-        return d;
-    };
-    auto add = [](float2 a, float2 b) {
-        float2 d;
-        asm("add.rn.f32x2 %0, %1, %2;"
-            : "=l"(reinterpret_cast<unsigned long long &>(d))
-            : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
-        return d;
-    };
     auto both = [](float c) { return make_float2(c, c); };
     x = make_float2(fmaxf(x.x, -127.f), fmaxf(x.y, -127.f));
-    const float2 t = add(x, both(12582912.f));
-    const float2 f = fma(add(t, both(-12582912.f)), both(-1.f), x);
-    float2 p = fma(both(1.327647129e-03f), f, both(9.675540961e-03f));
-    p = fma(p, f, both(5.550713092e-02f));
-    p = fma(p, f, both(2.402212024e-01f));
-    p = fma(p, f, both(6.931469440e-01f));
-    p = fma(p, f, both(1.000000119e+00f));
+    const float2 t = add2(x, both(12582912.f));
+    const float2 f = fma2(add2(t, both(-12582912.f)), both(-1.f), x);
+    float2 p = fma2(both(1.327647129e-03f), f, both(9.675540961e-03f));
+    p = fma2(p, f, both(5.550713092e-02f));
+    p = fma2(p, f, both(2.402212024e-01f));
+    p = fma2(p, f, both(6.931469440e-01f));
+    p = fma2(p, f, both(1.000000119e+00f));
     // t holds 0x4b400000 + j: shifted left by 23 its upper bits fall away
     return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
                        __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
@@ -445,10 +430,8 @@ bool launch_sink_weights_tc(hils_dtype dt, int d, const SinkBwdArgs &a, cudaStre
     Args f{};
     f.a = a;
     // few queries: several heads of the group share a step
-    const int64_t see = (int64_t)a.W + kKeys;  // queries that see a block of the window
-    const int rows = a.A == 0 && see < a.Lq ? (int)see : a.Lq;
     f.P = 1;
-    while (f.P < 8 && a.G % (2 * f.P) == 0 && rows * 2 * f.P <= kRows) f.P *= 2;
+    while (f.P < 8 && a.G % (2 * f.P) == 0 && (int64_t)a.Lq * 2 * f.P <= kRows) f.P *= 2;
     f.qn = kRows / f.P;
     f.Hk = Hk;
     f.heads = a.B * Hk;
