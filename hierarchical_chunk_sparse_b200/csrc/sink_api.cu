@@ -67,7 +67,7 @@ size_t key_ws(const hils_params *p, int Lq, int N, int A, int per_key, SinkBwdAr
     a->H = p->H;
     a->G = groups(p);
     sink_key_plan(p->dtype, p->B, p->H / a->G, a->G, Lq, N, clip(p->W, N), clip(A, N),
-                  per_key == 1 && p->dtype == HILS_BF16 ? 2 * kSinkKeys : kSinkKeys, a);
+                  per_key == 1 && p->dtype == HILS_BF16 ? 2 * kSinkKeys : kSinkKeys, device_sm_count(), a);
     return sink_align(sink_key_part_floats(*a, per_key) * 4);
 }
 

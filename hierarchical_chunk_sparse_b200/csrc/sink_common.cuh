@@ -174,9 +174,9 @@ __host__ __device__ inline void sink_rows_of_block(const SinkBwdArgs &a, int j0,
     if (*i1 < *i0) *i1 = *i0;
 }
 
-// The division of the key blocks: enough items for every SM, at least eight steps each
+// The division of the key blocks: four items for every SM, at least eight steps each
 // (float32: one 64-row tile, which costs more than its share of the reduction).
-inline void sink_key_plan(hils_dtype dt, int B, int Hk, int G, int Lq, int N, int W, int A, int keys, SinkBwdArgs *a) {
+inline void sink_key_plan(hils_dtype dt, int B, int Hk, int G, int Lq, int N, int W, int A, int keys, int sms, SinkBwdArgs *a) {
     const int step = dt == HILS_F32 ? 64 : kSinkRows, least = dt == HILS_F32 ? 1 : 8;
     a->keys = keys;
     a->nblk = (N + keys - 1) / keys;
@@ -184,7 +184,7 @@ inline void sink_key_plan(hils_dtype dt, int B, int Hk, int G, int Lq, int N, in
     if (a->nsink > a->nblk) a->nsink = a->nblk;
     auto segments = [&](int blocks, int64_t rows) {
         const int64_t steps = (int64_t)G * ((rows + step - 1) / step);
-        const int64_t items = (int64_t)B * Hk * blocks, fill = items > 0 ? 592 / items : 1;
+        const int64_t items = (int64_t)B * Hk * blocks, fill = items > 0 ? 4 * sms / items : 1;
         int64_t s = steps / least < fill ? steps / least : fill;
         return (int)(s < 1 ? 1 : s);
     };

@@ -641,7 +641,8 @@ __global__ void __launch_bounds__(256) sink_acc_kernel(SinkDecodeArgs a, const f
 
 }  // namespace
 
-// CTAs of a decode: two per SM, no more than there are tiles.
+// CTAs of a decode: two per SM, no more than there are tiles. (Both fit an SM's shared memory but in
+// float32 with d = 128 and groups of seven or eight, where one does: its 116 KB; the others follow.)
 int sink_decode_ctas(hils_dtype dt, int B, int Hk, int64_t keys, int sms) {
     const int kt = dt == HILS_BF16 ? tile_keys<bf16>() : tile_keys<float>();
     const int64_t tiles = (int64_t)B * Hk * (keys > kt ? (keys + kt - 1) / kt : 1);
