@@ -1,7 +1,9 @@
 // One query per sequence over the visible slots of its cache (formulas in sink_common.cuh).
 // Bound by HBM: 8 x 128K tokens of 8 key-value heads (32 heads, d = 128, bf16), 3.65 GB with the
 // weights added to acc, take 632 us, 5.8 TB/s (the walk 571, the join 9, acc 38; 7840 in float32 on
-// the CUDA cores). A window of 512 in one sequence takes 12 us, nearly all of it the launch.
+// the CUDA cores). A window of 512 in one sequence takes 13 us, nearly all of it the launch.
+// float32, 8 x 16K tokens of 8 key-value heads (32 heads, d = 128), 1.07 GB: 370 us, 2.9 TB/s, bound by
+// the products' shuffles and shared-memory reads; 1131 with 64 heads.
 #include "sink_common.cuh"
 
 namespace hils {

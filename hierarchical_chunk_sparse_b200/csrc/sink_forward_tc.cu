@@ -30,7 +30,7 @@
 // 41 by its bytes, 40 by its products): the tensor pipe is 35 % busy and the MUFU 39 %, a key tile
 // costs its warpgroup some 3570 cycles of which the softmax's dependent steps (TMEM load, maximum,
 // exponentials, TMEM store) are three quarters, and the last wave about a tenth of the time. The
-// prefix pass of 32 sequences over 64K tokens (8 key-value heads) takes 64 us, 4.2 TB/s.
+// prefix pass of 32 sequences over 64K tokens (8 key-value heads) takes 56 us, 4.8 TB/s.
 // 64-key tiles with two warpgroups each took 131 us where 128-key tiles with one took 222.
 // P is rounded to bf16 for its product (at most 2^-8 of each, averaged by the sum), as O is.
 // TMEM of tile x, from 128 x: S [0,64), P [64,96), [96,128); O_A [256,384), O_B [384,512).

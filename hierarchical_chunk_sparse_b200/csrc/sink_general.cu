@@ -5,7 +5,9 @@
 // cycles of an SM at d = 128; small calls are bound by the latency of one tile (7 us
 // at d = 64) and the launches, which is why their rows and keys are split to a tile a CTA: 2 x 6
 // heads of 333 queries, W 200, d = 64 take 28 us with the binding, the backward of 2 x 4 heads of
-// 509 tokens 53.
+// 509 tokens 49. Where products bind, 8 heads of 2048 causal tokens at d = 64 and 128: forward 338
+// and 452 us (58 and 115 by their FMAs), backward 542 and 996 (144 and 289), weights 110 and 187 (29
+// and 58); the FMA pipe is 47 to 51 % busy at d = 128, and its warps wait on shared-memory reads.
 #include "sink_common.cuh"
 
 namespace hils {
@@ -442,7 +444,7 @@ __device__ __forceinline__ void sink_bwd_rows(const SinkBwdArgs &a, int tiles, i
 }
 
 // dQ's CTAs [0, nq), then those of dK and dV: side by side, each reads D once its grid is complete
-// (in two kernels, dK and dV behind dQ, 2 x 4 heads of 509 tokens took 68 us, so 53). kPerSm CTAs an
+// (in two kernels, dK and dV behind dQ, 2 x 4 heads of 509 tokens took 68 us, so 49). kPerSm CTAs an
 // SM at d = 64; at d = 128 one fits.
 template <typename T, int D, int kPerSm>
 __global__ void __launch_bounds__(kThr, kPerSm) sink_bwd_kernel(SinkBwdArgs a, int qtiles, int nq, int items) {

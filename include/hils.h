@@ -363,6 +363,10 @@ int hils_summarize_backward(const hils_params *p, hils_ctensor K, int N, hils_ct
  * score gradients are rounded to bf16 as operands of their matrix products (for dQ the score
  * gradients are two bf16 parts, as a row of them sums to zero).
  * The first 32-bit word of each workspace is a status word, as in hils_attend_prefill.
+ * bf16 prefill, backward, weights and prefix run on the tensor cores if every stride over more
+ * than one element is positive and below 2^38 elements and, for prefill and prefix, scale > 0.
+ * Else, a batch that shares its keys by a stride of zero among them, they run on the CUDA cores,
+ * to the same bounds but some 20 times slower. The decode calls take any strides alike.
  * Outputs overlap neither inputs nor one another, but where it is said; a view that is
  * written has no stride of zero (HILS_ERR_INVALID_ARG).
  * A call takes up to 2^31 - 1025 tokens (hils_prefix_decode: P + T), more are
