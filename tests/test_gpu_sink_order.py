@@ -1,4 +1,5 @@
-"""The float32 backward reads D = dO . o only when the kernel that computes it is complete."""
+"""What a call leaves in its workspace is written before it is read, whatever was there: the
+float32 backward's D = dO . o, and every part of every call."""
 import math
 
 import pytest
@@ -7,6 +8,7 @@ import torch
 import hierarchical_chunk_sparse_b200 as hils
 from oracle import sink as ref
 from sink_testutil import grad_bounds, make, params, prefill, status_of, within
+from test_gpu_sink_use import Calls
 
 pytestmark = pytest.mark.gpu
 F32 = torch.float32
@@ -44,3 +46,23 @@ def test_backward_over_a_used_workspace(cuda_device, B, H, Hk, d, N, W, A):
         val, mag, es = ref.backward(Q, K, V, O, lse, dO, see, scale)
         for name, x, v, t in zip(("dQ", "dK", "dV"), got, val, grad_bounds(val, mag, es, L, lm, d, N * H // Hk, F32)):
             within(x, v, t, name)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, F32])
+@pytest.mark.parametrize("sizes", [dict(), dict(B=2, H=8, Hk=1, d=128, P=3000), dict(B=1, H=6, Hk=2, N=1500, W=600, A=0, budget=700),
+                                   dict(B=2, H=14, Hk=2, d=128, N=2100, W=64, A=70, P=5000, budget=1999)])
+def test_every_part_of_a_workspace_is_written_before_it_is_read(cuda_device, dtype, sizes):
+    """All six calls over workspaces of zeros and over workspaces of NaN: the same bits."""
+    c = Calls(cuda_device, dtype, 7, **sizes)
+    c.clear()
+    c.run()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in c.outputs()]
+    for _ in range(2):
+        for w in c.ws:
+            w[256:].fill_(255)  # NaN as float32; the status word's block stays
+        c.clear()
+        c.run()
+        torch.cuda.synchronize()
+        assert [i for i, (x, y) in enumerate(zip(c.outputs(), want)) if not torch.equal(x, y)] == []
+        assert all(status_of(w) == 0 for w in c.ws)
